@@ -6,8 +6,9 @@ PyTorch supplies device memory and streams. There is no CPU fallback: every call
 if ``libattnfuse.so`` is missing or fails to load.
 
 Low-level functions carry the C names (``attnfuse_fwd`` ...) and take raw pointers; the
-torch-level helpers ``fwd``, ``bwd``, ``decode`` and ``rope_prerotate`` allocate outputs and
-workspace with torch and call them on the current CUDA stream.
+torch-level helpers ``fwd``, ``bwd``, ``decode``, ``rope_prerotate`` and, on a ``PagedCache``,
+``paged_append``, ``paged_gather`` and ``paged_decode`` allocate outputs and workspace with torch
+and call them on the current CUDA stream.
 """
 from __future__ import annotations
 
@@ -20,6 +21,8 @@ __all__ = [
     "MASK_BLOCK_SPARSE", "BIAS_NONE", "BIAS_ALIBI", "BIAS_ADDITIVE", "AttnfuseError", "Variant",
     "load", "library_path", "fwd", "bwd", "decode", "rope_prerotate", "device_status",
     "fwd_workspace_size", "bwd_workspace_size", "decode_workspace_size",
+    "CACHE_BF16", "CACHE_Q4", "PagedCache", "paged_append", "paged_gather", "paged_decode",
+    "paged_decode_workspace_size",
 ]
 
 ROPE_NONE, ROPE_FUSED, ROPE_PREROTATE, ROPE_AUTO = 0, 1, 2, 3
@@ -27,8 +30,9 @@ ROPE_REUSE_TABLE = 0x100
 MASK_FULL, MASK_CAUSAL, MASK_WINDOW, MASK_BLOCK_SPARSE = 0, 1, 2, 3
 BIAS_NONE, BIAS_ALIBI, BIAS_ADDITIVE = 0, 1, 2
 NORM_SOFTMAX, NORM_RELU = 0, 1
+CACHE_BF16, CACHE_Q4 = 0, 1
 _STATUS = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "WORKSPACE_TOO_SMALL",
-           4: "CUDA_ERROR", 5: "TIMEOUT", 6: "FP16_RANGE"}
+           4: "CUDA_ERROR", 5: "TIMEOUT", 6: "FP16_RANGE", 7: "PAGE_RANGE"}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_lib", "libattnfuse.so")
@@ -65,6 +69,29 @@ class CVariant(ctypes.Structure):
     ]
 
 
+class CPagedCache(ctypes.Structure):
+    """Mirror of the C struct attnfuse_paged_cache."""
+    _fields_ = [
+        ("format", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("Hkv", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("B", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_strides", ctypes.c_int64 * 4),
+        ("v_strides", ctypes.c_int64 * 4),
+        ("k_scales", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
+        ("k_scale_strides", ctypes.c_int64 * 4),
+        ("v_scale_strides", ctypes.c_int64 * 4),
+        ("page_table", ctypes.c_void_p),
+        ("page_table_stride", ctypes.c_int64),
+    ]
+
+
 def library_path() -> str:
     return _LIB_PATH
 
@@ -82,6 +109,7 @@ def load():
         P, I, F, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
         ST = ctypes.POINTER(ctypes.c_int64)
         VP = ctypes.POINTER(CVariant)
+        CP = ctypes.POINTER(CPagedCache)
         sig = {
             "attnfuse_last_error": ([], ctypes.c_char_p),
             "attnfuse_version": ([], I),
@@ -97,6 +125,10 @@ def load():
             "attnfuse_decode_auto_splits": ([I, I, I, ctypes.POINTER(I)], I),
             "attnfuse_decode_noalloc": ([P, ST, P, ST, P, ST, P, ST, P, I, I, I, I, I, I, F, F, I,
                                          I, P], I),
+            "attnfuse_paged_append": ([CP, P, ST, P, ST, P, P, I, F, I, P], I),
+            "attnfuse_paged_gather": ([CP, P, P, P, ST, P, ST, I, P], I),
+            "attnfuse_paged_decode_workspace_size": ([I, I, I, I, ctypes.POINTER(S)], I),
+            "attnfuse_paged_decode": ([CP, P, ST, P, P, ST, P, I, F, F, I, I, P, P, S, P], I),
             "attnfuse_rope_prerotate": ([P, ST, P, I, I, I, I, F, P, S, P], I),
             "attnfuse_debug_wait_timeout": ([ctypes.c_uint64, P], I),
             "attnfuse_rope_table": ([P, S, I, I, F, P], I),
@@ -560,10 +592,190 @@ def rope_prerotate(x, rope_theta, out=None, workspace=None, stream=None):
     return out
 
 
+def _live_strides(t, n):
+    """Element strides with those of one-element dimensions, which address nothing and may hold
+    any value, replaced by what a contiguous tensor would have."""
+    st = list(t.stride())
+    inner = 1
+    for i in range(n - 1, -1, -1):
+        if t.size(i) == 1:
+            st[i] = inner
+        inner = max(inner, st[i] * t.size(i))
+    return (ctypes.c_int64 * n)(*st)
+
+
+class PagedCache:
+    """A key/value cache in pages (attnfuse_paged_cache): pools, and a table of pages per sequence.
+
+    k, v: bf16 [num_pages, Hkv, page_size, d], or for the 4-bit format uint8 [num_pages, Hkv,
+    page_size, d/2] with k_scales, v_scales bf16 [num_pages, Hkv, page_size, d/32]. page_table:
+    int32 [B, max_pages]; position p of sequence b is slot p % page_size of page
+    page_table[b, p // page_size]. The object holds references only: the caller allocates pages,
+    fills the table and keeps the lengths. page_size: a multiple of 16.
+    """
+
+    def __init__(self, k, v, page_table, k_scales=None, v_scales=None):
+        import torch
+
+        bf16 = (torch.bfloat16,)
+        self.q4 = isinstance(k, torch.Tensor) and k.dtype == torch.uint8
+        dims = "[num_pages, Hkv, page_size, d/2]" if self.q4 else "[num_pages, Hkv, page_size, d]"
+        types = (torch.uint8,) if self.q4 else (torch.bfloat16, torch.uint8)
+        _need(k, "cache k", types, ndim=4, dims=dims)
+        self.num_pages, self.Hkv, self.page_size, row = k.shape
+        self.d = 2 * row if self.q4 else row
+        self.device = k.device
+        _need(v, "cache v", (k.dtype,), tuple(k.shape), self.device)
+        if self.q4:
+            steps = (self.num_pages, self.Hkv, self.page_size, self.d // 32)
+            _need(k_scales, "cache k_scales", bf16, steps, self.device)
+            _need(v_scales, "cache v_scales", bf16, steps, self.device)
+        elif k_scales is not None or v_scales is not None:
+            raise ValueError("k_scales, v_scales belong to the 4-bit format (uint8 pools)")
+        _need(page_table, "page_table", (torch.int32,), ndim=2, dims="[B, max_pages]", device=self.device)
+        if page_table.size(1) > 1 and page_table.stride(1) != 1:
+            raise ValueError("page_table: rows must be contiguous")
+        self.B, self.max_pages = page_table.shape
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.page_table = page_table
+        self.format = CACHE_Q4 if self.q4 else CACHE_BF16
+
+    @classmethod
+    def empty(cls, num_pages, Hkv, page_size, d, page_table, q4=False):
+        """A cache with newly allocated (uninitialised) pools on page_table's device."""
+        import torch
+
+        dev = page_table.device
+        new = lambda row, dt: torch.empty((num_pages, Hkv, page_size, row), dtype=dt, device=dev)  # noqa: E731
+        if not q4:
+            return cls(new(d, torch.bfloat16), new(d, torch.bfloat16), page_table)
+        return cls(new(d // 2, torch.uint8), new(d // 2, torch.uint8), page_table,
+                   new(d // 32, torch.bfloat16), new(d // 32, torch.bfloat16))
+
+    def c_struct(self):
+        c = CPagedCache()
+        c.format, c.num_pages, c.Hkv, c.page_size = self.format, self.num_pages, self.Hkv, self.page_size
+        c.d, c.B, c.max_pages = self.d, self.B, self.max_pages
+        c.k, c.v = self.k.data_ptr(), self.v.data_ptr()
+        c.k_strides, c.v_strides = _live_strides(self.k, 4), _live_strides(self.v, 4)
+        if self.q4:
+            c.k_scales, c.v_scales = self.k_scales.data_ptr(), self.v_scales.data_ptr()
+            c.k_scale_strides = _live_strides(self.k_scales, 4)
+            c.v_scale_strides = _live_strides(self.v_scales, 4)
+        c.page_table, c.page_table_stride = self.page_table.data_ptr(), self.page_table.stride(0)
+        return c
+
+
+def _need_cache(cache):
+    if not isinstance(cache, PagedCache):
+        raise TypeError(f"cache: expected a PagedCache, got {type(cache).__name__}")
+
+
+def _need_index(t, name, B, device):
+    import torch
+
+    if t is not None:
+        _need(t, name, (torch.int32,), (B,), device, contiguous=True)
+
+
+def paged_append(cache, k, v, start, count=None, rope_theta=10000.0, rope_mode=ROPE_FUSED, stream=None):
+    """Write rows into the cache: k, v [B, Hkv, N, d] bf16; row n < count[b] of sequence b becomes
+    position start[b] + n (start, count: int32 [B] device tensors; count None: all N). K is
+    rotated at its position on the way (rope_mode ROPE_FUSED) or taken as it is (ROPE_NONE)."""
+    import torch
+
+    _need_cache(cache)
+    bf16, dev = (torch.bfloat16,), cache.device
+    _need(k, "k", bf16, ndim=4, dims="[B, Hkv, N, d]")
+    N = k.shape[2]
+    _need(k, "k", bf16, (cache.B, cache.Hkv, N, cache.d), dev)
+    _need(v, "v", bf16, (cache.B, cache.Hkv, N, cache.d), dev)
+    if start is None:
+        raise TypeError("start: expected an int32 [B] tensor")
+    _need_index(start, "start", cache.B, dev)
+    _need_index(count, "count", cache.B, dev)
+    cc = cache.c_struct()
+    ctx, st = _launch_context(dev, stream)
+    with ctx:
+        _check(load().attnfuse_paged_append(
+            ctypes.byref(cc), _ptr(k), _live_strides(k, 4), _ptr(v), _live_strides(v, 4), _ptr(start),
+            _ptr(count), N, float(rope_theta), rope_mode, st))
+
+
+def paged_gather(cache, start, count, N, k=None, v=None, stream=None):
+    """Read rows back: positions start[b] .. start[b] + count[b] - 1 (start None: from 0; count None:
+    N rows) into rows 0 .. of k, v [B, Hkv, N, d] bf16, zeros behind. Returns (k, v)."""
+    import torch
+
+    _need_cache(cache)
+    bf16, dev = (torch.bfloat16,), cache.device
+    shape = (cache.B, cache.Hkv, int(N), cache.d)
+    k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
+    v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
+    _need(k, "k", bf16, shape, dev)
+    _need(v, "v", bf16, shape, dev)
+    _need_index(start, "start", cache.B, dev)
+    _need_index(count, "count", cache.B, dev)
+    cc = cache.c_struct()
+    ctx, st = _launch_context(dev, stream)
+    with ctx:
+        _check(load().attnfuse_paged_gather(
+            ctypes.byref(cc), _ptr(start), _ptr(count), _ptr(k), _live_strides(k, 4), _ptr(v),
+            _live_strides(v, 4), int(N), st))
+    return k, v
+
+
+def paged_decode_workspace_size(Hq, Hkv, d, cache_format):
+    """Bytes of workspace for paged_decode on the current device (independent of the lengths)."""
+    n = ctypes.c_size_t()
+    _check(load().attnfuse_paged_decode_workspace_size(Hq, Hkv, d, cache_format, ctypes.byref(n)))
+    return n.value
+
+
+def paged_decode(q, cache, lens, scale=None, rope_theta=10000.0, rope_mode=ROPE_FUSED, window=0,
+                 alibi_slopes=None, out=None, lse=None, with_lse=True, workspace=None, stream=None):
+    """Decode over a paged cache: q [B, Hq, d] bf16 at position lens[b] - 1 against positions
+    n < lens[b] (window > 0: the last `window` of them) -> (out [B, Hq, d], lse [B, Hq]).
+    lens: int32 [B] device tensor (0: out 0, lse -inf); alibi_slopes: fp32 [Hq], adds
+    slope_h (n - (lens[b] - 1)) to the scores."""
+    import torch
+
+    _need_cache(cache)
+    bf16, f32, dev = (torch.bfloat16,), (torch.float32,), cache.device
+    _need(q, "q", bf16, ndim=3, dims="[B, Hq, d]")
+    Hq = q.shape[1]
+    _need(q, "q", bf16, (cache.B, Hq, cache.d), dev)
+    if lens is None:
+        raise TypeError("lens: expected an int32 [B] tensor")
+    _need_index(lens, "lens", cache.B, dev)
+    if alibi_slopes is not None:
+        _need(alibi_slopes, "alibi_slopes", f32, (Hq,), dev, contiguous=True)
+    if scale is None:
+        scale = cache.d ** -0.5
+    if out is None:
+        out = torch.empty((cache.B, Hq, cache.d), dtype=torch.bfloat16, device=dev)
+    _need(out, "out", bf16, (cache.B, Hq, cache.d), dev)
+    if with_lse and lse is None:
+        lse = torch.empty((cache.B, Hq), dtype=torch.float32, device=dev)
+    if lse is not None:
+        _need(lse, "lse", f32, (cache.B, Hq), dev, contiguous=True)
+    cc = cache.c_struct()
+    ctx, st = _launch_context(dev, stream)
+    with ctx:
+        ws_n = paged_decode_workspace_size(Hq, cache.Hkv, cache.d, cache.format)
+        ws = _workspace(ws_n, dev, workspace)
+        _check(load().attnfuse_paged_decode(
+            ctypes.byref(cc), _ptr(q), _live_strides(q, 3), _ptr(lens), _ptr(out), _live_strides(out, 3),
+            _ptr(lse), Hq, float(scale), float(rope_theta), rope_mode, int(window), _ptr(alibi_slopes),
+            _ptr(ws), ws_n, st))
+    return out, lse
+
+
 def device_status(clear=True, stream=None, device=None):
     """Synchronise and return the device status of `device` (default: the stream's device,
     else the current device): 0 OK, 5 TIMEOUT (a kernel gave up waiting), 6 FP16_RANGE (a
-    rotating-mode forward saturated an fp16 Q' / K' element or met a non-finite input)."""
+    rotating-mode forward saturated an fp16 Q' / K' element or met a non-finite input), 7 PAGE_RANGE
+    (a paged-cache call skipped rows on a page, or with a start, length or count, out of range)."""
     import torch
 
     if device is None:

@@ -248,6 +248,15 @@ int set_last_error(int code, const char* msg) {
   return fail(code, "%s", msg);
 }
 
+int current_status_word(int** status) { return device_state(status); }
+
+int encode_map_bhnd(CUtensorMap* m, const void* ptr, const int64_t st[4], int B, int H, int N, int d,
+                    const char* name, int box_rows) {
+  return encode_bhnd(m, ptr, st, B, H, N, d, name, box_rows);
+}
+
+RopeFreqs rope_freqs(int d, float theta) { return make_freqs(d, theta); }
+
 }  // namespace afx
 
 using namespace afx;
@@ -273,7 +282,9 @@ attnfuse_status attnfuse_device_status(cudaStream_t stream, int clear, int* code
     e = cudaMemcpy(st, &zero, sizeof(int), cudaMemcpyHostToDevice);
     if (e != cudaSuccess) return cuda_fail(e, "clear status word");
   }
-  *code = (v & kDevTimeout) ? ATTNFUSE_ERR_TIMEOUT : (v & kDevF16Range) ? ATTNFUSE_ERR_FP16_RANGE : ATTNFUSE_OK;
+  *code = (v & kDevTimeout) ? ATTNFUSE_ERR_TIMEOUT
+          : (v & kDevPageRange) ? ATTNFUSE_ERR_PAGE_RANGE
+          : (v & kDevF16Range) ? ATTNFUSE_ERR_FP16_RANGE : ATTNFUSE_OK;
   return ok();
 }
 

@@ -18,6 +18,7 @@ enum : int {
   kDevOk = 0,
   kDevTimeout = 1,    // a kernel gave up waiting
   kDevF16Range = 2,   // a rotated Q' / K' value reached the fp16 limit (saturated) or is not finite
+  kDevPageRange = 4,  // a paged-cache call met a page, a length or a row count out of range
 };
 
 // Wall-clock limit for any single wait, in nanoseconds (globaltimer). Generous: a legitimate

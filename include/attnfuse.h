@@ -53,6 +53,7 @@ typedef int attnfuse_status;
 #define ATTNFUSE_ERR_CUDA 4
 #define ATTNFUSE_ERR_TIMEOUT 5
 #define ATTNFUSE_ERR_FP16_RANGE 6 /* device status: a rotated Q' / K' value saturated fp16 */
+#define ATTNFUSE_ERR_PAGE_RANGE 7 /* device status: a paged call met a page, length or count out of range */
 
 /* Where RoPE is applied (paper §4.1 "Fused RoPE" vs. the pre-rotation of Fig. 1a / §5.3).
  * In both rotating modes the rotation runs in fp32 and the rotated Q', K' are rounded to fp16
@@ -152,6 +153,8 @@ int attnfuse_version(void);
 
 /* Synchronise `stream`, then read (and if `clear`, reset) the device status word of the
  * current device: ATTNFUSE_OK; ATTNFUSE_ERR_TIMEOUT if a kernel gave up waiting; else
+ * ATTNFUSE_ERR_PAGE_RANGE if a call on a paged cache met a page number, a start, a length or a
+ * row count out of range (it skipped those rows); else
  * ATTNFUSE_ERR_FP16_RANGE if a forward in a rotating mode (FUSED or PREROTATE) produced a
  * rotated Q' or K' element of magnitude >= 65504 or not finite: the fp16 operand saturated
  * (or the input was not finite) and that call's scores are not to be trusted. */
@@ -309,6 +312,92 @@ attnfuse_status attnfuse_decode_noalloc(const void* q, const int64_t q_strides[3
 
 /* Number of KV chunks attnfuse_decode uses for num_splits = 0 on the current device. */
 attnfuse_status attnfuse_decode_auto_splits(int B, int Hkv, int L, int* num_splits);
+
+/* ------------------------------------------------------------------------------------------
+ * Paged key/value caches. (The paper has no counterpart: its decode reads one dense cache of one
+ * length. A server holds sequences of many lengths that grow one token at a time.)
+ * A cache is a pool of pages [num_pages, Hkv, page_size, row] for K, one for V, and a table of
+ * page numbers per sequence: position p of sequence b is slot p % page_size of page
+ * page_table[b][p / page_size]. Sequences may share pages that nothing is appended to; the rows
+ * that one append writes have to be distinct slots. Table entries behind a sequence's rows are
+ * not read. Formats:
+ *   BF16  a row is d bf16 values. Pool strides (page, head, slot, c) in elements, as elsewhere:
+ *         innermost 1, the others positive multiples of 8, pools 16-byte aligned.
+ *   Q4    a row is d/2 bytes of codes in k / v (uint8 pools) and d/32 bf16 steps in k_scales /
+ *         v_scales. For the bf16 row x that a BF16 cache would hold and each group of 32
+ *         elements: step s = bf16(max|x| / 7), code = round_half_away(x / s) within [-7, 7],
+ *         value = s * code; max|x| < 2^-96 gives s = 0 (zeros), an infinity or a NaN in the
+ *         group s = NaN. code + 8 is stored in a nibble. The row is 8 chunks of d/16 bytes; chunk
+ *         r holds for each group g, in order, the 16-bit word of elements 32g + 4r .. 32g + 4r + 3,
+ *         lowest nibble first; with d = 128, slots with bit 1 set hold chunk r at place r ^ 4.
+ *         Slots of a (page, head) are contiguous (slot strides d/2 bytes and d/32 steps); page
+ *         and head strides are positive multiples of 16 bytes.
+ * page_size: a multiple of 16, at most 65536. max_pages * page_size <= 2^24 positions.
+ * Values read from the device (page_table, start, count, lens) are checked by the kernels: a
+ * row on a page outside [0, num_pages), a start or length outside the table, or a count outside
+ * [0, N] is skipped (lengths and counts are clamped), never accessed, and sets
+ * ATTNFUSE_ERR_PAGE_RANGE in the device status word. Nothing on the host depends on them, so a
+ * captured call follows them at every replay.
+ * ------------------------------------------------------------------------------------------ */
+typedef enum { ATTNFUSE_CACHE_BF16 = 0, ATTNFUSE_CACHE_Q4 = 1 } attnfuse_cache_format;
+
+typedef struct {
+  int32_t format;              /* attnfuse_cache_format */
+  int32_t num_pages;
+  int32_t Hkv;
+  int32_t page_size;
+  int32_t d;                   /* 64 or 128 */
+  int32_t B;                   /* sequences: rows of page_table */
+  int32_t max_pages;           /* columns of page_table */
+  void* k;                     /* device pools */
+  void* v;
+  int64_t k_strides[4];        /* (page, head, slot, c) */
+  int64_t v_strides[4];
+  void* k_scales;              /* Q4 only */
+  void* v_scales;
+  int64_t k_scale_strides[4];  /* (page, head, slot, group) in steps */
+  int64_t v_scale_strides[4];
+  const int32_t* page_table;   /* [B, max_pages], row stride page_table_stride */
+  int64_t page_table_stride;
+} attnfuse_paged_cache;
+
+/* Append rows: k, v [B, Hkv, N, d] bf16 (strides as in attnfuse_fwd). Row n < count[b] of
+ * sequence b becomes position start[b] + n; rows at and behind count[b] (padding) are not read.
+ * count NULL: all N. rope_mode NONE or FUSED (AUTO means FUSED): K is rotated at its position,
+ * K' = bf16(fp32(R_p k)) of the exact rotation (correctly rounded, whatever the position), so a
+ * slot's bits do not depend on the batch it was written in. N = 1 is the decode step's form. */
+attnfuse_status attnfuse_paged_append(const attnfuse_paged_cache* cache, const void* k,
+                                      const int64_t k_strides[4], const void* v,
+                                      const int64_t v_strides[4], const int32_t* start,
+                                      const int32_t* count, int N, float rope_theta,
+                                      attnfuse_rope_mode rope_mode, cudaStream_t stream);
+
+/* Gather: positions start[b] .. start[b] + count[b] - 1 of sequence b into rows 0 .. count[b] - 1
+ * of k, v [B, Hkv, N, d] bf16 (Q4: the values, rounded to bf16); rows behind are zeros. start
+ * NULL: 0; count NULL: N. */
+attnfuse_status attnfuse_paged_gather(const attnfuse_paged_cache* cache, const int32_t* start,
+                                      const int32_t* count, void* k, const int64_t k_strides[4],
+                                      void* v, const int64_t v_strides[4], int N,
+                                      cudaStream_t stream);
+
+/* Decode: one query per sequence, q [B, Hq, d] at position lens[b] - 1 (append the token's K and
+ * V first), against positions n < lens[b], with window > 0 only n >= lens[b] - window. scores
+ * s_n = scale <R q, k_n> [+ alibi_slopes[h] (n - (lens[b] - 1))]; alibi_slopes [Hq] fp32 or NULL.
+ * out [B, Hq, d] bf16 (strides as in attnfuse_decode), lse [B, Hq] fp32 or NULL. lens[b] = 0:
+ * out 0, lse -inf. rope_mode NONE or FUSED (AUTO means FUSED): q is rotated in fp32 and keeps
+ * 16 or more significant bits. Hq any multiple of Hkv. Sequences of any mix of lengths share the
+ * GPU evenly: the work is cut into equal runs of 64-key tiles over the whole batch. Results do
+ * not vary from run to run. workspace: attnfuse_paged_decode_workspace_size bytes, 16-byte
+ * aligned; it depends on the device, d and Hq / Hkv only, not on lengths. Calls that may
+ * overlap need workspaces of their own. */
+attnfuse_status attnfuse_paged_decode_workspace_size(int Hq, int Hkv, int d, int format, size_t* bytes);
+
+attnfuse_status attnfuse_paged_decode(const attnfuse_paged_cache* cache, const void* q,
+                                      const int64_t q_strides[3], const int32_t* lens, void* out,
+                                      const int64_t o_strides[3], float* lse, int Hq, float scale,
+                                      float rope_theta, attnfuse_rope_mode rope_mode, int window,
+                                      const float* alibi_slopes, void* workspace,
+                                      size_t workspace_bytes, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------------------------
  * Pre-rotation alone (paper Fig. 1a / §5.3 T_pre): x_rot = R_n x for x of shape [B, H, N, d]
