@@ -76,12 +76,22 @@ struct PagedDecodeParams {
   const float* slopes;              // [Hq] or null
   int rope;
   float scale_log2;
+  CUtensorMap tmK, tmV;             // bf16: pools [num_pages, Hkv, page_size, d], box (64, frag_rows)
+  int frag_rows;                    // rows of a page that one copy takes
+  void* workspace;
+  // set by the launcher
+  float* part_acc;                  // [ctas][2][head_rows][d]: partial rows of a run's ends
+  float2* part_ml;                  // (max in log2 units, sum)
+  int ctas, head_rows;              // query heads per item
+  int chunks, items;                // items per KV head, and per sequence
   RopeFreqs freqs;
   int* status;
 };
+constexpr int kPagedMaxCtas = 1024;
 cudaError_t launch_paged_append(PagedAppendParams p, int d, int format, bool rope, cudaStream_t stream);
 cudaError_t launch_paged_gather(PagedGatherParams p, int d, int format, cudaStream_t stream);
-size_t paged_decode_workspace(int d, int g);
+size_t paged_decode_workspace(int d, int g, int format);
+int paged_frag_rows(int page_size);
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, int d, int format, cudaStream_t stream);
 
 // pos / page_size for 0 <= pos < 2^24: pos * (M d - 2^40) < 2^24 * 2^16 keeps the error of

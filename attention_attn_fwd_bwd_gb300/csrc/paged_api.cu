@@ -195,7 +195,7 @@ attnfuse_status attnfuse_paged_decode_workspace_size(int Hq, int Hkv, int d, int
   if (d != 64 && d != 128) return fail(ATTNFUSE_ERR_UNSUPPORTED, "head dim %d (need 64 or 128)", d);
   if (format != ATTNFUSE_CACHE_BF16 && format != ATTNFUSE_CACHE_Q4)
     return fail(ATTNFUSE_ERR_INVALID_ARG, "cache format %d", format);
-  *bytes = paged_decode_workspace(d, Hq / Hkv);
+  *bytes = paged_decode_workspace(d, Hq / Hkv, format);
   return set_last_error(ATTNFUSE_OK, "");
 }
 
@@ -223,7 +223,9 @@ attnfuse_status attnfuse_paged_decode(const attnfuse_paged_cache* cache, const v
   if ((rc = check_rope(&mode, rope_theta))) return rc;
   if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
     return fail(ATTNFUSE_ERR_WORKSPACE_TOO_SMALL, "workspace needs %zu bytes (got %zu)", need, workspace_bytes);
-  if ((int64_t)cache->B * Hq > 0x7fffffff) return fail(ATTNFUSE_ERR_UNSUPPORTED, "B * Hq too large");
+  if ((int64_t)cache->B * Hq > 0x7fffffff || Hq > 4096 ||
+      (int64_t)cache->B * Hq * (p.cache.cap / 64 + 1) > ((int64_t)1 << 36))
+    return fail(ATTNFUSE_ERR_UNSUPPORTED, "B * Hq * max_pages * page_size too large (Hq at most 4096)");
   if ((rc = current_status_word(&p.status))) return rc;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.q_sb = q_strides[0], p.q_sh = q_strides[1];
@@ -238,6 +240,16 @@ attnfuse_status attnfuse_paged_decode(const attnfuse_paged_cache* cache, const v
   p.rope = mode == ATTNFUSE_ROPE_FUSED;
   p.scale_log2 = scale * kLog2e;
   if (p.rope) p.freqs = rope_freqs(cache->d, rope_theta);
+  p.workspace = workspace;
+  p.frag_rows = paged_frag_rows(cache->page_size);
+  if (cache->format == ATTNFUSE_CACHE_BF16) {
+    if ((rc = encode_map_bhnd(&p.tmK, cache->k, cache->k_strides, cache->num_pages, cache->Hkv, cache->page_size,
+                              cache->d, "cache k", p.frag_rows)))
+      return rc;
+    if ((rc = encode_map_bhnd(&p.tmV, cache->v, cache->v_strides, cache->num_pages, cache->Hkv, cache->page_size,
+                              cache->d, "cache v", p.frag_rows)))
+      return rc;
+  }
   return done(launch_paged_decode(p, cache->d, cache->format, stream), "paged decode launch");
 }
 

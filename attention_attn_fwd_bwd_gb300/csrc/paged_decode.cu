@@ -1,11 +1,30 @@
-// Decode over a paged cache: one query per sequence against that sequence's own length.
+// Decode over a paged cache for sm_103a: one query per sequence against that sequence's own length.
 //
 //   O_h = sum_n p_n v_n,  p = softmax over n in [max(0, L - W), L) of
 //   s_n = scale <R_{L-1} q_h, k_n> + slope_h (n - (L - 1)),  L = lens[b].
 //
-// One CTA per (sequence, query head); warps take keys in turn, each keeps a running maximum,
-// sum and accumulator (lane = d / 32 elements), and the warps' states are joined at the end.
+// The cache is read once, from HBM, and that bounds the kernel: 2 d g multiply-adds per pair of
+// K and V elements is far below what the tensor cores do meanwhile, on either path. So the
+// matrix instructions are warp-level ones with the KEYS as rows (S^T = K Q^T, O^T = V^T P^T):
+// their operands come straight from registers, which is where 4-bit codes have to be expanded
+// (writing them back to shared memory as bf16 for tcgen05 would move 94 of the 128 bytes per
+// cycle that shared memory has, and as much again to read them), and a group of 8 query heads
+// fills the instruction's 8 columns, where a 128-row query tile would be padding.
+//
+// Work. Sequences are cut into 64-key tiles; the tiles of the whole batch, ordered by (sequence,
+// KV head, chunk of query heads), are dealt to the CTAs in equal runs, from lengths read on the
+// device. A CTA walks the segments of its run. A segment that is a whole item (all tiles of one
+// (sequence, head chunk)) is finished in place; otherwise its (max, sum, acc) goes to the
+// workspace, at most two per CTA, and combine_kernel joins them in a fixed order.
+//
+// CTA: 4 consumer warps, each with 16 keys of every tile and its own running (max, sum, acc)
+// (joined once per segment), and a producer warp that looks pages up and fills a ring of tiles:
+// TMA boxes of one page's rows (bf16, 128-byte swizzle) or bulk copies (q4: codes and steps of a
+// page's rows are contiguous).
+#include <cuda.h>
 #include <cuda_runtime.h>
+
+#include <atomic>
 
 #include "launch.h"
 #include "paged.cuh"
@@ -14,104 +33,963 @@ namespace afx {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;              // consumers
+constexpr int kConsumers = kWarps * 32;
+constexpr int kThreads = kConsumers + 32;
+constexpr int kTile = kWarps * 16;     // keys per tile
+constexpr float kLazy = 8.0f;          // the running maximum may lag by 2^8
 
-// Element e of a cache row (any format).
-template <int D, bool Q4>
-__device__ __forceinline__ float row_elem(const uint8_t* row, const uint8_t* scales, int slot, int e) {
-  if (!Q4) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[e]);
-  const int g = e / 32, r = (e % 32) / 4, i = e % 4;
-  const uint16_t w = reinterpret_cast<const uint16_t*>(row + q4_place<D>(r, slot) * (D / 16))[g];
-  return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(scales)[g]) *
-         static_cast<float>(((w >> (4 * i)) & 15) - 8);
+template <int D, int NT, bool Q4>
+struct Cfg {
+  static constexpr int ROWS = 8 * NT;                                   // query heads per item
+  static constexpr uint32_t KB = kTile * (Q4 ? D / 2 : 2 * D);          // K (and V) bytes of a tile
+  static constexpr uint32_t SB = Q4 ? kTile * (D / 16) : 0;             // and their steps
+  static constexpr uint32_t STAGE = 2 * KB + 2 * SB;
+  static constexpr int STAGES = Q4 ? 4 : (NT == 1 || D == 64 ? 3 : 5);
+  static constexpr int CTAS = Q4 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 2 : (D == 64 ? 2 : 1));
+  static constexpr uint32_t QROW = 2 * D + 16;                          // padded query row
+  static constexpr uint32_t OFF_Q = STAGES * STAGE;
+  static constexpr uint32_t OFF_O = OFF_Q + 2 * ROWS * QROW;            // two warps' accumulators
+  static constexpr uint32_t OBUF = (D / 16) * NT * 512;
+  static constexpr uint32_t OFF_CTL = OFF_O + 2 * OBUF;
+};
+
+struct Ctl {
+  uint64_t full[8], empty[8];
+  uint32_t frags[8];                   // fragments of the tile that were loaded
+  int abort_flag;
+  int b0;                              // first sequence of this CTA's run, and the units of it
+  int rem0;                            // before the run
+  int64_t total;
+  int64_t wsum[kThreads / 32];
+  float m[kWarps][16], l[kWarps][16];
+};
+
+template <int D, int NT, bool Q4>
+constexpr size_t smem_bytes() {
+  return 1024 + Cfg<D, NT, Q4>::OFF_CTL + sizeof(Ctl);
 }
 
-template <int D, bool Q4>
-__global__ void __launch_bounds__(kWarps * 32) paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
-  constexpr int E = D / 32;
-  __shared__ float qs[D];
-  __shared__ float sm[kWarps], sl[kWarps], so[kWarps][D];
-  const int b = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq, kvh = h / p.g;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  int L = __ldg(p.lens + b);
-  if (L < 0 || L > p.cache.cap) {
-    atomicOr(p.status, kDevPageRange);
-    L = L < 0 ? 0 : p.cache.cap;
+// ---------------------------------------------------------------------------------------------
+// Warp-level matrix instructions and shared-memory fragments
+// ---------------------------------------------------------------------------------------------
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// Transpose of an 8x8 b16 matrix held one row pair per lane.
+__device__ __forceinline__ uint32_t movm(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// D (16 x 8, fp32) = A (16 x 16) B (16 x 8) + C
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t w;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, float x, float y, float z, float w) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
+}
+// Bulk copy of `bytes` (a multiple of 16; both addresses 16-byte aligned) that completes on bar.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// ---------------------------------------------------------------------------------------------
+// Work: lengths -> tiles -> this CTA's run
+// ---------------------------------------------------------------------------------------------
+struct Span {
+  int L, first, t0, nt;  // visible keys [first, L), first tile, tiles
+};
+
+__device__ __forceinline__ Span span_of(const PagedDecodeParams& p, int b) {
+  Span s;
+  s.L = min(max(__ldg(p.lens + b), 0), p.cache.cap);
+  s.first = p.window > 0 && s.L > p.window ? s.L - p.window : 0;
+  s.t0 = s.first / kTile;
+  s.nt = s.L > 0 ? (s.L - 1) / kTile - s.t0 + 1 : 0;
+  return s;
+}
+
+// Exclusive prefix over the block's threads of v, and the total (all threads call).
+template <int NTHREADS>
+__device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t* wsum, int64_t* total) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  int64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
-  const int first = p.window > 0 && L > p.window ? L - p.window : 0;
-  const __nv_bfloat16* q = p.q + b * p.q_sb + h * p.q_sh;
-  if (threadIdx.x < D / 2) {
-    const int i = threadIdx.x;
-    float lo = __bfloat162float(q[i]), hi = __bfloat162float(q[i + D / 2]);
-    if (p.rope && L > 0) {
-      float c, s, yl, yh;
-      rope_cossin_fine(static_cast<float>(L - 1), p.freqs.hi[i], p.freqs.lo[i], &c, &s);
-      rot_pair(lo, hi, c, s, yl, yh);
-      lo = yl;
-      hi = yh;
+  if (lane == 31) wsum[warp] = x;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < NTHREADS / 32; ++w) {
+    if (w < warp) before += wsum[w];
+    all += wsum[w];
+  }
+  *total = all;
+  return before + x - v;
+}
+
+// The run of CTA i over T units and the CTA that a unit belongs to, where G = min(CTAs, T) CTAs
+// share the units (so no run is empty).
+__device__ __forceinline__ int sharers(int64_t T, int ctas) { return T < ctas ? static_cast<int>(T) : ctas; }
+__device__ __forceinline__ int64_t run_start(int64_t T, int i, int G) { return T * i / G; }
+__device__ __forceinline__ int run_of(int64_t T, int64_t unit, int G) {
+  return static_cast<int>(((unit + 1) * G - 1) / T);
+}
+
+// Walks the segments of a run: all roles step through the same ones.
+struct Walk {
+  const PagedDecodeParams& p;
+  Span s;
+  int b, hh, t, left, n;  // item (b, hh), first tile of the segment (within the item), its tiles
+  bool head;              // the segment starts the run
+  __device__ Walk(const PagedDecodeParams& p_, int b0, int rem0, int left_) : p(p_), b(b0), left(left_), head(true) {
+    n = 0;
+    if (left <= 0) return;
+    s = span_of(p, b);
+    hh = rem0 / s.nt;
+    t = rem0 - hh * s.nt;
+    n = min(left, s.nt - t);
+  }
+  __device__ bool live() const { return n > 0; }
+  __device__ bool whole() const { return t == 0 && n == s.nt; }
+  __device__ void next() {
+    left -= n;
+    head = false;
+    t += n;
+    n = 0;
+    if (left <= 0) return;
+    if (t == s.nt) {
+      t = 0;
+      if (++hh == p.items) {
+        hh = 0;
+        do s = span_of(p, ++b);
+        while (s.nt == 0);
+      }
     }
-    qs[i] = lo;
-    qs[i + D / 2] = hi;
+    n = min(left, s.nt - t);
+  }
+};
+
+// ---------------------------------------------------------------------------------------------
+// Producer
+// ---------------------------------------------------------------------------------------------
+template <int D, int NT, bool Q4>
+__device__ __forceinline__ void produce(const PagedDecodeParams& p, uint8_t* smem, Ctl* ctl, Walk w) {
+  using C = Cfg<D, NT, Q4>;
+  const int lane = threadIdx.x % 32;
+  const PagedDev& c = p.cache;
+  const int F = p.frag_rows, nf = kTile / F;
+  int it = 0;
+  bool ok = true;
+  for (; w.live() && ok; w.next()) {
+    const int kvh = w.hh / p.chunks;
+    // fragments of F rows, one per lane and 32 at a time, looked up one window ahead
+    int base = (w.s.t0 + w.t) * nf;
+    const int end = base + w.n * nf;
+    auto look = [&](int f, int* slot, bool* bad) {
+      const int pos = f * F;
+      const bool need = f < end && pos < w.s.L && pos + F > w.s.first;
+      *slot = 0;
+      const int page = need ? page_at(c, w.b, pos, slot) : -1;
+      *bad = need && page < 0;
+      return page;
+    };
+    int slot, slot_n;
+    bool bad, bad_n;
+    int page = look(base + lane, &slot, &bad);
+    int page_n = look(base + 32 + lane, &slot_n, &bad_n);
+    for (int i = 0; i < w.n; ++i, ++it) {
+      const int f0 = (w.s.t0 + w.t + i) * nf;
+      if (f0 == base + 32) {
+        base += 32;
+        page = page_n, slot = slot_n, bad = bad_n;
+        page_n = look(base + 32 + lane, &slot_n, &bad_n);
+      }
+      const int st = it % C::STAGES;
+      if (it >= C::STAGES)
+        ok = mbar_wait(&ctl->empty[st], ((it / C::STAGES) - 1) & 1, p.status, &ctl->abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const int src = (f0 - base + lane) & 31;
+      const int pg = __shfl_sync(0xffffffffu, page, src), sl = __shfl_sync(0xffffffffu, slot, src);
+      const bool bd = __shfl_sync(0xffffffffu, bad, src);
+      const bool mine = lane < nf && pg >= 0;
+      const uint32_t got = __ballot_sync(0xffffffffu, mine);
+      if (lane < nf && bd) atomicOr(p.status, kDevPageRange);
+      uint8_t* stage = smem + st * C::STAGE;
+      if (lane == 0) {
+        ctl->frags[st] = got;
+        mbar_arrive_expect_tx(&ctl->full[st], __popc(got) * F * (C::STAGE / kTile));
+      }
+      __syncwarp();
+      if (mine) {
+        if constexpr (Q4) {
+          const uint32_t dst = smem_u32(stage);
+          const uint32_t cb = F * (D / 2), sb = F * (D / 16);
+          bulk_load(dst + lane * cb, c.k + pg * c.k_sp + kvh * c.k_sh + sl * (D / 2), cb, &ctl->full[st]);
+          bulk_load(dst + C::KB + lane * cb, c.v + pg * c.v_sp + kvh * c.v_sh + sl * (D / 2), cb, &ctl->full[st]);
+          bulk_load(dst + 2 * C::KB + lane * sb, c.ks + pg * c.ks_sp + kvh * c.ks_sh + sl * (D / 16), sb,
+                    &ctl->full[st]);
+          bulk_load(dst + 2 * C::KB + C::SB + lane * sb, c.vs + pg * c.vs_sp + kvh * c.vs_sh + sl * (D / 16), sb,
+                    &ctl->full[st]);
+        } else {
+#pragma unroll
+          for (int pn = 0; pn < D / 64; ++pn) {
+            uint8_t* kd = stage + pn * (kTile * 128) + lane * F * 128;
+            tma_load_4d(kd, &p.tmK, &ctl->full[st], pn * 64, sl, kvh, pg);
+            tma_load_4d(kd + C::KB, &p.tmV, &ctl->full[st], pn * 64, sl, kvh, pg);
+          }
+        }
+      }
+    }
+  }
+  // no copy may still be landing in shared memory when the CTA exits
+  if (lane == 0)
+    for (int k = max(0, it - C::STAGES); k < it; ++k)
+      mbar_wait(&ctl->full[k % C::STAGES], (k / C::STAGES) & 1, p.status, nullptr);
+}
+
+// ---------------------------------------------------------------------------------------------
+// Consumers. lane = 4 r + t. Matrix rows r, r + 8 are keys (S) or elements (O), columns 2t, 2t + 1
+// query heads; accumulator i: (row r + 8 (i / 2), column 2t + i % 2).
+// ---------------------------------------------------------------------------------------------
+
+// The key of a 16-key block that S row i stands for. q4: lane t of the V fragments reads rows
+// 2t, 2t + 1, 2t + 8, 2t + 9; this order makes the four keys of each such read differ modulo 4
+// (different banks, with the row format's exchange of halves), and the two keys of a quarter
+// warp's K read odd and even.
+template <bool Q4>
+__device__ __forceinline__ int key_of(int i) {
+  if (!Q4) return i;
+  const int j = i & 7;
+  return (i & 8) + ((j & 1) ? 4 + ((j >> 1) ^ 1) : j >> 1);
+}
+
+template <int D, int NT, bool Q4>
+__device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* smem, Ctl* ctl, Walk w) {
+  using C = Cfg<D, NT, Q4>;
+  constexpr int KS = D / 16;       // 16-element steps of a row
+  constexpr int G = D / kQ4Group;
+  constexpr int MT = D / 16;       // 16-element tiles of O
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, r = lane / 4, t = lane % 4;
+  const uint32_t base = smem_u32(smem);
+  // x = s * c2 in log2 units; 4-bit codes come out of the matrix product 16 times too small
+  const float c2 = p.scale_log2 * (Q4 ? 16.0f : 1.0f);
+  int it = 0;
+  bool ok = true;
+  for (; w.live(); w.next()) {
+    const int kvh = w.hh / p.chunks, h0 = kvh * p.g + (w.hh % p.chunks) * C::ROWS;
+    const int rows = min(C::ROWS, kvh * p.g + p.g - h0);
+    // ---- the item's queries: rotated in fp32, kept as the sum of two bf16 (16 bits) ----
+    {
+      const int i = tid % (D / 2);
+      float cs = 1.f, sn = 0.f;
+      if (p.rope) rope_cossin_fine(static_cast<float>(w.s.L - 1), p.freqs.hi[i], p.freqs.lo[i], &cs, &sn);
+#pragma unroll
+      for (int j = tid / (D / 2); j < C::ROWS; j += kConsumers / (D / 2)) {
+        float x = 0.f, y = 0.f;
+        if (j < rows) {
+          const __nv_bfloat16* q = p.q + w.b * p.q_sb + (h0 + j) * p.q_sh + i;
+          x = __bfloat162float(q[0]);
+          y = __bfloat162float(q[D / 2]);
+          if (p.rope) {
+            float a, b;
+            rot_pair(x, y, cs, sn, a, b);
+            x = a, y = b;
+          }
+        }
+        __nv_bfloat16* hi = reinterpret_cast<__nv_bfloat16*>(smem + C::OFF_Q + j * C::QROW);
+        __nv_bfloat16* lo = reinterpret_cast<__nv_bfloat16*>(smem + C::OFF_Q + (C::ROWS + j) * C::QROW);
+        hi[i] = __float2bfloat16_rn(x);
+        hi[i + D / 2] = __float2bfloat16_rn(y);
+        lo[i] = __float2bfloat16_rn(x - __bfloat162float(hi[i]));
+        lo[i + D / 2] = __float2bfloat16_rn(y - __bfloat162float(hi[i + D / 2]));
+      }
+    }
+    named_bar_sync(1, kConsumers);
+    uint32_t qf[2][NT][KS][2];  // [hi, lo]
+#pragma unroll
+    for (int part = 0; part < 2; ++part)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint32_t row = base + C::OFF_Q + (part * C::ROWS + nt * 8 + r) * C::QROW;
+        if constexpr (Q4) {
+          // group g, step s: the pairs (e, e + 4) of elements 32g + 8t + e, e = 2s and 2s + 1
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const uint4 x = lds128(row + g * 64 + t * 16);
+            qf[part][nt][2 * g][0] = __byte_perm(x.x, x.z, 0x5410);
+            qf[part][nt][2 * g][1] = __byte_perm(x.x, x.z, 0x7632);
+            qf[part][nt][2 * g + 1][0] = __byte_perm(x.y, x.w, 0x5410);
+            qf[part][nt][2 * g + 1][1] = __byte_perm(x.y, x.w, 0x7632);
+          }
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            qf[part][nt][ks][0] = lds32(row + ks * 32 + t * 4);
+            qf[part][nt][ks][1] = lds32(row + ks * 32 + t * 4 + 16);
+          }
+        }
+      }
+    // q4: a nibble n = code + 8 enters the product as 1 + n/16 (four bits set into the mantissa of
+    // 1.0), so each group's sum starts at -1.5 times the sum of its q. The sum is itself a
+    // product with ones.
+    float qs[Q4 ? NT : 1][Q4 ? G : 1][2];
+    if constexpr (Q4) {
+      const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          float x[4] = {};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mma_bf16(x, ones, qf[e & 1][nt][2 * g + e / 2][0], qf[e & 1][nt][2 * g + e / 2][1]);
+          qs[nt][g][0] = -1.5f * x[0];
+          qs[nt][g][1] = -1.5f * x[1];
+        }
+    }
+    float slope[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int j = nt * 8 + 2 * t + e;
+        slope[nt][e] = p.slopes && j < rows ? __ldg(p.slopes + h0 + j) * kLog2e : 0.f;
+      }
+
+    float o[NT][MT][4] = {};
+    float m[NT][2], l[NT][2] = {};
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = kNegInf;
+    // q4: weights p * step go into fp16 as p * step * vmul[g], vmul = 2^-e of the largest step
+    // seen so far in group g (it may be exceeded by 2^4 before it is renewed)
+    uint32_t vthr[Q4 ? G / 2 : 1] = {};
+    float vmul[Q4 ? G : 1];
+#pragma unroll
+    for (int g = 0; g < (Q4 ? G : 1); ++g) vmul[g] = 1.f;
+
+    for (int i = 0; i < w.n; ++i, ++it) {
+      const int st = it % C::STAGES;
+      if (ok) ok = mbar_wait(&ctl->full[st], (it / C::STAGES) & 1, p.status, &ctl->abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) continue;  // unwind through the same barriers as the other warps
+      const uint32_t stage = base + st * C::STAGE;
+      const int n0 = (w.s.t0 + w.t + i) * kTile + warp * 16;
+      const bool loaded = (ctl->frags[st] >> (warp * 16 / p.frag_rows)) & 1;
+      if (loaded && n0 < w.s.L && n0 + 16 > w.s.first) {
+        const bool edge = n0 < w.s.first || n0 + 16 > w.s.L;
+        // ---- scores: s[nt][i], key rows r and r + 8 ----
+        float s[NT][4];
+        uint32_t vs[2][Q4 ? G / 2 : 1];  // q4: steps of V's rows r, r + 8 (two bf16 per word)
+        const int ka = key_of<Q4>(r), kb = key_of<Q4>(r + 8);
+        if constexpr (Q4) {
+          uint32_t kw[2][G], ks[2][G / 2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int key = warp * 16 + (e ? kb : ka);
+            if constexpr (D == 128) {
+              const uint4 x = lds128(stage + key * 64 + ((t ^ (key & 2)) * 16));
+              kw[e][0] = __byte_perm(x.x, x.z, 0x5410);
+              kw[e][1] = __byte_perm(x.x, x.z, 0x7632);
+              kw[e][2] = __byte_perm(x.y, x.w, 0x5410);
+              kw[e][3] = __byte_perm(x.y, x.w, 0x7632);
+              const uint2 y = lds64(stage + 2 * C::KB + key * 8);
+              ks[e][0] = y.x, ks[e][1] = y.y;
+              const uint2 z = lds64(stage + 2 * C::KB + C::SB + key * 8);
+              vs[e][0] = z.x, vs[e][1] = z.y;
+            } else {
+              const uint2 x = lds64(stage + key * 32 + t * 8);
+              kw[e][0] = __byte_perm(x.x, x.y, 0x5410);
+              kw[e][1] = __byte_perm(x.x, x.y, 0x7632);
+              ks[e][0] = lds32(stage + 2 * C::KB + key * 4);
+              vs[e][0] = lds32(stage + 2 * C::KB + C::SB + key * 4);
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            uint32_t a[2][4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t x = kw[e][g];
+              a[0][e] = ((x << 3) & 0x00780078u) | 0x3F803F80u;
+              a[0][2 + e] = ((x >> 1) & 0x00780078u) | 0x3F803F80u;
+              a[1][e] = ((x >> 5) & 0x00780078u) | 0x3F803F80u;
+              a[1][2 + e] = ((x >> 9) & 0x00780078u) | 0x3F803F80u;
+            }
+            const float sa = (g & 1) ? bf16hi_to_f32(ks[0][g / 2]) : bf16lo_to_f32(ks[0][g / 2]);
+            const float sb = (g & 1) ? bf16hi_to_f32(ks[1][g / 2]) : bf16lo_to_f32(ks[1][g / 2]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float x[4] = {qs[nt][g][0], qs[nt][g][1], qs[nt][g][0], qs[nt][g][1]};
+#pragma unroll
+              for (int part = 0; part < 2; ++part)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) mma_bf16(x, a[e], qf[part][nt][2 * g + e][0], qf[part][nt][2 * g + e][1]);
+              s[nt][0] = fmaf(sa, x[0], s[nt][0]);
+              s[nt][1] = fmaf(sa, x[1], s[nt][1]);
+              s[nt][2] = fmaf(sb, x[2], s[nt][2]);
+              s[nt][3] = fmaf(sb, x[3], s[nt][3]);
+            }
+          }
+        } else {
+          float x[2][NT][4] = {};
+          const int row = warp * 16 + (lane & 15);
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            uint32_t a[4];
+            ldsm4(a, stage + (k / 4) * (kTile * 128) + row * 128 + ((((k & 3) * 2 + (lane >> 4)) ^ (row & 7)) * 16));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int part = 0; part < 2; ++part) mma_bf16(x[part][nt], a, qf[part][nt][k][0], qf[part][nt][k][1]);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[nt][e] = x[0][nt][e] + x[1][nt][e];
+        }
+        // ---- log2 units, bias, mask ----
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[nt][e] *= c2;
+        if (p.slopes) {
+          const float da = static_cast<float>(n0 + ka - (w.s.L - 1)), db = static_cast<float>(n0 + kb - (w.s.L - 1));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[nt][e] = fmaf(slope[nt][e & 1], e < 2 ? da : db, s[nt][e]);
+        }
+        if (edge) {
+          const bool va = n0 + ka >= w.s.first && n0 + ka < w.s.L, vb = n0 + kb >= w.s.first && n0 + kb < w.s.L;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!(e < 2 ? va : vb)) s[nt][e] = kNegInf;
+          if constexpr (Q4) {
+#pragma unroll
+            for (int q = 0; q < G / 2; ++q) {
+              if (!va) vs[0][q] = 0;
+              if (!vb) vs[1][q] = 0;
+            }
+          }
+        }
+        // ---- running maximum, renewed only where a score passes it by 2^8 ----
+        bool up = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) up |= s[nt][e] > m[nt][e & 1] + kLazy;
+        if constexpr (Q4) {
+#pragma unroll
+          for (int q = 0; q < G / 2; ++q) up |= __vmaxu2(__vmaxu2(vs[0][q], vs[1][q]), vthr[q]) != vthr[q];
+        }
+        if (__any_sync(0xffffffffu, up)) {
+          float f[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = fmaxf(s[nt][e], s[nt][e + 2]);
+#pragma unroll
+              for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+              const float mn = fmaxf(m[nt][e], x);
+              f[nt][e] = ex2_approx(m[nt][e] - (mn == kNegInf ? 0.f : mn));
+              m[nt][e] = mn;
+              l[nt][e] *= f[nt][e];
+            }
+          float fv[Q4 ? G : 1];
+          if constexpr (Q4) {
+#pragma unroll
+            for (int q = 0; q < G / 2; ++q) {
+              uint32_t x = __vmaxu2(vs[0][q], vs[1][q]);
+#pragma unroll
+              for (int off = 4; off < 32; off <<= 1) x = __vmaxu2(x, __shfl_xor_sync(0xffffffffu, x, off));
+              uint32_t thr = 0;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t old = (vthr[q] >> (16 * e)) & 0xFFFFu, now = (x >> (16 * e)) & 0xFFFFu;
+                const int g = 2 * q + e;
+                fv[g] = 1.f;
+                uint32_t th = old;
+                if (now > old) {
+                  const uint32_t ex = min(now >> 7, 253u);  // biased exponent of the largest step
+                  const float mul = __uint_as_float((254u - ex) << 23);
+                  fv[g] = __fdiv_rn(mul, vmul[g]);
+                  vmul[g] = mul;
+                  th = min(((ex + 4) << 7) | 0x7Fu, 0x7FFFu);
+                }
+                thr |= th << (16 * e);
+              }
+              vthr[q] = thr;
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < MT; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[nt][k][e] *= Q4 ? f[nt][e & 1] * fv[Q4 ? k / 2 : 0] : f[nt][e & 1];
+        }
+        // ---- weights ----
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float mm = m[nt][e & 1];
+            s[nt][e] = ex2_approx(s[nt][e] - (mm == kNegInf ? 0.f : mm));
+            l[nt][e & 1] += s[nt][e];
+          }
+        // ---- O^T += V^T P^T ----
+        if constexpr (Q4) {
+          uint32_t vw[2][G];  // keys (2t, 2t + 1), (2t + 8, 2t + 9): 4 nibbles of each per group
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int k0 = warp * 16 + key_of<true>(8 * e + 2 * t), k1 = warp * 16 + key_of<true>(8 * e + 2 * t + 1);
+            const uint32_t v0 = stage + C::KB;
+            if constexpr (D == 128) {
+              const uint2 x = lds64(v0 + k0 * 64 + ((r ^ ((k0 & 2) << 1)) * 8));
+              const uint2 y = lds64(v0 + k1 * 64 + ((r ^ ((k1 & 2) << 1)) * 8));
+              vw[e][0] = __byte_perm(x.x, y.x, 0x5410);
+              vw[e][1] = __byte_perm(x.x, y.x, 0x7632);
+              vw[e][2] = __byte_perm(x.y, y.y, 0x5410);
+              vw[e][3] = __byte_perm(x.y, y.y, 0x7632);
+            } else {
+              const uint32_t x = lds32(v0 + k0 * 32 + r * 4), y = lds32(v0 + k1 * 32 + r * 4);
+              vw[e][0] = __byte_perm(x, y, 0x5410);
+              vw[e][1] = __byte_perm(x, y, 0x7632);
+            }
+          }
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            uint32_t a[2][4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              // fp16 bit patterns 1024 + n and 1024 + 16 n; exact down to n - 8 = code
+              const uint32_t x = vw[e][g], y = x >> 8;
+              a[0][2 * e] = hadd2((x & 0x000F000Fu) | 0x64006400u, 0xE408E408u);
+              a[0][2 * e + 1] = hfma2((x & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
+              a[1][2 * e] = hadd2((y & 0x000F000Fu) | 0x64006400u, 0xE408E408u);
+              a[1][2 * e + 1] = hfma2((y & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
+            }
+            const float sa = ((g & 1) ? bf16hi_to_f32(vs[0][g / 2]) : bf16lo_to_f32(vs[0][g / 2])) * vmul[g];
+            const float sb = ((g & 1) ? bf16hi_to_f32(vs[1][g / 2]) : bf16lo_to_f32(vs[1][g / 2])) * vmul[g];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint32_t b0 = movm(pack_f16x2(s[nt][0] * sa, s[nt][1] * sa));
+              const uint32_t b1 = movm(pack_f16x2(s[nt][2] * sb, s[nt][3] * sb));
+              mma_f16(o[nt][2 * g], a[0], b0, b1);
+              mma_f16(o[nt][2 * g + 1], a[1], b0, b1);
+            }
+          }
+        } else {
+          // p as the sum of two bf16: rounded once, its error would be as large as that of the
+          // bf16 output itself
+          uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t x = pack_bf16x2(s[nt][2 * e], s[nt][2 * e + 1]);
+              ph[nt][e] = movm(x);
+              pl[nt][e] = movm(pack_bf16x2(s[nt][2 * e] - bf16lo_to_f32(x), s[nt][2 * e + 1] - bf16hi_to_f32(x)));
+            }
+          uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};  // rows behind the length may hold anything, NaN too
+          if (edge) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int n = n0 + 8 * e + 2 * t;
+              keep[e] = (n >= w.s.first && n < w.s.L ? 0xFFFFu : 0u) |
+                        (n + 1 >= w.s.first && n + 1 < w.s.L ? 0xFFFF0000u : 0u);
+            }
+          }
+          const int row = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+          for (int k = 0; k < MT; ++k) {
+            uint32_t a[4];
+            ldsm4t(a, stage + C::KB + (k / 4) * (kTile * 128) + row * 128 +
+                          ((((k & 3) * 2 + ((lane >> 3) & 1)) ^ (row & 7)) * 16));
+            if (edge) {
+              a[0] &= keep[0], a[1] &= keep[0];
+              a[2] &= keep[1], a[3] &= keep[1];
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_bf16(o[nt][k], a, ph[nt][0], ph[nt][1]);
+              mma_bf16(o[nt][k], a, pl[nt][0], pl[nt][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->empty[st]);
+    }
+
+    // ---- join the warps: weights 2^(m_w - M), then pairwise sums in a fixed order ----
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], off);
+        if (r == 0) {
+          ctl->m[warp][nt * 8 + 2 * t + e] = m[nt][e];
+          ctl->l[warp][nt * 8 + 2 * t + e] = l[nt][e];
+        }
+      }
+    named_bar_sync(1, kConsumers);
+    float M[NT][2], total[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int j = nt * 8 + 2 * t + e;
+        float x = ctl->m[0][j];
+#pragma unroll
+        for (int k = 1; k < kWarps; ++k) x = fmaxf(x, ctl->m[k][j]);
+        const float bs = x == kNegInf ? 0.f : x;
+        float y = 0.f;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) y += ctl->l[k][j] * ex2_approx(ctl->m[k][j] - bs);
+        M[nt][e] = x;
+        total[nt][e] = y;
+        const float f = ex2_approx(m[nt][e] - bs);
+#pragma unroll
+        for (int k = 0; k < MT; ++k) {
+          const float fk = Q4 ? f * __fdiv_rn(1.f, vmul[Q4 ? k / 2 : 0]) : f;
+          o[nt][k][e] *= fk;
+          o[nt][k][e + 2] *= fk;
+        }
+      }
+    const uint32_t obuf = base + C::OFF_O + lane * 16;
+    auto put = [&](uint32_t at) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < MT; ++k)
+          sts128(at + (nt * MT + k) * 512, o[nt][k][0], o[nt][k][1], o[nt][k][2], o[nt][k][3]);
+    };
+    auto add = [&](uint32_t at) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < MT; ++k) {
+          const uint4 x = lds128(at + (nt * MT + k) * 512);
+          o[nt][k][0] += __uint_as_float(x.x);
+          o[nt][k][1] += __uint_as_float(x.y);
+          o[nt][k][2] += __uint_as_float(x.z);
+          o[nt][k][3] += __uint_as_float(x.w);
+        }
+    };
+    if (warp >= 2) put(obuf + (warp - 2) * C::OBUF);
+    named_bar_sync(1, kConsumers);
+    if (warp < 2) add(obuf + warp * C::OBUF);
+    if (warp == 1) put(obuf + C::OBUF);
+    named_bar_sync(1, kConsumers);
+    if (warp == 0) {
+      add(obuf + C::OBUF);
+      const bool whole = w.whole();
+      const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (w.head ? 0 : 1)) * C::ROWS;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int j = nt * 8 + 2 * t + e;
+          if (j >= rows) continue;
+          const float tot = total[nt][e];
+          const bool any = !(tot == 0.f);  // a NaN goes to the output
+          if (whole) {
+            __nv_bfloat16* out = p.out + w.b * p.o_sb + (h0 + j) * p.o_sh;
+            const float inv = any ? __fdiv_rn(1.f, tot) : 0.f;
+#pragma unroll
+            for (int k = 0; k < MT; ++k)
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const int d = Q4 ? (k / 2) * 32 + 4 * r + 2 * (k & 1) + u : k * 16 + r + 8 * u;
+                out[d] = __float2bfloat16_rn(any ? o[nt][k][e + 2 * u] * inv : 0.f);
+              }
+            if (p.lse && r == 0)
+              p.lse[static_cast<int64_t>(w.b) * p.Hq + h0 + j] = any ? (M[nt][e] + log2f(tot)) * kLn2 : kNegInf;
+          } else {
+            float* acc = p.part_acc + (part + j) * D;
+#pragma unroll
+            for (int k = 0; k < MT; ++k)
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const int d = Q4 ? (k / 2) * 32 + 4 * r + 2 * (k & 1) + u : k * 16 + r + 8 * u;
+                acc[d] = o[nt][k][e + 2 * u];
+              }
+            if (r == 0) p.part_ml[part + j] = make_float2(M[nt][e], tot);
+          }
+        }
+    }
+  }
+}
+
+template <int D, int NT, bool Q4>
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT, Q4>::CTAS)
+    paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
+  using C = Cfg<D, NT, Q4>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + C::OFF_CTL);
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&ctl->full[i], 1);
+      mbar_init(&ctl->empty[i], kWarps);
+    }
+    ctl->abort_flag = 0;
+    fence_mbar_init();
+  }
+  // Launched as a programmatic dependent: global memory is touched only from here on.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // this CTA's run: thread j sums the tiles of its share of the sequences
+  const int B = p.cache.B, share = (B + kThreads - 1) / kThreads;
+  int64_t mine = 0;
+  for (int b = tid * share; b < min(B, (tid + 1) * share); ++b) {
+    const int L = __ldg(p.lens + b);
+    if (blockIdx.x == 0 && (L < 0 || L > p.cache.cap)) atomicOr(p.status, kDevPageRange);
+    mine += span_of(p, b).nt;
+  }
+  int64_t tiles;
+  int64_t before = block_prefix<kThreads>(mine, ctl->wsum, &tiles);
+  const int64_t T = tiles * p.items;
+  const int G = sharers(T, gridDim.x), cta = blockIdx.x;
+  const int64_t lo = cta < G ? run_start(T, cta, G) : 0, hi = cta < G ? run_start(T, cta + 1, G) : 0;
+  if (lo < hi && before * p.items <= lo && lo < (before + mine) * p.items) {
+    int b = tid * share;
+    for (;; ++b) {
+      const int nt = span_of(p, b).nt;
+      if (lo < (before + nt) * p.items) break;
+      before += nt;
+    }
+    ctl->b0 = b;
+    ctl->rem0 = static_cast<int>(lo - before * p.items);
   }
   __syncthreads();
-  float qr[E], o[E] = {}, m = kNegInf, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) qr[e] = qs[lane + 32 * e];
-  const float slope = p.slopes ? __ldg(p.slopes + h) * kLog2e : 0.f;
-  for (int n = first + warp; n < L; n += kWarps) {
-    int slot;
-    const int page = page_at(p.cache, b, n, &slot);
-    if (page < 0) {
-      if (lane == 0) atomicOr(p.status, kDevPageRange);
-      continue;
-    }
-    const uint8_t* kr = p.cache.k + page * p.cache.k_sp + kvh * p.cache.k_sh + slot * p.cache.k_st;
-    const uint8_t* vr = p.cache.v + page * p.cache.v_sp + kvh * p.cache.v_sh + slot * p.cache.v_st;
-    const uint8_t* ks = p.cache.ks + page * p.cache.ks_sp + kvh * p.cache.ks_sh + slot * (D / 16);
-    const uint8_t* vs = p.cache.vs + page * p.cache.vs_sp + kvh * p.cache.vs_sh + slot * (D / 16);
-    float x = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) x = fmaf(qr[e], row_elem<D, Q4>(kr, ks, slot, lane + 32 * e), x);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-    x = x * p.scale_log2 + slope * static_cast<float>(n - (L - 1));
-    const float mn = fmaxf(m, x);
-    const float base = mn == kNegInf ? 0.f : mn;
-    const float a = ex2_approx(m - base), w = ex2_approx(x - base);
-    m = mn;
-    l = l * a + w;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * a + w * row_elem<D, Q4>(vr, vs, slot, lane + 32 * e);
+  if (lo < hi) {
+    Walk w(p, ctl->b0, ctl->rem0, static_cast<int>(hi - lo));
+    if (tid >= kConsumers) produce<D, NT, Q4>(p, smem, ctl, w);
+    else consume<D, NT, Q4>(p, smem, ctl, w);
   }
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
-#pragma unroll
-  for (int e = 0; e < E; ++e) so[warp][lane + 32 * e] = o[e];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Joins the segments of items that more than one CTA walked, and writes the rows of empty
+// sequences. One CTA per (sequence, query head), thread = output element.
+template <int D>
+__global__ void __launch_bounds__(D) paged_combine_kernel(const __grid_constant__ PagedDecodeParams p) {
+  __shared__ int64_t wsum[D / 32];
+  __shared__ float w_sh[kPagedMaxCtas];
+  __shared__ float red[D / 32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int b = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int rows = p.head_rows;
+  // tiles of all sequences, and of those before b
+  int64_t all = 0, pre = 0;
+  for (int i = tid; i < p.cache.B; i += D) {
+    const int nt = span_of(p, i).nt;
+    all += nt;
+    if (i < b) pre += nt;
+  }
+  int64_t tiles, before;
+  block_prefix<D>(all, wsum, &tiles);
   __syncthreads();
-  if (threadIdx.x < D) {
-    float M = kNegInf, total = 0.f, acc = 0.f;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w]);
-    const float base = M == kNegInf ? 0.f : M;
-    for (int w = 0; w < kWarps; ++w) {
-      const float a = ex2_approx(sm[w] - base);
-      total += a * sl[w];
-      acc += a * so[w][threadIdx.x];
-    }
-    const bool any = !(total == 0.f);  // a NaN goes to the output
-    p.out[b * p.o_sb + h * p.o_sh + threadIdx.x] = __float2bfloat16_rn(any ? acc / total : 0.f);
-    if (p.lse && threadIdx.x == 0) p.lse[blockIdx.x] = any ? (base + log2f(total)) * kLn2 : kNegInf;
+  block_prefix<D>(pre, wsum, &before);
+  const int nt = span_of(p, b).nt;
+  __nv_bfloat16* out = p.out + b * p.o_sb + h * p.o_sh + tid;
+  if (nt == 0) {
+    *out = __float2bfloat16_rn(0.f);
+    if (p.lse && tid == 0) p.lse[blockIdx.x] = kNegInf;
+    return;
   }
+  const int kvh = h / p.g, j0 = h % p.g;
+  const int hh = kvh * p.chunks + j0 / rows, j = j0 % rows;
+  const int64_t T = tiles * p.items;
+  const int64_t s = before * p.items + static_cast<int64_t>(hh) * nt, e = s + nt;
+  const int G = sharers(T, p.ctas);
+  const int i0 = run_of(T, s, G), i1 = run_of(T, e - 1, G);
+  if (i0 == i1) return;  // finished by that CTA
+  const int n = i1 - i0 + 1;
+  const int first_slot = run_start(T, i0, G) < s ? 1 : 0;
+  auto row_of = [&](int k) { return (static_cast<int64_t>(i0 + k) * 2 + (k == 0 ? first_slot : 0)) * rows + j; };
+  float mx = kNegInf;
+  for (int k = tid; k < n; k += D) mx = fmaxf(mx, p.part_ml[row_of(k)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (lane == 0) red[warp] = mx;
+  __syncthreads();
+  float M = red[0];
+#pragma unroll
+  for (int k = 1; k < D / 32; ++k) M = fmaxf(M, red[k]);
+  const float base = M == kNegInf ? 0.f : M;
+  __syncthreads();
+  float sum = 0.f;
+  for (int k = tid; k < n; k += D) {
+    const float2 ml = p.part_ml[row_of(k)];
+    const float w = ex2_approx(ml.x - base);
+    w_sh[k] = w;
+    sum += w * ml.y;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) red[warp] = sum;
+  __syncthreads();
+  float total = 0.f;
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) total += red[k];
+  float acc = 0.f;
+#pragma unroll 8
+  for (int k = 0; k < n; ++k) acc += w_sh[k] * p.part_acc[row_of(k) * D + tid];
+  const bool any = !(total == 0.f);
+  *out = __float2bfloat16_rn(any ? acc / total : 0.f);
+  if (p.lse && tid == 0) p.lse[blockIdx.x] = any ? (M + log2f(total)) * kLn2 : kNegInf;
+}
+
+int sm_count() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+template <int D, int NT, bool Q4>
+int cta_count() {
+  return std::min(sm_count() * Cfg<D, NT, Q4>::CTAS, kPagedMaxCtas);
+}
+
+template <int D, int NT, bool Q4>
+cudaError_t launch(PagedDecodeParams p, cudaStream_t stream) {
+  using C = Cfg<D, NT, Q4>;
+  static_assert(smem_bytes<D, NT, Q4>() <= 232448 && (smem_bytes<D, NT, Q4>() + 1024) * C::CTAS <= 233472,
+                "shared memory of the resident CTAs");
+  static_assert(C::STAGES <= 8, "barriers");
+  auto kern = paged_decode_kernel<D, NT, Q4>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D, NT, Q4>());
+  if (e != cudaSuccess) return e;
+  p.head_rows = C::ROWS;
+  p.chunks = (p.g + C::ROWS - 1) / C::ROWS;
+  p.items = p.cache.Hkv * p.chunks;
+  p.ctas = cta_count<D, NT, Q4>();
+  p.part_acc = static_cast<float*>(p.workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part_acc + (int64_t)p.ctas * 2 * C::ROWS * D);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<D, NT, Q4>();
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, p);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(p.cache.B * p.Hq);
+  cfg.blockDim = dim3(D);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D>, p);
+}
+
+template <int D, int NT, bool Q4>
+size_t workspace() {
+  return (size_t)cta_count<D, NT, Q4>() * 2 * Cfg<D, NT, Q4>::ROWS * (D * sizeof(float) + sizeof(float2));
 }
 
 }  // namespace
 
-size_t paged_decode_workspace(int, int) { return 0; }
+// Up to 8 query heads per KV head fill one column tile; more take two (16 heads a pass), and
+// groups above 16 read the cache once per 16 heads (through L2).
+#define AFX_PAGED_DISPATCH(fn, ...)                                                              \
+  (format == kPagedQ4 ? (d == 128 ? (g <= 8 ? fn<128, 1, true>(__VA_ARGS__) : fn<128, 2, true>(__VA_ARGS__))     \
+                                  : (g <= 8 ? fn<64, 1, true>(__VA_ARGS__) : fn<64, 2, true>(__VA_ARGS__)))      \
+                      : (d == 128 ? (g <= 8 ? fn<128, 1, false>(__VA_ARGS__) : fn<128, 2, false>(__VA_ARGS__))   \
+                                  : (g <= 8 ? fn<64, 1, false>(__VA_ARGS__) : fn<64, 2, false>(__VA_ARGS__))))
+
+size_t paged_decode_workspace(int d, int g, int format) { return AFX_PAGED_DISPATCH(workspace); }
 
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, int d, int format, cudaStream_t stream) {
-  void (*kern)(PagedDecodeParams) = nullptr;
-  if (format == kPagedQ4) kern = d == 128 ? paged_decode_kernel<128, true> : paged_decode_kernel<64, true>;
-  else kern = d == 128 ? paged_decode_kernel<128, false> : paged_decode_kernel<64, false>;
-  kern<<<p.cache.B * p.Hq, kWarps * 32, 0, stream>>>(p);
-  return cudaGetLastError();
+  const int g = p.g;
+  return AFX_PAGED_DISPATCH(launch, p, stream);
+}
+
+int paged_frag_rows(int page_size) {
+  int a = page_size, b = kTile;
+  while (b) {
+    const int r = a % b;
+    a = b;
+    b = r;
+  }
+  return a;
 }
 
 }  // namespace afx
