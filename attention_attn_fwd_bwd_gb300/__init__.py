@@ -592,16 +592,54 @@ def rope_prerotate(x, rope_theta, out=None, workspace=None, stream=None):
     return out
 
 
+# Paged caches. A decode step on a small batch is a few microseconds on the GPU, so the binding's
+# own cost counts here: checks that pass touch each tensor once (_need runs for the message of
+# one that does not), a cache's C struct is built once, and pointers go to ctypes as integers.
+_I3, _I4 = ctypes.c_int64 * 3, ctypes.c_int64 * 4
+
+
 def _live_strides(t, n):
     """Element strides with those of one-element dimensions, which address nothing and may hold
     any value, replaced by what a contiguous tensor would have."""
-    st = list(t.stride())
-    inner = 1
-    for i in range(n - 1, -1, -1):
-        if t.size(i) == 1:
-            st[i] = inner
-        inner = max(inner, st[i] * t.size(i))
-    return (ctypes.c_int64 * n)(*st)
+    st, shape = t.stride(), t.shape
+    if 1 in shape:
+        st = list(st)
+        inner = 1
+        for i in range(n - 1, -1, -1):
+            if shape[i] == 1:
+                st[i] = inner
+            elif st[i] * shape[i] > inner:
+                inner = st[i] * shape[i]
+    return _I4(*st) if n == 4 else _I3(*st)
+
+
+def _want(t, name, dtype, shape, device, contiguous=False):
+    if not (getattr(t, "dtype", None) is dtype and t.shape == shape and t.device == device
+            and (not contiguous or t.is_contiguous())):
+        _need(t, name, (dtype,), shape, device, contiguous)
+
+
+def _launch_stream(device, stream):
+    """(context manager or None, stream handle): _launch_context, without a context manager where
+    the tensors' device is the current one already."""
+    import torch
+
+    if stream is None and device.index == torch.cuda.current_device():
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return None, raw(device.index)
+    return _launch_context(device, stream)
+
+
+def _launch(fn, args, device, stream):
+    ctx, st = _launch_stream(device, stream)
+    if ctx is None:
+        rc = fn(*args, st)
+    else:
+        with ctx:
+            rc = fn(*args, st)
+    if rc:
+        _check(rc)
 
 
 class PagedCache:
@@ -610,35 +648,50 @@ class PagedCache:
     k, v: bf16 [num_pages, Hkv, page_size, d], or for the 4-bit format uint8 [num_pages, Hkv,
     page_size, d/2] with k_scales, v_scales bf16 [num_pages, Hkv, page_size, d/32]. page_table:
     int32 [B, max_pages]; position p of sequence b is slot p % page_size of page
-    page_table[b, p // page_size]. The object holds references only: the caller allocates pages,
-    fills the table and keeps the lengths. page_size: a multiple of 16.
+    page_table[b, p // page_size]. The object holds references only, and its tensors cannot be
+    exchanged: the caller allocates pages, fills the table in place (or makes another PagedCache
+    over the same pools) and keeps the lengths. page_size: a multiple of 16.
     """
 
     def __init__(self, k, v, page_table, k_scales=None, v_scales=None):
         import torch
 
-        bf16 = (torch.bfloat16,)
-        self.q4 = isinstance(k, torch.Tensor) and k.dtype == torch.uint8
-        dims = "[num_pages, Hkv, page_size, d/2]" if self.q4 else "[num_pages, Hkv, page_size, d]"
-        types = (torch.uint8,) if self.q4 else (torch.bfloat16, torch.uint8)
-        _need(k, "cache k", types, ndim=4, dims=dims)
-        self.num_pages, self.Hkv, self.page_size, row = k.shape
-        self.d = 2 * row if self.q4 else row
-        self.device = k.device
-        _need(v, "cache v", (k.dtype,), tuple(k.shape), self.device)
-        if self.q4:
-            steps = (self.num_pages, self.Hkv, self.page_size, self.d // 32)
-            _need(k_scales, "cache k_scales", bf16, steps, self.device)
-            _need(v_scales, "cache v_scales", bf16, steps, self.device)
+        bf16 = torch.bfloat16
+        q4 = getattr(k, "dtype", None) is torch.uint8
+        if not (q4 or getattr(k, "dtype", None) is bf16) or k.dim() != 4 or k.device.type != "cuda":
+            _need(k, "cache k", (torch.uint8,) if q4 else (bf16, torch.uint8), ndim=4,
+                  dims="[num_pages, Hkv, page_size, d/2]" if q4 else "[num_pages, Hkv, page_size, d]")
+        shape, dev = k.shape, k.device
+        P, H, S, row = shape
+        d = 2 * row if q4 else row
+        _want(v, "cache v", k.dtype, shape, dev)
+        if q4:
+            _want(k_scales, "cache k_scales", bf16, (P, H, S, d // 32), dev)
+            _want(v_scales, "cache v_scales", bf16, (P, H, S, d // 32), dev)
         elif k_scales is not None or v_scales is not None:
             raise ValueError("k_scales, v_scales belong to the 4-bit format (uint8 pools)")
-        _need(page_table, "page_table", (torch.int32,), ndim=2, dims="[B, max_pages]", device=self.device)
-        if page_table.size(1) > 1 and page_table.stride(1) != 1:
+        if getattr(page_table, "dtype", None) is not torch.int32 or page_table.dim() != 2 or page_table.device != dev:
+            _need(page_table, "page_table", (torch.int32,), ndim=2, dims="[B, max_pages]", device=dev)
+        B, max_pages = page_table.shape
+        ts = page_table.stride()
+        if max_pages > 1 and ts[1] != 1:
             raise ValueError("page_table: rows must be contiguous")
-        self.B, self.max_pages = page_table.shape
-        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
-        self.page_table = page_table
-        self.format = CACHE_Q4 if self.q4 else CACHE_BF16
+        self._tensors = (k, v, page_table, k_scales, v_scales)
+        self.q4, self.format, self.device = q4, CACHE_Q4 if q4 else CACHE_BF16, dev
+        self.num_pages, self.Hkv, self.page_size, self.d, self.B, self.max_pages = P, H, S, d, B, max_pages
+        none = _NO_STRIDES
+        self._c = CPagedCache(
+            self.format, P, H, S, d, B, max_pages, k.data_ptr(), v.data_ptr(), _live_strides(k, 4), _live_strides(v, 4),
+            k_scales.data_ptr() if q4 else None, v_scales.data_ptr() if q4 else None,
+            _live_strides(k_scales, 4) if q4 else none, _live_strides(v_scales, 4) if q4 else none,
+            page_table.data_ptr(), ts[0])
+        self._ref = ctypes.byref(self._c)
+
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    page_table = property(lambda self: self._tensors[2])
+    k_scales = property(lambda self: self._tensors[3])
+    v_scales = property(lambda self: self._tensors[4])
 
     @classmethod
     def empty(cls, num_pages, Hkv, page_size, d, page_table, q4=False):
@@ -652,18 +705,8 @@ class PagedCache:
         return cls(new(d // 2, torch.uint8), new(d // 2, torch.uint8), page_table,
                    new(d // 32, torch.bfloat16), new(d // 32, torch.bfloat16))
 
-    def c_struct(self):
-        c = CPagedCache()
-        c.format, c.num_pages, c.Hkv, c.page_size = self.format, self.num_pages, self.Hkv, self.page_size
-        c.d, c.B, c.max_pages = self.d, self.B, self.max_pages
-        c.k, c.v = self.k.data_ptr(), self.v.data_ptr()
-        c.k_strides, c.v_strides = _live_strides(self.k, 4), _live_strides(self.v, 4)
-        if self.q4:
-            c.k_scales, c.v_scales = self.k_scales.data_ptr(), self.v_scales.data_ptr()
-            c.k_scale_strides = _live_strides(self.k_scales, 4)
-            c.v_scale_strides = _live_strides(self.v_scales, 4)
-        c.page_table, c.page_table_stride = self.page_table.data_ptr(), self.page_table.stride(0)
-        return c
+
+_NO_STRIDES = _I4(0, 0, 0, 0)
 
 
 def _need_cache(cache):
@@ -671,11 +714,14 @@ def _need_cache(cache):
         raise TypeError(f"cache: expected a PagedCache, got {type(cache).__name__}")
 
 
-def _need_index(t, name, B, device):
+def _index(t, name, cache):
+    """Address of an int32 [B] tensor, or None."""
     import torch
 
-    if t is not None:
-        _need(t, name, (torch.int32,), (B,), device, contiguous=True)
+    if t is None:
+        return None
+    _want(t, name, torch.int32, (cache.B,), cache.device, contiguous=True)
+    return t.data_ptr()
 
 
 def paged_append(cache, k, v, start, count=None, rope_theta=10000.0, rope_mode=ROPE_FUSED, stream=None):
@@ -685,21 +731,18 @@ def paged_append(cache, k, v, start, count=None, rope_theta=10000.0, rope_mode=R
     import torch
 
     _need_cache(cache)
-    bf16, dev = (torch.bfloat16,), cache.device
-    _need(k, "k", bf16, ndim=4, dims="[B, Hkv, N, d]")
+    bf16, dev = torch.bfloat16, cache.device
+    if getattr(k, "dtype", None) is not bf16 or k.dim() != 4:
+        _need(k, "k", (bf16,), ndim=4, dims="[B, Hkv, N, d]")
     N = k.shape[2]
-    _need(k, "k", bf16, (cache.B, cache.Hkv, N, cache.d), dev)
-    _need(v, "v", bf16, (cache.B, cache.Hkv, N, cache.d), dev)
+    shape = (cache.B, cache.Hkv, N, cache.d)
+    _want(k, "k", bf16, shape, dev)
+    _want(v, "v", bf16, shape, dev)
     if start is None:
         raise TypeError("start: expected an int32 [B] tensor")
-    _need_index(start, "start", cache.B, dev)
-    _need_index(count, "count", cache.B, dev)
-    cc = cache.c_struct()
-    ctx, st = _launch_context(dev, stream)
-    with ctx:
-        _check(load().attnfuse_paged_append(
-            ctypes.byref(cc), _ptr(k), _live_strides(k, 4), _ptr(v), _live_strides(v, 4), _ptr(start),
-            _ptr(count), N, float(rope_theta), rope_mode, st))
+    _launch(load().attnfuse_paged_append,
+            (cache._ref, k.data_ptr(), _live_strides(k, 4), v.data_ptr(), _live_strides(v, 4),
+             _index(start, "start", cache), _index(count, "count", cache), N, rope_theta, rope_mode), dev, stream)
 
 
 def paged_gather(cache, start, count, N, k=None, v=None, stream=None):
@@ -708,20 +751,15 @@ def paged_gather(cache, start, count, N, k=None, v=None, stream=None):
     import torch
 
     _need_cache(cache)
-    bf16, dev = (torch.bfloat16,), cache.device
-    shape = (cache.B, cache.Hkv, int(N), cache.d)
-    k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
-    v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
-    _need(k, "k", bf16, shape, dev)
-    _need(v, "v", bf16, shape, dev)
-    _need_index(start, "start", cache.B, dev)
-    _need_index(count, "count", cache.B, dev)
-    cc = cache.c_struct()
-    ctx, st = _launch_context(dev, stream)
-    with ctx:
-        _check(load().attnfuse_paged_gather(
-            ctypes.byref(cc), _ptr(start), _ptr(count), _ptr(k), _live_strides(k, 4), _ptr(v),
-            _live_strides(v, 4), int(N), st))
+    bf16, dev, N = torch.bfloat16, cache.device, int(N)
+    shape = (cache.B, cache.Hkv, N, cache.d)
+    k = torch.empty(shape, dtype=bf16, device=dev) if k is None else k
+    v = torch.empty(shape, dtype=bf16, device=dev) if v is None else v
+    _want(k, "k", bf16, shape, dev)
+    _want(v, "v", bf16, shape, dev)
+    _launch(load().attnfuse_paged_gather,
+            (cache._ref, _index(start, "start", cache), _index(count, "count", cache), k.data_ptr(), _live_strides(k, 4),
+             v.data_ptr(), _live_strides(v, 4), N), dev, stream)
     return k, v
 
 
@@ -730,6 +768,19 @@ def paged_decode_workspace_size(Hq, Hkv, d, cache_format):
     n = ctypes.c_size_t()
     _check(load().attnfuse_paged_decode_workspace_size(Hq, Hkv, d, cache_format, ctypes.byref(n)))
     return n.value
+
+
+_paged_sizes = {}  # (device index, Hq, Hkv, d, format) -> workspace bytes
+
+
+def _paged_workspace_size(device, *key):
+    import torch
+
+    n = _paged_sizes.get((device.index,) + key)
+    if n is None:
+        with torch.cuda.device(device):
+            n = _paged_sizes[(device.index,) + key] = paged_decode_workspace_size(*key)
+    return n
 
 
 def paged_decode(q, cache, lens, scale=None, rope_theta=10000.0, rope_mode=ROPE_FUSED, window=0,
@@ -741,33 +792,35 @@ def paged_decode(q, cache, lens, scale=None, rope_theta=10000.0, rope_mode=ROPE_
     import torch
 
     _need_cache(cache)
-    bf16, f32, dev = (torch.bfloat16,), (torch.float32,), cache.device
-    _need(q, "q", bf16, ndim=3, dims="[B, Hq, d]")
+    bf16, f32, dev, B, d = torch.bfloat16, torch.float32, cache.device, cache.B, cache.d
+    if getattr(q, "dtype", None) is not bf16 or q.dim() != 3:
+        _need(q, "q", (bf16,), ndim=3, dims="[B, Hq, d]")
     Hq = q.shape[1]
-    _need(q, "q", bf16, (cache.B, Hq, cache.d), dev)
+    shape = (B, Hq, d)
+    _want(q, "q", bf16, shape, dev)
     if lens is None:
         raise TypeError("lens: expected an int32 [B] tensor")
-    _need_index(lens, "lens", cache.B, dev)
     if alibi_slopes is not None:
-        _need(alibi_slopes, "alibi_slopes", f32, (Hq,), dev, contiguous=True)
-    if scale is None:
-        scale = cache.d ** -0.5
+        _want(alibi_slopes, "alibi_slopes", f32, (Hq,), dev, contiguous=True)
+        alibi_slopes = alibi_slopes.data_ptr()
     if out is None:
-        out = torch.empty((cache.B, Hq, cache.d), dtype=torch.bfloat16, device=dev)
-    _need(out, "out", bf16, (cache.B, Hq, cache.d), dev)
-    if with_lse and lse is None:
-        lse = torch.empty((cache.B, Hq), dtype=torch.float32, device=dev)
-    if lse is not None:
-        _need(lse, "lse", f32, (cache.B, Hq), dev, contiguous=True)
-    cc = cache.c_struct()
-    ctx, st = _launch_context(dev, stream)
-    with ctx:
-        ws_n = paged_decode_workspace_size(Hq, cache.Hkv, cache.d, cache.format)
+        out = torch.empty(shape, dtype=bf16, device=dev)
+    else:
+        _want(out, "out", bf16, shape, dev)
+    if lse is None:
+        if with_lse:
+            lse = torch.empty((B, Hq), dtype=f32, device=dev)
+    else:
+        _want(lse, "lse", f32, (B, Hq), dev, contiguous=True)
+    ws_n = _paged_workspace_size(dev, Hq, cache.Hkv, d, cache.format)
+    if workspace is None:
+        ws = torch.empty(ws_n, dtype=torch.uint8, device=dev)
+    else:
         ws = _workspace(ws_n, dev, workspace)
-        _check(load().attnfuse_paged_decode(
-            ctypes.byref(cc), _ptr(q), _live_strides(q, 3), _ptr(lens), _ptr(out), _live_strides(out, 3),
-            _ptr(lse), Hq, float(scale), float(rope_theta), rope_mode, int(window), _ptr(alibi_slopes),
-            _ptr(ws), ws_n, st))
+    _launch(load().attnfuse_paged_decode,
+            (cache._ref, q.data_ptr(), _live_strides(q, 3), _index(lens, "lens", cache), out.data_ptr(),
+             _live_strides(out, 3), None if lse is None else lse.data_ptr(), Hq, d ** -0.5 if scale is None else scale,
+             rope_theta, rope_mode, window, alibi_slopes, ws.data_ptr(), ws_n), dev, stream)
     return out, lse
 
 

@@ -255,8 +255,6 @@ int encode_map_bhnd(CUtensorMap* m, const void* ptr, const int64_t st[4], int B,
   return encode_bhnd(m, ptr, st, B, H, N, d, name, box_rows);
 }
 
-RopeFreqs rope_freqs(int d, float theta) { return make_freqs(d, theta); }
-
 }  // namespace afx
 
 using namespace afx;

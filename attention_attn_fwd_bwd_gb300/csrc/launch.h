@@ -113,10 +113,9 @@ cudaError_t launch_wait_timeout(uint64_t limit_ns, int* status, cudaStream_t str
 int set_last_error(int code, const char* msg);
 // What the entry points of other translation units share with api.cu: the status word of the
 // current device, a bf16 tensor map of [B, H, N, d] (box (64, box_rows, 1, 1), 128-byte
-// swizzle), the frequencies of a theta. They return an attnfuse_status and set its message.
+// swizzle). They return an attnfuse_status and set its message.
 int current_status_word(int** status);
 int encode_map_bhnd(CUtensorMap* m, const void* ptr, const int64_t st[4], int B, int H, int N, int d,
                     const char* name, int box_rows);
-RopeFreqs rope_freqs(int d, float theta);
 
 }  // namespace afx

@@ -19,6 +19,7 @@
 #include <cstdint>
 
 #include "common.cuh"
+#include "turn_table.cuh"
 
 namespace afx {
 
@@ -41,6 +42,11 @@ struct PagedDev {
   int B, Hkv;
 };
 
+// theta_i / (2 pi) for i < d/2 as the sum of three floats (all of a double).
+struct PagedFreqs {
+  float f1[64], f2[64], f3[64];
+};
+
 // Launch parameters. Strides of the dense sides are in bytes, the innermost is one element.
 struct PagedAppendParams {
   PagedDev cache;
@@ -49,8 +55,8 @@ struct PagedAppendParams {
   const int32_t *first, *count;     // [B]; count may be null: every sequence has N rows
   int N;
   int64_t rows;                     // B * N
-  int heads_per_thread;             // set by the launcher
-  RopeFreqs freqs;
+  int hb;                           // heads of a block (set by the launcher)
+  PagedFreqs freqs;
   int* status;
 };
 struct PagedGatherParams {
@@ -84,7 +90,7 @@ struct PagedDecodeParams {
   float2* part_ml;                  // (max in log2 units, sum)
   int ctas, head_rows;              // query heads per item
   int chunks, items;                // items per KV head, and per sequence
-  RopeFreqs freqs;
+  PagedFreqs freqs;
   int* status;
 };
 constexpr int kPagedMaxCtas = 1024;
@@ -119,61 +125,85 @@ __device__ __forceinline__ int q4_place(int r, int slot) {
 //
 // A 4-bit code jumps by a whole step where a value crosses a border between two codes, so the
 // rotated key is defined as the exact R_p k rounded to fp32 and then to bf16, whatever
-// computes it. The fast path is fp32: (cos, sin) within 2^-22.9 (sincospif and the residual of
-// the reduced angle), two roundings on top: |error| < 2^-21.5 (|x_lo| + |x_hi|). Where that
-// interval holds a border between two bf16 values (about 3 elements in 10^4) the element is
-// computed again in fp64.
+// computes it. fp32 alone would move about one element in 10^6 across such a border, and the
+// GPU's fp64 units are few (a first version recomputed doubtful elements in fp64: 126 us for
+// 18.5k rows of 8 heads, d = 128, against 20 us of traffic). So angles and products are carried as the
+// sum of two floats, to about 2^-37: 55 instructions per angle, shared by the heads of a row, and
+// 16 packed ones per pair and head.
 // ---------------------------------------------------------------------------------------------
 
-// (cos, sin) of 2 pi * pos * (hi + lo) as rope_cossin, with the rounding of the reduced angle
-// put back: the residual rl (turns) turns (c, s) by 2 pi rl to first order.
-__device__ __forceinline__ void rope_cossin_fine(float pos, float hi, float lo, float* c, float* s) {
-  const float prod = __fmul_rn(pos, hi);
-  const float err = __fmaf_rn(pos, hi, -prod);
-  const float frac = __fsub_rn(prod, rintf(prod));
-  const float low = __fmaf_rn(pos, lo, err);
-  const float r = __fadd_rn(frac, low);
-  const float bb = __fsub_rn(r, frac);
-  const float rl = __fadd_rn(__fsub_rn(frac, __fsub_rn(r, bb)), __fsub_rn(low, bb));
-  float c0, s0;
-  sincospif(__fmul_rn(2.0f, r), &s0, &c0);
-  const float dl = __fmul_rn(6.283185307179586f, rl);
-  *c = __fmaf_rn(-s0, dl, c0);
-  *s = __fmaf_rn(c0, dl, s0);
+// (cos, sin) of 2 pi pos (f1 + f2 + f3), each as hi + lo. The angle in turns is reduced exactly,
+// its nearest multiple of 1/256 looked up (table-driven reduction as in Tang, "Table-driven
+// implementation of the exponential function", 1989) and the rest, |d| <= 2 pi / 512, added by
+// the angle-sum formulas with Taylor series to d^5.
+__device__ __forceinline__ float4 turn_cossin(float pos, float f1, float f2, float f3) {
+  const float p1 = __fmul_rn(pos, f1), e1 = __fmaf_rn(pos, f1, -p1);
+  const float frac = __fsub_rn(p1, rintf(p1));
+  const float p2 = __fmul_rn(pos, f2), e2 = __fmaf_rn(pos, f2, -p2);
+  const float a = __fadd_rn(e1, p2), ab = __fsub_rn(a, e1);
+  const float ea = __fadd_rn(__fsub_rn(e1, __fsub_rn(a, ab)), __fsub_rn(p2, ab));
+  const float r = __fadd_rn(frac, a), rb = __fsub_rn(r, frac);
+  const float er = __fadd_rn(__fsub_rn(frac, __fsub_rn(r, rb)), __fsub_rn(a, rb));
+  const float lo = __fadd_rn(__fadd_rn(er, ea), __fmaf_rn(pos, f3, e2));
+  const float kf = rintf(__fmul_rn(r, 256.0f));
+  const float rs = __fmaf_rn(kf, -1.0f / 256.0f, r);  // exact
+  const int k = static_cast<int>(kf);
+  const float4 T = __ldg(kTurn256 + (k & 63));
+  constexpr float kTwoPiHi = 0x1.921fb6p+2f, kTwoPiLo = -0x1.777a5cp-23f;
+  const float dh = __fmul_rn(rs, kTwoPiHi);
+  const float dl = __fmaf_rn(rs, kTwoPiLo, __fmaf_rn(lo, kTwoPiHi, __fmaf_rn(rs, kTwoPiHi, -dh)));
+  const float d2 = __fmul_rn(dh, dh);
+  const float u = __fmul_rn(d2, __fmaf_rn(d2, 1.0f / 24.0f, -0.5f));                              // cos d - 1
+  const float v = __fmaf_rn(__fmul_rn(dh, d2), __fmaf_rn(d2, 1.0f / 120.0f, -1.0f / 6.0f), dl);  // sin d - dh
+  const float pc = __fmul_rn(T.z, dh), pce = __fmaf_rn(T.z, dh, -pc);
+  float tc = __fmaf_rn(T.x, u, T.y);
+  tc = __fmaf_rn(-T.z, v, tc);
+  tc = __fmaf_rn(-T.w, dh, tc);
+  const float ch = __fsub_rn(T.x, pc);
+  const float cl = __fadd_rn(__fsub_rn(__fsub_rn(T.x, ch), pc), __fsub_rn(tc, pce));
+  const float ps = __fmul_rn(T.x, dh), pse = __fmaf_rn(T.x, dh, -ps);
+  float ts = __fmaf_rn(T.z, u, T.w);
+  ts = __fmaf_rn(T.x, v, ts);
+  ts = __fmaf_rn(T.y, dh, ts);
+  const float sh = __fadd_rn(T.z, ps);
+  const float sl = __fadd_rn(__fsub_rn(ps, __fsub_rn(sh, T.z)), __fadd_rn(ts, pse));
+  // quarter turns: (c, s) -> (-s, c) -> (-c, -s) -> (s, -c)
+  const int q = (k >> 6) & 3;
+  const float4 w = (q & 1) ? make_float4(-sh, -sl, ch, cl) : make_float4(ch, cl, sh, sl);
+  return (q & 2) ? make_float4(-w.x, -w.y, -w.z, -w.w) : w;
 }
 
-// One pair in fp64, rounded to fp32.
-static __device__ __noinline__ void rot_pair_f64(float xl, float xh, float pos, float hi, float lo, float* yl,
-                                          float* yh) {
-  const double p = pos;
-  double t = p * static_cast<double>(hi);  // 24 x 24 bits: exact
-  t -= rint(t);
-  t += p * static_cast<double>(lo);
-  double s, c;
-  sincospi(2.0 * t, &s, &c);
-  *yl = static_cast<float>(static_cast<double>(xl) * c - static_cast<double>(xh) * s);
-  *yh = static_cast<float>(static_cast<double>(xh) * c + static_cast<double>(xl) * s);
+// x c + y s of two lanes with c, s as hi + lo and nx = -x, ny = -y: h + t, h the rounded sum of
+// the products, t what all roundings lost.
+__device__ __forceinline__ void dot2_exact(uint64_t x, uint64_t nx, uint64_t y, uint64_t ny, uint64_t ch, uint64_t cl,
+                                           uint64_t sh, uint64_t sl, uint64_t& h, uint64_t& t) {
+  const uint64_t m1 = f2_pack(-1.0f, -1.0f);
+  const uint64_t p1 = mul2(x, ch), p2 = mul2(y, sh);
+  const uint64_t n = add2(fma2(nx, ch, p1), fma2(ny, sh, p2));  // minus the products' errors
+  h = add2(p1, p2);
+  const uint64_t bb = fma2(p1, m1, h);
+  const uint64_t er = add2(fma2(fma2(bb, m1, h), m1, p1), fma2(bb, m1, p2));
+  t = fma2(n, m1, add2(fma2(y, sl, mul2(x, cl)), er));
 }
 
-// Two consecutive pairs (i, i + 1), each word a bf16x2: rotated and rounded to bf16.
-__device__ __forceinline__ void rot_word_exact(uint32_t& lo, uint32_t& hi, const float (&c)[2],
-                                               const float (&s)[2], float pos, const RopeFreqs& f, int i) {
-  const float xl0 = bf16lo_to_f32(lo), xl1 = bf16hi_to_f32(lo);
-  const float xh0 = bf16lo_to_f32(hi), xh1 = bf16hi_to_f32(hi);
-  float yl0, yh0, yl1, yh1;
-  rot_pair(xl0, xh0, c[0], s[0], yl0, yh0);
-  rot_pair(xl1, xh1, c[1], s[1], yl1, yh1);
-  const float e0 = 3.4e-7f * (fabsf(xl0) + fabsf(xh0));  // 2^-21.5
-  const float e1 = 3.4e-7f * (fabsf(xl1) + fabsf(xh1));
-  const uint32_t wl = pack_bf16x2(yl0 + e0, yl1 + e1), wh = pack_bf16x2(yh0 + e0, yh1 + e1);
-  if (wl != pack_bf16x2(yl0 - e0, yl1 - e1) || wh != pack_bf16x2(yh0 - e0, yh1 - e1)) {
-    rot_pair_f64(xl0, xh0, pos, f.hi[i], f.lo[i], &yl0, &yh0);
-    rot_pair_f64(xl1, xh1, pos, f.hi[i + 1], f.lo[i + 1], &yl1, &yh1);
-    lo = pack_bf16x2(yl0, yl1);
-    hi = pack_bf16x2(yh0, yh1);
-  } else {
-    lo = wl;
-    hi = wh;
+// Two consecutive pairs, each word a bf16x2, rotated by the two angles packed in ch .. sl.
+__device__ __forceinline__ void rot_word_exact(uint32_t& lo, uint32_t& hi, uint64_t ch, uint64_t cl, uint64_t sh,
+                                               uint64_t sl) {
+  constexpr uint64_t kSigns = 0x8000000080000000ull;
+  const uint64_t xl = bf16x2_to_f2(lo), xh = bf16x2_to_f2(hi);
+  const uint64_t nl = xl ^ kSigns, nh = xh ^ kSigns;
+  uint64_t h0, t0, h1, t1;
+  dot2_exact(xl, nl, nh, xh, ch, cl, sh, sl, h0, t0);  // xl c - xh s
+  dot2_exact(xh, nh, xl, nl, ch, cl, sh, sl, h1, t1);  // xh c + xl s
+  const uint64_t y0 = add2(h0, t0), y1 = add2(h1, t1);
+  lo = pack_bf16x2(f2_lo(y0), f2_hi(y0));
+  hi = pack_bf16x2(f2_lo(y1), f2_hi(y1));
+  const uint32_t big = __vmaxu2(lo & 0x7FFF7FFFu, hi & 0x7FFF7FFFu);
+  if (big >= 0x7F800000u || (big & 0xFFFFu) >= 0x7F80u) {
+    // an infinity makes the error terms NaN: the rounded sum itself is the value
+    auto pick = [](float y, float h) { return y == y ? y : h; };
+    lo = pack_bf16x2(pick(f2_lo(y0), f2_lo(h0)), pick(f2_hi(y0), f2_hi(h0)));
+    hi = pack_bf16x2(pick(f2_lo(y1), f2_lo(h1)), pick(f2_hi(y1), f2_hi(h1)));
   }
 }
 

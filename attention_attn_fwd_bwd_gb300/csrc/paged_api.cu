@@ -116,6 +116,19 @@ int check_rope(int* mode, float theta) {
   return ATTNFUSE_OK;
 }
 
+PagedFreqs paged_freqs(int d, float theta) {
+  PagedFreqs f;
+  memset(&f, 0, sizeof(f));
+  const double two_pi = 6.283185307179586476925286766559;
+  for (int i = 0; i < d / 2; ++i) {
+    double x = std::pow((double)theta, -2.0 * i / d) / two_pi;
+    x -= (f.f1[i] = (float)x);
+    x -= (f.f2[i] = (float)x);
+    f.f3[i] = (float)x;
+  }
+  return f;
+}
+
 int check_index(const int32_t* p, bool need, const char* name) {
   if (!p && need) return fail(ATTNFUSE_ERR_INVALID_ARG, "%s is NULL", name);
   if (!aligned(p, 4)) return fail(ATTNFUSE_ERR_INVALID_ARG, "%s is not 4-byte aligned", name);
@@ -159,7 +172,7 @@ attnfuse_status attnfuse_paged_append(const attnfuse_paged_cache* cache, const v
   p.count = count;
   p.N = N;
   p.rows = (int64_t)cache->B * N;
-  if (mode == ATTNFUSE_ROPE_FUSED) p.freqs = rope_freqs(cache->d, rope_theta);
+  if (mode == ATTNFUSE_ROPE_FUSED) p.freqs = paged_freqs(cache->d, rope_theta);
   return done(launch_paged_append(p, cache->d, cache->format, mode == ATTNFUSE_ROPE_FUSED, stream),
               "paged append launch");
 }
@@ -239,7 +252,7 @@ attnfuse_status attnfuse_paged_decode(const attnfuse_paged_cache* cache, const v
   p.slopes = alibi_slopes;
   p.rope = mode == ATTNFUSE_ROPE_FUSED;
   p.scale_log2 = scale * kLog2e;
-  if (p.rope) p.freqs = rope_freqs(cache->d, rope_theta);
+  if (p.rope) p.freqs = paged_freqs(cache->d, rope_theta);
   p.workspace = workspace;
   p.frag_rows = paged_frag_rows(cache->page_size);
   if (cache->format == ATTNFUSE_CACHE_BF16) {

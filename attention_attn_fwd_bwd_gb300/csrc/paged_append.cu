@@ -1,9 +1,7 @@
 // Writing rows into a paged cache (with the rotation of K and, for q4, the quantisation on the
 // way) and reading them back out as dense bf16 rows.
 //
-// Both are bound by HBM: a row of K and V is read once and written once; prompts of 18.5k rows
-// (Hkv = 8, d = 128) move 151 MB. A thread keeps its part of the row for a run of heads, so that
-// the D/2 angles of a position are computed once per run and not once per head.
+// Both are bound by HBM: a row of K and V is read once and written once.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -49,61 +47,113 @@ __device__ __forceinline__ bool find_row(const PagedDev& c, int b, int n, int fi
   return r->page >= 0;
 }
 
+// A block covers rb rows x hb heads, tpr threads for each; the angles of its rows are computed
+// once, by all threads, into shared memory: angle (k, t) of a row is that of thread t's k-th pair.
+struct Place {
+  int64_t row;
+  int t, rr, h;  // thread of the row, row of the block, head
+};
+template <int TPR>
+__device__ __forceinline__ Place place_of(const PagedAppendParams& p) {
+  const int rb = kThreads / TPR / p.hb;
+  Place w;
+  w.t = threadIdx.x % TPR;
+  w.rr = threadIdx.x / TPR % rb;
+  w.row = static_cast<int64_t>(blockIdx.x) * rb + w.rr;
+  w.h = blockIdx.y * p.hb + threadIdx.x / TPR / rb;
+  return w;
+}
+
+// Pair that angle slot (k, t) of a row stands for.
+template <int D, int TPR, bool Q4>
+__device__ __forceinline__ int pair_of(int k, int t) {
+  return Q4 ? 32 * (k / 4) + 4 * t + k % 4 : 8 * t + k;
+}
+
+template <int D, int TPR, bool Q4>
+__device__ __forceinline__ void block_angles(const PagedAppendParams& p, float4* ang) {
+  constexpr int K = D / 2 / TPR;  // pairs per thread of a row
+  const int rb = kThreads / TPR / p.hb;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rb;
+  for (int i = threadIdx.x; i < rb * (D / 2); i += kThreads) {
+    const int64_t row = row0 + i / (D / 2);
+    if (row >= p.rows) break;
+    const int j = i % (D / 2), b = static_cast<int>(row / p.N), n = static_cast<int>(row - static_cast<int64_t>(b) * p.N);
+    if (p.count && n >= __ldg(p.count + b)) continue;
+    const int64_t pos = static_cast<int64_t>(__ldg(p.first + b)) + n;
+    if (pos < 0 || pos >= p.cache.cap) continue;
+    const int i0 = pair_of<D, TPR, Q4>(j / TPR, j % TPR);
+    ang[i] = turn_cossin(static_cast<float>(pos), p.freqs.f1[i0], p.freqs.f2[i0], p.freqs.f3[i0]);
+  }
+  static_assert(K * TPR == D / 2, "pairs");
+  __syncthreads();
+}
+
+// The two angles of pairs k, k + 1 of thread t of a row, packed.
+template <int D, int TPR>
+__device__ __forceinline__ void two_angles(const float4* ang, int rr, int k, int t, uint64_t (&w)[4]) {
+  const float4 a = ang[rr * (D / 2) + k * TPR + t], b = ang[rr * (D / 2) + (k + 1) * TPR + t];
+  w[0] = f2_pack(a.x, b.x);
+  w[1] = f2_pack(a.y, b.y);
+  w[2] = f2_pack(a.z, b.z);
+  w[3] = f2_pack(a.w, b.w);
+}
+
 // ---------------------------------------------------------------------------------------------
 // bf16: thread = 8 pairs (x_i, x_{i + D/2}) of a row, two 16-byte chunks
 // ---------------------------------------------------------------------------------------------
 template <int D, bool ROPE>
 __global__ void __launch_bounds__(kThreads) append_bf16_kernel(const __grid_constant__ PagedAppendParams p) {
   constexpr int CP = D / 16;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / CP) + threadIdx.x / CP;
-  const int ch = threadIdx.x % CP;
-  if (row >= p.rows) return;
-  const int b = static_cast<int>(row / p.N), n = static_cast<int>(row - static_cast<int64_t>(b) * p.N);
-  if (n >= live_rows(p.count, b, p.N, p.status)) return;
+  extern __shared__ float4 ang[];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Place w = place_of<CP>(p);
+  const bool in = w.row < p.rows && w.h < p.cache.Hkv;
+  const int b = in ? static_cast<int>(w.row / p.N) : 0;
+  const int n = in ? static_cast<int>(w.row - static_cast<int64_t>(b) * p.N) : 0;
   RowAt r;
-  if (!find_row(p.cache, b, n, __ldg(p.first + b), p.status, &r)) return;
-  float c[8], s[8];
-  if (ROPE) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      rope_cossin_fine(r.pos, p.freqs.hi[ch * 8 + e], p.freqs.lo[ch * 8 + e], &c[e], &s[e]);
+  const bool live = in && n < live_rows(p.count, b, p.N, p.status) &&
+                    find_row(p.cache, b, n, __ldg(p.first + b), p.status, &r);
+  uint4 lo, hi, v0, v1;
+  if (live) {
+    const uint8_t* k = p.k + b * p.k_sb + n * p.k_sn + w.h * p.k_sh + w.t * 16;
+    const uint8_t* v = p.v + b * p.v_sb + n * p.v_sn + w.h * p.v_sh + w.t * 16;
+    lo = __ldg(reinterpret_cast<const uint4*>(k));
+    hi = __ldg(reinterpret_cast<const uint4*>(k + D));
+    v0 = __ldg(reinterpret_cast<const uint4*>(v));
+    v1 = __ldg(reinterpret_cast<const uint4*>(v + D));
   }
-  const int h0 = blockIdx.y * p.heads_per_thread, h1 = min(p.cache.Hkv, h0 + p.heads_per_thread);
-  const uint8_t* k = p.k + b * p.k_sb + n * p.k_sn + ch * 16;
-  const uint8_t* v = p.v + b * p.v_sb + n * p.v_sn + ch * 16;
-  uint8_t* kd = p.cache.k + r.page * p.cache.k_sp + r.slot * p.cache.k_st + ch * 16;
-  uint8_t* vd = p.cache.v + r.page * p.cache.v_sp + r.slot * p.cache.v_st + ch * 16;
-#pragma unroll 2
-  for (int h = h0; h < h1; ++h) {
-    uint4 lo = __ldg(reinterpret_cast<const uint4*>(k + h * p.k_sh));
-    uint4 hi = __ldg(reinterpret_cast<const uint4*>(k + h * p.k_sh + D));
-    const uint4 v0 = __ldg(reinterpret_cast<const uint4*>(v + h * p.v_sh));
-    const uint4 v1 = __ldg(reinterpret_cast<const uint4*>(v + h * p.v_sh + D));
+  if (ROPE) block_angles<D, CP, false>(p, ang);
+  if (live) {
     if (ROPE) {
       uint32_t* L = reinterpret_cast<uint32_t*>(&lo);
       uint32_t* H = reinterpret_cast<uint32_t*>(&hi);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float cw[2] = {c[2 * w], c[2 * w + 1]}, sw[2] = {s[2 * w], s[2 * w + 1]};
-        rot_word_exact(L[w], H[w], cw, sw, r.pos, p.freqs, ch * 8 + 2 * w);
+      for (int q = 0; q < 4; ++q) {
+        uint64_t a[4];
+        two_angles<D, CP>(ang, w.rr, 2 * q, w.t, a);
+        rot_word_exact(L[q], H[q], a[0], a[1], a[2], a[3]);
       }
     }
-    *reinterpret_cast<uint4*>(kd + h * p.cache.k_sh) = lo;
-    *reinterpret_cast<uint4*>(kd + h * p.cache.k_sh + D) = hi;
-    *reinterpret_cast<uint4*>(vd + h * p.cache.v_sh) = v0;
-    *reinterpret_cast<uint4*>(vd + h * p.cache.v_sh + D) = v1;
+    uint8_t* kd = p.cache.k + r.page * p.cache.k_sp + r.slot * p.cache.k_st + w.h * p.cache.k_sh + w.t * 16;
+    uint8_t* vd = p.cache.v + r.page * p.cache.v_sp + r.slot * p.cache.v_st + w.h * p.cache.v_sh + w.t * 16;
+    *reinterpret_cast<uint4*>(kd) = lo;
+    *reinterpret_cast<uint4*>(kd + D) = hi;
+    *reinterpret_cast<uint4*>(vd) = v0;
+    *reinterpret_cast<uint4*>(vd + D) = v1;
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------------------------
-// q4: 8 threads per row; thread r holds elements 32g + 4r .. + 3 of every group g, which are
-// whole pairs (group g with group g + G/2) and exactly chunk r of the stored row
+// q4: 8 threads per row; thread t holds elements 32g + 4t .. + 3 of every group g, which are
+// whole pairs (group g with group g + G/2) and exactly chunk t of the stored row
 // ---------------------------------------------------------------------------------------------
 
 // 4 elements (two bf16x2 words) with reciprocal step inv -> 4 nibbles, lowest first.
 // x and the step have 8 significant bits each, so |x| / s is a tie k + 1/2 or at least 2^-12
-// (relative) away from one; the product with the reciprocal is within 2^-23, and the factor
-// 1 + 2^-20 puts ties, and only them, on the far side.
+// (relative) away from one; the product with the reciprocal (1 ulp) is within 2^-22, and the
+// factor 1 + 2^-20 puts ties, and only them, on the far side.
 __device__ __forceinline__ uint32_t q4_codes(uint32_t w0, uint32_t w1, float inv) {
   const float x[4] = {bf16lo_to_f32(w0), bf16hi_to_f32(w0), bf16lo_to_f32(w1), bf16hi_to_f32(w1)};
   uint32_t out = 0;
@@ -117,98 +167,100 @@ __device__ __forceinline__ uint32_t q4_codes(uint32_t w0, uint32_t w1, float inv
   return out;
 }
 
-// Quantises one row: w[g] = this thread's two words of group g. Returns the chunk; thread 0 of
-// the row also gets the scales.
+// Largest magnitudes of a row's groups as bf16 bits (their integers order like the values, NaN
+// above infinity), two groups per word, the same in all 8 threads of the row.
 template <int G>
-__device__ __forceinline__ void q4_row(const uint2 (&w)[G], uint32_t (&chunk)[G / 2], uint32_t (&scales)[G / 2]) {
+__device__ __forceinline__ void q4_amax(const uint2 (&w)[G], uint32_t (&a)[G / 2]) {
 #pragma unroll
   for (int q = 0; q < G / 2; ++q) {
-    // largest magnitudes of groups 2q and 2q + 1 as bf16 bits (their integers order like the
-    // values, NaN above infinity), in one word
-    uint32_t a = __vmaxu2(w[2 * q].x & 0x7FFF7FFFu, w[2 * q].y & 0x7FFF7FFFu);
-    uint32_t b = __vmaxu2(w[2 * q + 1].x & 0x7FFF7FFFu, w[2 * q + 1].y & 0x7FFF7FFFu);
-    a = __vmaxu2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+    const uint32_t x = __vmaxu2(w[2 * q].x & 0x7FFF7FFFu, w[2 * q].y & 0x7FFF7FFFu);
+    const uint32_t y = __vmaxu2(w[2 * q + 1].x & 0x7FFF7FFFu, w[2 * q + 1].y & 0x7FFF7FFFu);
+    a[q] = __vmaxu2(__byte_perm(x, y, 0x5410), __byte_perm(x, y, 0x7632));
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) a = __vmaxu2(a, __shfl_xor_sync(0xffffffffu, a, o));
-    chunk[q] = 0;
-    scales[q] = 0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t bits = i ? a >> 16 : a & 0xFFFFu;
-      const float amax = __uint_as_float(bits << 16);
-      uint32_t s = __bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(amax, 7.0f)));
-      float inv = __fdiv_rn(1.0f, __uint_as_float(s << 16));
-      if (amax < 0x1p-96f) s = 0, inv = 0.0f;         // reads back as zeros
-      if (bits >= 0x7F80u) s = 0x7FC0u, inv = 0.0f;   // an infinity or a NaN: reads back as NaN
-      // (inf * 0 and NaN * 0 are NaN, which fminf turns into 7: harmless under a NaN scale)
-      chunk[q] |= q4_codes(w[2 * q + i].x, w[2 * q + i].y, inv) << (16 * i);
-      scales[q] |= s << (16 * i);
-    }
+    for (int o = 1; o < 8; o <<= 1) a[q] = __vmaxu2(a[q], __shfl_xor_sync(0xffffffffu, a[q], o));
   }
 }
 
 template <int D, bool ROPE>
 __global__ void __launch_bounds__(kThreads) append_q4_kernel(const __grid_constant__ PagedAppendParams p) {
   constexpr int G = D / kQ4Group;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / 8) + threadIdx.x / 8;
-  const int t = threadIdx.x % 8;
-  // rows without work stay for the shuffles
-  const bool in = row < p.rows;
-  const int b = in ? static_cast<int>(row / p.N) : 0;
-  const int n = in ? static_cast<int>(row - static_cast<int64_t>(b) * p.N) : 0;
+  extern __shared__ float4 ang[];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Place w = place_of<8>(p);
+  const bool in = w.row < p.rows && w.h < p.cache.Hkv;
+  const int b = in ? static_cast<int>(w.row / p.N) : 0;
+  const int n = in ? static_cast<int>(w.row - static_cast<int64_t>(b) * p.N) : 0;
   RowAt r = {};
   const bool live = in && n < live_rows(p.count, b, p.N, p.status) &&
                     find_row(p.cache, b, n, __ldg(p.first + b), p.status, &r);
-  if (!__any_sync(0xffffffffu, live)) return;
-  float c[G / 2][4], s[G / 2][4];
-  if (ROPE) {
+  uint2 x[2][G];  // K, V
 #pragma unroll
-    for (int g = 0; g < G / 2; ++g)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        rope_cossin_fine(r.pos, p.freqs.hi[32 * g + 4 * t + e], p.freqs.lo[32 * g + 4 * t + e], &c[g][e],
-                         &s[g][e]);
-  }
-  const int h0 = blockIdx.y * p.heads_per_thread, h1 = min(p.cache.Hkv, h0 + p.heads_per_thread);
-  const uint8_t* k = p.k + b * p.k_sb + n * p.k_sn + t * 8;
-  const uint8_t* v = p.v + b * p.v_sb + n * p.v_sn + t * 8;
-  const int64_t at = static_cast<int64_t>(r.slot) * (D / 2) + q4_place<D>(t, r.slot) * (D / 16);
-  uint8_t* kd = p.cache.k + r.page * p.cache.k_sp + at;
-  uint8_t* vd = p.cache.v + r.page * p.cache.v_sp + at;
-  uint8_t* ksd = p.cache.ks + r.page * p.cache.ks_sp + r.slot * (D / 16);
-  uint8_t* vsd = p.cache.vs + r.page * p.cache.vs_sp + r.slot * (D / 16);
-  for (int h = h0; h < h1; ++h) {
-    uint2 kw[G], vw[G];
+  for (int g = 0; g < G; ++g) x[0][g] = x[1][g] = make_uint2(0, 0);
+  if (live) {
+    const uint8_t* k = p.k + b * p.k_sb + n * p.k_sn + w.h * p.k_sh + w.t * 8;
+    const uint8_t* v = p.v + b * p.v_sb + n * p.v_sn + w.h * p.v_sh + w.t * 8;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      kw[g] = live ? __ldg(reinterpret_cast<const uint2*>(k + h * p.k_sh + g * 64)) : make_uint2(0, 0);
-      vw[g] = live ? __ldg(reinterpret_cast<const uint2*>(v + h * p.v_sh + g * 64)) : make_uint2(0, 0);
+      x[0][g] = __ldg(reinterpret_cast<const uint2*>(k + g * 64));
+      x[1][g] = __ldg(reinterpret_cast<const uint2*>(v + g * 64));
     }
-    if (ROPE) {
+  }
+  if (ROPE) {
+    block_angles<D, 8, true>(p, ang);
+    if (live) {
 #pragma unroll
       for (int g = 0; g < G / 2; ++g) {
-        const float c0[2] = {c[g][0], c[g][1]}, s0[2] = {s[g][0], s[g][1]};
-        const float c1[2] = {c[g][2], c[g][3]}, s1[2] = {s[g][2], s[g][3]};
-        rot_word_exact(kw[g].x, kw[g + G / 2].x, c0, s0, r.pos, p.freqs, 32 * g + 4 * t);
-        rot_word_exact(kw[g].y, kw[g + G / 2].y, c1, s1, r.pos, p.freqs, 32 * g + 4 * t + 2);
-      }
-    }
-    uint32_t chunk[G / 2], scales[G / 2];
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      q4_row<G>(which ? vw : kw, chunk, scales);
-      uint8_t* dst = which ? vd + h * p.cache.v_sh : kd + h * p.cache.k_sh;
-      uint8_t* sd = which ? vsd + h * p.cache.vs_sh : ksd + h * p.cache.ks_sh;
-      if (!live) continue;
-      if constexpr (G == 4) {
-        *reinterpret_cast<uint2*>(dst) = make_uint2(chunk[0], chunk[1]);
-        if (t == 0) *reinterpret_cast<uint2*>(sd) = make_uint2(scales[0], scales[1]);
-      } else {
-        *reinterpret_cast<uint32_t*>(dst) = chunk[0];
-        if (t == 0) *reinterpret_cast<uint32_t*>(sd) = scales[0];
+        uint64_t a[4];
+        two_angles<D, 8>(ang, w.rr, 4 * g, w.t, a);
+        rot_word_exact(x[0][g].x, x[0][g + G / 2].x, a[0], a[1], a[2], a[3]);
+        two_angles<D, 8>(ang, w.rr, 4 * g + 2, w.t, a);
+        rot_word_exact(x[0][g].y, x[0][g + G / 2].y, a[0], a[1], a[2], a[3]);
       }
     }
   }
+  // Steps: thread t finds the step of group t % G, of K (t < G) or V, stores it, and hands its
+  // reciprocal to the row's other threads. amax / 7 is never a tie of bf16 (or is exact), and at
+  // least 2^-12 (relative) away from one, so the product with 1/7 rounds to the same step.
+  uint32_t am[2][G / 2];
+  q4_amax<G>(x[0], am[0]);
+  q4_amax<G>(x[1], am[1]);
+  const int mine = w.t % (2 * G);
+  uint32_t bits = 0;
+#pragma unroll
+  for (int j = 0; j < 2 * G; ++j)
+    if (mine == j) bits = (am[j / G][(j % G) / 2] >> (16 * (j & 1))) & 0xFFFFu;
+  const float amax = __uint_as_float(bits << 16);
+  uint32_t s = __bfloat16_as_ushort(__float2bfloat16_rn(amax * (1.0f / 7.0f)));
+  float inv;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(__uint_as_float(s << 16)));
+  if (amax < 0x1p-96f) s = 0, inv = 0.0f;        // reads back as zeros
+  if (bits >= 0x7F80u) s = 0x7FC0u, inv = 0.0f;  // an infinity or a NaN: reads back as NaN
+  // (inf * 0 and NaN * 0 are NaN, which fminf turns into 7: harmless under a NaN step)
+  uint32_t code[2][G];
+  const int row0 = threadIdx.x & 24;  // the row's first lane
+#pragma unroll
+  for (int which = 0; which < 2; ++which)
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+      code[which][g] = q4_codes(x[which][g].x, x[which][g].y, __shfl_sync(0xffffffffu, inv, row0 + which * G + g));
+  if (live) {
+    const int64_t at = static_cast<int64_t>(r.slot) * (D / 2) + q4_place<D>(w.t, r.slot) * (D / 16);
+    uint8_t* kd = p.cache.k + r.page * p.cache.k_sp + w.h * p.cache.k_sh + at;
+    uint8_t* vd = p.cache.v + r.page * p.cache.v_sp + w.h * p.cache.v_sh + at;
+    if constexpr (G == 4) {
+      *reinterpret_cast<uint2*>(kd) = make_uint2(code[0][0] | code[0][1] << 16, code[0][2] | code[0][3] << 16);
+      *reinterpret_cast<uint2*>(vd) = make_uint2(code[1][0] | code[1][1] << 16, code[1][2] | code[1][3] << 16);
+    } else {
+      *reinterpret_cast<uint32_t*>(kd) = code[0][0] | code[0][1] << 16;
+      *reinterpret_cast<uint32_t*>(vd) = code[1][0] | code[1][1] << 16;
+    }
+    if (w.t < 2 * G) {
+      uint8_t* sd = w.t < G ? p.cache.ks + r.page * p.cache.ks_sp + w.h * p.cache.ks_sh
+                            : p.cache.vs + r.page * p.cache.vs_sp + w.h * p.cache.vs_sh;
+      *reinterpret_cast<uint16_t*>(sd + r.slot * (D / 16) + (w.t % G) * 2) = static_cast<uint16_t>(s);
+    }
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -270,22 +322,31 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
   }
 }
 
-// Heads per thread: a run of heads shares one row's lookup and angles (8 angles cost about as
-// much as 4 heads), but the launch should still fill the GPU's thread slots.
-int heads_per_thread(int64_t rows, int tpr, int Hkv) {
-  const int64_t want = 152 * 1024;
-  const int64_t h = rows * tpr * Hkv / want;
+// Heads per thread of the gather: a run of heads shares one row's lookup, but the launch should
+// still fill the GPU's thread slots.
+int gather_heads(int64_t rows, int tpr, int Hkv) {
+  const int64_t h = rows * tpr * Hkv / (152 * 1024);
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(h, std::min(Hkv, 8))));
+}
+
+// Heads per block of the append: angles (about 2.6 times a row-head's other work, per row) are
+// shared by the block's heads, heads behind the last one idle.
+int append_heads(int Hkv) {
+  int best = 1;
+  double cost = 1e30;
+  for (int hb = 8; hb >= 1; hb /= 2) {
+    const double c = (Hkv + hb - 1) / hb * hb * (1.0 + 2.6 / hb);
+    if (c < cost) cost = c, best = hb;
+  }
+  return best;
 }
 
 }  // namespace
 
 cudaError_t launch_paged_append(PagedAppendParams p, int d, int format, bool rope, cudaStream_t stream) {
   const int tpr = format == kPagedQ4 ? 8 : d / 16;
-  p.heads_per_thread = heads_per_thread(p.rows, tpr, p.cache.Hkv);
-  const int rpb = kThreads / tpr;
-  const dim3 grid(static_cast<unsigned>((p.rows + rpb - 1) / rpb),
-                  (p.cache.Hkv + p.heads_per_thread - 1) / p.heads_per_thread);
+  p.hb = append_heads(p.cache.Hkv);
+  const int rb = kThreads / tpr / p.hb;
   void (*kern)(PagedAppendParams) = nullptr;
   if (format == kPagedQ4)
     kern = d == 128 ? (rope ? append_q4_kernel<128, true> : append_q4_kernel<128, false>)
@@ -293,13 +354,22 @@ cudaError_t launch_paged_append(PagedAppendParams p, int d, int format, bool rop
   else
     kern = d == 128 ? (rope ? append_bf16_kernel<128, true> : append_bf16_kernel<128, false>)
                     : (rope ? append_bf16_kernel<64, true> : append_bf16_kernel<64, false>);
-  kern<<<grid, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.rows + rb - 1) / rb), (p.cache.Hkv + p.hb - 1) / p.hb);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = rope ? rb * (d / 2) * sizeof(float4) : 0;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 cudaError_t launch_paged_gather(PagedGatherParams p, int d, int format, cudaStream_t stream) {
   const int tpr = format == kPagedQ4 ? 8 : d / 8;
-  p.heads_per_thread = heads_per_thread(p.rows, tpr, p.cache.Hkv);
+  p.heads_per_thread = gather_heads(p.rows, tpr, p.cache.Hkv);
   const int rpb = kThreads / tpr;
   const dim3 grid(static_cast<unsigned>((p.rows + rpb - 1) / rpb),
                   (p.cache.Hkv + p.heads_per_thread - 1) / p.heads_per_thread);

@@ -341,7 +341,10 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
     {
       const int i = tid % (D / 2);
       float cs = 1.f, sn = 0.f;
-      if (p.rope) rope_cossin_fine(static_cast<float>(w.s.L - 1), p.freqs.hi[i], p.freqs.lo[i], &cs, &sn);
+      if (p.rope) {
+        const float4 a = turn_cossin(static_cast<float>(w.s.L - 1), p.freqs.f1[i], p.freqs.f2[i], p.freqs.f3[i]);
+        cs = a.x, sn = a.z;
+      }
 #pragma unroll
       for (int j = tid / (D / 2); j < C::ROWS; j += kConsumers / (D / 2)) {
         float x = 0.f, y = 0.f;
