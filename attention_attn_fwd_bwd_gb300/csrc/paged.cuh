@@ -42,9 +42,9 @@ struct PagedDev {
   int B, Hkv;
 };
 
-// theta_i / (2 pi) for i < d/2 as the sum of three floats (all of a double).
+// theta_i / (2 pi) for i < d/2 as the sum of three floats (all of a double): x + y + z.
 struct PagedFreqs {
-  float f1[64], f2[64], f3[64];
+  float4 f[64];
 };
 
 // Launch parameters. Strides of the dense sides are in bytes, the innermost is one element.
@@ -97,7 +97,8 @@ constexpr int kPagedMaxCtas = 1024;
 cudaError_t launch_paged_append(PagedAppendParams p, int d, int format, bool rope, cudaStream_t stream);
 cudaError_t launch_paged_gather(PagedGatherParams p, int d, int format, cudaStream_t stream);
 size_t paged_decode_workspace(int d, int g, int format);
-int paged_frag_rows(int page_size);
+// Rows of a page that one copy takes: the largest that pages and tiles are both whole multiples of.
+int paged_frag_rows(int page_size, int d, int g, int format);
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, int d, int format, cudaStream_t stream);
 
 // pos / page_size for 0 <= pos < 2^24: pos * (M d - 2^40) < 2^24 * 2^16 keeps the error of
@@ -128,15 +129,25 @@ __device__ __forceinline__ int q4_place(int r, int slot) {
 // computes it. fp32 alone would move about one element in 10^6 across such a border, and the
 // GPU's fp64 units are few (a first version recomputed doubtful elements in fp64: 126 us for
 // 18.5k rows of 8 heads, d = 128, against 20 us of traffic). So angles and products are carried as the
-// sum of two floats, to about 2^-37: 55 instructions per angle, shared by the heads of a row, and
-// 16 packed ones per pair and head.
+// sum of two floats, to about 2^-37: some 60 instructions per angle, shared by the heads of a
+// block, and 11 packed ones per pair and head.
 // ---------------------------------------------------------------------------------------------
 
-// (cos, sin) of 2 pi pos (f1 + f2 + f3), each as hi + lo. The angle in turns is reduced exactly,
+// Entry i of the frequencies, which are a kernel parameter: through a generic address, since an
+// indexed read of constant memory takes one pass per different index of the warp.
+__device__ __forceinline__ float4 freq_at(const PagedFreqs& f, int i) {
+  float4 v;
+  asm("ld.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(f.f + i));
+  return v;
+}
+
+// (cos, sin) of 2 pi pos (f.x + f.y + f.z), each as hi + lo, hi a multiple of 2^-16 (so that its
+// product with a bf16 is exact in fp32). The angle in turns is reduced exactly,
 // its nearest multiple of 1/256 looked up (table-driven reduction as in Tang, "Table-driven
 // implementation of the exponential function", 1989) and the rest, |d| <= 2 pi / 512, added by
 // the angle-sum formulas with Taylor series to d^5.
-__device__ __forceinline__ float4 turn_cossin(float pos, float f1, float f2, float f3) {
+__device__ __forceinline__ float4 turn_cossin(float pos, const float4& f) {
+  const float f1 = f.x, f2 = f.y, f3 = f.z;
   const float p1 = __fmul_rn(pos, f1), e1 = __fmaf_rn(pos, f1, -p1);
   const float frac = __fsub_rn(p1, rintf(p1));
   const float p2 = __fmul_rn(pos, f2), e2 = __fmaf_rn(pos, f2, -p2);
@@ -159,31 +170,33 @@ __device__ __forceinline__ float4 turn_cossin(float pos, float f1, float f2, flo
   float tc = __fmaf_rn(T.x, u, T.y);
   tc = __fmaf_rn(-T.z, v, tc);
   tc = __fmaf_rn(-T.w, dh, tc);
-  const float ch = __fsub_rn(T.x, pc);
-  const float cl = __fadd_rn(__fsub_rn(__fsub_rn(T.x, ch), pc), __fsub_rn(tc, pce));
+  const float c = __fsub_rn(T.x, pc);
+  const float ce = __fadd_rn(__fsub_rn(__fsub_rn(T.x, c), pc), __fsub_rn(tc, pce));
   const float ps = __fmul_rn(T.x, dh), pse = __fmaf_rn(T.x, dh, -ps);
   float ts = __fmaf_rn(T.z, u, T.w);
   ts = __fmaf_rn(T.x, v, ts);
   ts = __fmaf_rn(T.y, dh, ts);
-  const float sh = __fadd_rn(T.z, ps);
-  const float sl = __fadd_rn(__fsub_rn(ps, __fsub_rn(sh, T.z)), __fadd_rn(ts, pse));
+  const float s = __fadd_rn(T.z, ps);
+  const float se = __fadd_rn(__fsub_rn(ps, __fsub_rn(s, T.z)), __fadd_rn(ts, pse));
+  // 192 + x rounds x to a multiple of 2^-16
+  const float ch = __fsub_rn(__fadd_rn(c, 192.0f), 192.0f), cl = __fadd_rn(__fsub_rn(c, ch), ce);
+  const float sh = __fsub_rn(__fadd_rn(s, 192.0f), 192.0f), sl = __fadd_rn(__fsub_rn(s, sh), se);
   // quarter turns: (c, s) -> (-s, c) -> (-c, -s) -> (s, -c)
   const int q = (k >> 6) & 3;
   const float4 w = (q & 1) ? make_float4(-sh, -sl, ch, cl) : make_float4(ch, cl, sh, sl);
   return (q & 2) ? make_float4(-w.x, -w.y, -w.z, -w.w) : w;
 }
 
-// x c + y s of two lanes with c, s as hi + lo and nx = -x, ny = -y: h + t, h the rounded sum of
-// the products, t what all roundings lost.
-__device__ __forceinline__ void dot2_exact(uint64_t x, uint64_t nx, uint64_t y, uint64_t ny, uint64_t ch, uint64_t cl,
-                                           uint64_t sh, uint64_t sl, uint64_t& h, uint64_t& t) {
+// x c + y s of two lanes, c and s as hi + lo: h + t, h the rounded sum of the (exact) products
+// with the hi parts, t what that rounding lost and the products with the lo parts.
+__device__ __forceinline__ void dot2_exact(uint64_t x, uint64_t y, uint64_t ch, uint64_t cl, uint64_t sh, uint64_t sl,
+                                           uint64_t& h, uint64_t& t) {
   const uint64_t m1 = f2_pack(-1.0f, -1.0f);
   const uint64_t p1 = mul2(x, ch), p2 = mul2(y, sh);
-  const uint64_t n = add2(fma2(nx, ch, p1), fma2(ny, sh, p2));  // minus the products' errors
   h = add2(p1, p2);
   const uint64_t bb = fma2(p1, m1, h);
   const uint64_t er = add2(fma2(fma2(bb, m1, h), m1, p1), fma2(bb, m1, p2));
-  t = fma2(n, m1, add2(fma2(y, sl, mul2(x, cl)), er));
+  t = fma2(x, cl, fma2(y, sl, er));
 }
 
 // Two consecutive pairs, each word a bf16x2, rotated by the two angles packed in ch .. sl.
@@ -191,10 +204,9 @@ __device__ __forceinline__ void rot_word_exact(uint32_t& lo, uint32_t& hi, uint6
                                                uint64_t sl) {
   constexpr uint64_t kSigns = 0x8000000080000000ull;
   const uint64_t xl = bf16x2_to_f2(lo), xh = bf16x2_to_f2(hi);
-  const uint64_t nl = xl ^ kSigns, nh = xh ^ kSigns;
   uint64_t h0, t0, h1, t1;
-  dot2_exact(xl, nl, nh, xh, ch, cl, sh, sl, h0, t0);  // xl c - xh s
-  dot2_exact(xh, nh, xl, nl, ch, cl, sh, sl, h1, t1);  // xh c + xl s
+  dot2_exact(xl, xh ^ kSigns, ch, cl, sh, sl, h0, t0);  // xl c - xh s
+  dot2_exact(xh, xl, ch, cl, sh, sl, h1, t1);  // xh c + xl s
   const uint64_t y0 = add2(h0, t0), y1 = add2(h1, t1);
   lo = pack_bf16x2(f2_lo(y0), f2_hi(y0));
   hi = pack_bf16x2(f2_lo(y1), f2_hi(y1));

@@ -122,9 +122,9 @@ PagedFreqs paged_freqs(int d, float theta) {
   const double two_pi = 6.283185307179586476925286766559;
   for (int i = 0; i < d / 2; ++i) {
     double x = std::pow((double)theta, -2.0 * i / d) / two_pi;
-    x -= (f.f1[i] = (float)x);
-    x -= (f.f2[i] = (float)x);
-    f.f3[i] = (float)x;
+    x -= (f.f[i].x = (float)x);
+    x -= (f.f[i].y = (float)x);
+    f.f[i].z = (float)x;
   }
   return f;
 }
@@ -254,7 +254,7 @@ attnfuse_status attnfuse_paged_decode(const attnfuse_paged_cache* cache, const v
   p.scale_log2 = scale * kLog2e;
   if (p.rope) p.freqs = paged_freqs(cache->d, rope_theta);
   p.workspace = workspace;
-  p.frag_rows = paged_frag_rows(cache->page_size);
+  p.frag_rows = paged_frag_rows(cache->page_size, cache->d, p.g, cache->format);
   if (cache->format == ATTNFUSE_CACHE_BF16) {
     if ((rc = encode_map_bhnd(&p.tmK, cache->k, cache->k_strides, cache->num_pages, cache->Hkv, cache->page_size,
                               cache->d, "cache k", p.frag_rows)))

@@ -49,6 +49,8 @@ __device__ __forceinline__ bool find_row(const PagedDev& c, int b, int n, int fi
 
 // A block covers rb rows x hb heads, tpr threads for each; the angles of its rows are computed
 // once, by all threads, into shared memory: angle (k, t) of a row is that of thread t's k-th pair.
+// Angles 2q and 2q + 1 of a thread lie as it uses them, packed: (cos hi, cos hi, cos lo, cos lo),
+// then the sines.
 struct Place {
   int64_t row;
   int t, rr, h;  // thread of the row, row of the block, head
@@ -82,21 +84,24 @@ __device__ __forceinline__ void block_angles(const PagedAppendParams& p, float4*
     if (p.count && n >= __ldg(p.count + b)) continue;
     const int64_t pos = static_cast<int64_t>(__ldg(p.first + b)) + n;
     if (pos < 0 || pos >= p.cache.cap) continue;
-    const int i0 = pair_of<D, TPR, Q4>(j / TPR, j % TPR);
-    ang[i] = turn_cossin(static_cast<float>(pos), p.freqs.f1[i0], p.freqs.f2[i0], p.freqs.f3[i0]);
+    const int k = j / TPR, t = j % TPR;
+    const float4 a = turn_cossin(static_cast<float>(pos), freq_at(p.freqs, pair_of<D, TPR, Q4>(k, t)));
+    float* at = reinterpret_cast<float*>(ang + (i / (D / 2)) * (D / 2) + (k / 2) * 2 * TPR + t) + (k & 1);
+    at[0] = a.x;
+    at[2] = a.y;
+    at[4 * TPR] = a.z;
+    at[4 * TPR + 2] = a.w;
   }
   static_assert(K * TPR == D / 2, "pairs");
   __syncthreads();
 }
 
-// The two angles of pairs k, k + 1 of thread t of a row, packed.
+// Rotates the words of pairs 2q, 2q + 1 of thread t of a row.
 template <int D, int TPR>
-__device__ __forceinline__ void two_angles(const float4* ang, int rr, int k, int t, uint64_t (&w)[4]) {
-  const float4 a = ang[rr * (D / 2) + k * TPR + t], b = ang[rr * (D / 2) + (k + 1) * TPR + t];
-  w[0] = f2_pack(a.x, b.x);
-  w[1] = f2_pack(a.y, b.y);
-  w[2] = f2_pack(a.z, b.z);
-  w[3] = f2_pack(a.w, b.w);
+__device__ __forceinline__ void rotate(uint32_t& lo, uint32_t& hi, const float4* ang, int rr, int q, int t) {
+  const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(ang + rr * (D / 2) + q * 2 * TPR + t);
+  const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(ang + rr * (D / 2) + (q * 2 + 1) * TPR + t);
+  rot_word_exact(lo, hi, c.x, c.y, s.x, s.y);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -129,11 +134,7 @@ __global__ void __launch_bounds__(kThreads) append_bf16_kernel(const __grid_cons
       uint32_t* L = reinterpret_cast<uint32_t*>(&lo);
       uint32_t* H = reinterpret_cast<uint32_t*>(&hi);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint64_t a[4];
-        two_angles<D, CP>(ang, w.rr, 2 * q, w.t, a);
-        rot_word_exact(L[q], H[q], a[0], a[1], a[2], a[3]);
-      }
+      for (int q = 0; q < 4; ++q) rotate<D, CP>(L[q], H[q], ang, w.rr, q, w.t);
     }
     uint8_t* kd = p.cache.k + r.page * p.cache.k_sp + r.slot * p.cache.k_st + w.h * p.cache.k_sh + w.t * 16;
     uint8_t* vd = p.cache.v + r.page * p.cache.v_sp + r.slot * p.cache.v_st + w.h * p.cache.v_sh + w.t * 16;
@@ -150,21 +151,19 @@ __global__ void __launch_bounds__(kThreads) append_bf16_kernel(const __grid_cons
 // whole pairs (group g with group g + G/2) and exactly chunk t of the stored row
 // ---------------------------------------------------------------------------------------------
 
-// 4 elements (two bf16x2 words) with reciprocal step inv -> 4 nibbles, lowest first.
-// x and the step have 8 significant bits each, so |x| / s is a tie k + 1/2 or at least 2^-12
-// (relative) away from one; the product with the reciprocal (1 ulp) is within 2^-22, and the
-// factor 1 + 2^-20 puts ties, and only them, on the far side.
+// 4 elements (two bf16x2 words) -> 4 nibbles code + 8 in the low 16 bits, lowest first.
+// inv = (1 + 2^-20) / s. x and s have 8 significant bits each, so |x| / s is a tie k + 1/2 or at
+// least 2^-12 (relative) away from one; the reciprocal's error (1 ulp) and a rounding stay within
+// 2^-22, so the factor puts ties, and only them, past the middle. |x| / s < 7.03: no clamp.
+// Added to 1.5 2^23 + 8, the rounded quotient is the sum's low bits; those of four sums, shifted
+// by multiplications, add up without carries.
 __device__ __forceinline__ uint32_t q4_codes(uint32_t w0, uint32_t w1, float inv) {
-  const float x[4] = {bf16lo_to_f32(w0), bf16hi_to_f32(w0), bf16lo_to_f32(w1), bf16hi_to_f32(w1)};
-  uint32_t out = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float t = fminf(fabsf(x[i] * inv), 7.0f);
-    const float z = __fadd_rd(__fmaf_rn(t, 1.00000095367431640625f, 0.5f), 8388608.0f);  // 2^23 + floor
-    const int m = __float_as_int(z) & 7;
-    out |= static_cast<uint32_t>(x[i] < 0.0f ? 8 - m : 8 + m) << (4 * i);
-  }
-  return out;
+  constexpr float kAt = 12582920.0f;
+  const uint32_t n0 = __float_as_uint(__fmaf_rn(bf16lo_to_f32(w0), inv, kAt));
+  const uint32_t n1 = __float_as_uint(__fmaf_rn(bf16hi_to_f32(w0), inv, kAt));
+  const uint32_t n2 = __float_as_uint(__fmaf_rn(bf16lo_to_f32(w1), inv, kAt));
+  const uint32_t n3 = __float_as_uint(__fmaf_rn(bf16hi_to_f32(w1), inv, kAt));
+  return n0 + n1 * 16u + n2 * 256u + n3 * 4096u;
 }
 
 // Largest magnitudes of a row's groups as bf16 bits (their integers order like the values, NaN
@@ -210,11 +209,8 @@ __global__ void __launch_bounds__(kThreads) append_q4_kernel(const __grid_consta
     if (live) {
 #pragma unroll
       for (int g = 0; g < G / 2; ++g) {
-        uint64_t a[4];
-        two_angles<D, 8>(ang, w.rr, 4 * g, w.t, a);
-        rot_word_exact(x[0][g].x, x[0][g + G / 2].x, a[0], a[1], a[2], a[3]);
-        two_angles<D, 8>(ang, w.rr, 4 * g + 2, w.t, a);
-        rot_word_exact(x[0][g].y, x[0][g + G / 2].y, a[0], a[1], a[2], a[3]);
+        rotate<D, 8>(x[0][g].x, x[0][g + G / 2].x, ang, w.rr, 2 * g, w.t);
+        rotate<D, 8>(x[0][g].y, x[0][g + G / 2].y, ang, w.rr, 2 * g + 1, w.t);
       }
     }
   }
@@ -233,9 +229,9 @@ __global__ void __launch_bounds__(kThreads) append_q4_kernel(const __grid_consta
   uint32_t s = __bfloat16_as_ushort(__float2bfloat16_rn(amax * (1.0f / 7.0f)));
   float inv;
   asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(__uint_as_float(s << 16)));
+  inv *= 1.00000095367431640625f;
   if (amax < 0x1p-96f) s = 0, inv = 0.0f;        // reads back as zeros
-  if (bits >= 0x7F80u) s = 0x7FC0u, inv = 0.0f;  // an infinity or a NaN: reads back as NaN
-  // (inf * 0 and NaN * 0 are NaN, which fminf turns into 7: harmless under a NaN step)
+  if (bits >= 0x7F80u) s = 0x7FC0u, inv = 0.0f;  // an infinity or a NaN: reads back as NaN, whatever the codes
   uint32_t code[2][G];
   const int row0 = threadIdx.x & 24;  // the row's first lane
 #pragma unroll
@@ -248,11 +244,11 @@ __global__ void __launch_bounds__(kThreads) append_q4_kernel(const __grid_consta
     uint8_t* kd = p.cache.k + r.page * p.cache.k_sp + w.h * p.cache.k_sh + at;
     uint8_t* vd = p.cache.v + r.page * p.cache.v_sp + w.h * p.cache.v_sh + at;
     if constexpr (G == 4) {
-      *reinterpret_cast<uint2*>(kd) = make_uint2(code[0][0] | code[0][1] << 16, code[0][2] | code[0][3] << 16);
-      *reinterpret_cast<uint2*>(vd) = make_uint2(code[1][0] | code[1][1] << 16, code[1][2] | code[1][3] << 16);
+      *reinterpret_cast<uint2*>(kd) = make_uint2(__byte_perm(code[0][0], code[0][1], 0x5410), __byte_perm(code[0][2], code[0][3], 0x5410));
+      *reinterpret_cast<uint2*>(vd) = make_uint2(__byte_perm(code[1][0], code[1][1], 0x5410), __byte_perm(code[1][2], code[1][3], 0x5410));
     } else {
-      *reinterpret_cast<uint32_t*>(kd) = code[0][0] | code[0][1] << 16;
-      *reinterpret_cast<uint32_t*>(vd) = code[1][0] | code[1][1] << 16;
+      *reinterpret_cast<uint32_t*>(kd) = __byte_perm(code[0][0], code[0][1], 0x5410);
+      *reinterpret_cast<uint32_t*>(vd) = __byte_perm(code[1][0], code[1][1], 0x5410);
     }
     if (w.t < 2 * G) {
       uint8_t* sd = w.t < G ? p.cache.ks + r.page * p.cache.ks_sp + w.h * p.cache.ks_sh

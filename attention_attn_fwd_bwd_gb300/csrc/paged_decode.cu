@@ -36,17 +36,20 @@ namespace {
 constexpr int kWarps = 4;              // consumers
 constexpr int kConsumers = kWarps * 32;
 constexpr int kThreads = kConsumers + 32;
-constexpr int kTile = kWarps * 16;     // keys per tile
 constexpr float kLazy = 8.0f;          // the running maximum may lag by 2^8
 
 template <int D, int NT, bool Q4>
 struct Cfg {
   static constexpr int ROWS = 8 * NT;                                   // query heads per item
-  static constexpr uint32_t KB = kTile * (Q4 ? D / 2 : 2 * D);          // K (and V) bytes of a tile
-  static constexpr uint32_t SB = Q4 ? kTile * (D / 16) : 0;             // and their steps
+  // 16-key blocks of a tile per warp: two hide each other's latencies and share the per-tile
+  // work; rows of 256 bytes (bf16, d = 128) keep the HBM busy with one.
+  static constexpr int BPW = Q4 || D == 64 ? 2 : 1;
+  static constexpr int TILE = kWarps * 16 * BPW;                        // keys
+  static constexpr uint32_t KB = TILE * (Q4 ? D / 2 : 2 * D);           // K (and V) bytes of a tile
+  static constexpr uint32_t SB = Q4 ? TILE * (D / 16) : 0;              // and their steps
   static constexpr uint32_t STAGE = 2 * KB + 2 * SB;
-  static constexpr int STAGES = Q4 ? 4 : (NT == 1 || D == 64 ? 3 : 5);
-  static constexpr int CTAS = Q4 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 2 : (D == 64 ? 2 : 1));
+  static constexpr int STAGES = Q4 ? 3 : (NT == 1 || D == 64 ? 3 : 5);
+  static constexpr int CTAS = Q4 ? (NT == 1 ? 3 : 2) : (NT == 1 || D == 64 ? 2 : 1);
   static constexpr uint32_t QROW = 2 * D + 16;                          // padded query row
   static constexpr uint32_t OFF_Q = STAGES * STAGE;
   static constexpr uint32_t OFF_O = OFF_Q + 2 * ROWS * QROW;            // two warps' accumulators
@@ -60,9 +63,9 @@ struct Ctl {
   int abort_flag;
   int b0;                              // first sequence of this CTA's run, and the units of it
   int rem0;                            // before the run
-  int64_t total;
   int64_t wsum[kThreads / 32];
   float m[kWarps][16], l[kWarps][16];
+  float qmax[16][2];                   // q4: largest |q| of a head, by half rows
 };
 
 template <int D, int NT, bool Q4>
@@ -154,12 +157,13 @@ struct Span {
   int L, first, t0, nt;  // visible keys [first, L), first tile, tiles
 };
 
+template <int TILE>
 __device__ __forceinline__ Span span_of(const PagedDecodeParams& p, int b) {
   Span s;
   s.L = min(max(__ldg(p.lens + b), 0), p.cache.cap);
   s.first = p.window > 0 && s.L > p.window ? s.L - p.window : 0;
-  s.t0 = s.first / kTile;
-  s.nt = s.L > 0 ? (s.L - 1) / kTile - s.t0 + 1 : 0;
+  s.t0 = s.first / TILE;
+  s.nt = s.L > 0 ? (s.L - 1) / TILE - s.t0 + 1 : 0;
   return s;
 }
 
@@ -194,6 +198,7 @@ __device__ __forceinline__ int run_of(int64_t T, int64_t unit, int G) {
 }
 
 // Walks the segments of a run: all roles step through the same ones.
+template <int TILE>
 struct Walk {
   const PagedDecodeParams& p;
   Span s;
@@ -202,7 +207,7 @@ struct Walk {
   __device__ Walk(const PagedDecodeParams& p_, int b0, int rem0, int left_) : p(p_), b(b0), left(left_), head(true) {
     n = 0;
     if (left <= 0) return;
-    s = span_of(p, b);
+    s = span_of<TILE>(p, b);
     hh = rem0 / s.nt;
     t = rem0 - hh * s.nt;
     n = min(left, s.nt - t);
@@ -219,7 +224,7 @@ struct Walk {
       t = 0;
       if (++hh == p.items) {
         hh = 0;
-        do s = span_of(p, ++b);
+        do s = span_of<TILE>(p, ++b);
         while (s.nt == 0);
       }
     }
@@ -231,8 +236,10 @@ struct Walk {
 // Producer
 // ---------------------------------------------------------------------------------------------
 template <int D, int NT, bool Q4>
-__device__ __forceinline__ void produce(const PagedDecodeParams& p, uint8_t* smem, Ctl* ctl, Walk w) {
+__device__ __forceinline__ void produce(const PagedDecodeParams& p, uint8_t* smem, Ctl* ctl,
+                                        Walk<Cfg<D, NT, Q4>::TILE> w) {
   using C = Cfg<D, NT, Q4>;
+  constexpr int kTile = C::TILE;
   const int lane = threadIdx.x % 32;
   const PagedDev& c = p.cache;
   const int F = p.frag_rows, nf = kTile / F;
@@ -322,48 +329,95 @@ __device__ __forceinline__ int key_of(int i) {
   return (i & 8) + ((j & 1) ? 4 + ((j >> 1) ^ 1) : j >> 1);
 }
 
+// A word of 4 nibbles n (bits 4i, in both halves) -> the fp16 pairs of n - 8. Set into the mantissa
+// of 1024, a nibble at bits 0-3 makes 1024 + n and one at bits 4-7 makes 1024 + 16 n; one
+// fp16 operation, exact, takes that to n - 8.
+__device__ __forceinline__ void nibbles(uint32_t x, uint32_t& a0, uint32_t& a1, uint32_t& a2, uint32_t& a3) {
+  const uint32_t y = x >> 8;
+  a0 = hadd2((x & 0x000F000Fu) | 0x64006400u, 0xE408E408u);
+  a1 = hfma2((x & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
+  a2 = hadd2((y & 0x000F000Fu) | 0x64006400u, 0xE408E408u);
+  a3 = hfma2((y & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
+}
+
+// q4: the power of two that takes the largest |q| of head j to [1/2, 1) (or its reciprocal).
+template <int D>
+__device__ __forceinline__ float q_scale(const Ctl* ctl, int j, bool down) {
+  const float m = D == 128 ? fmaxf(ctl->qmax[j][0], ctl->qmax[j][1]) : ctl->qmax[j][0];
+  const uint32_t ex = __float_as_uint(m) >> 23;                 // biased; 0: zero or subnormal, 255: not finite
+  const uint32_t e = ex == 0 || ex == 255 ? 126u : min(ex, 252u);  // 2^(e - 126) > m
+  return __uint_as_float((down ? 253u - e : 1u + e) << 23);
+}
+
 template <int D, int NT, bool Q4>
-__device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* smem, Ctl* ctl, Walk w) {
+__device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* smem, Ctl* ctl,
+                                        Walk<Cfg<D, NT, Q4>::TILE> w) {
   using C = Cfg<D, NT, Q4>;
+  constexpr int BPW = C::BPW;
   constexpr int KS = D / 16;       // 16-element steps of a row
   constexpr int G = D / kQ4Group;
   constexpr int MT = D / 16;       // 16-element tiles of O
+  constexpr int JS = kConsumers / (D / 2), JN = C::ROWS / JS;  // query heads a thread prepares
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, r = lane / 4, t = lane % 4;
   const uint32_t base = smem_u32(smem);
-  // x = s * c2 in log2 units; 4-bit codes come out of the matrix product 16 times too small
-  const float c2 = p.scale_log2 * (Q4 ? 16.0f : 1.0f);
   int it = 0;
   bool ok = true;
   for (; w.live(); w.next()) {
     const int kvh = w.hh / p.chunks, h0 = kvh * p.g + (w.hh % p.chunks) * C::ROWS;
     const int rows = min(C::ROWS, kvh * p.g + p.g - h0);
-    // ---- the item's queries: rotated in fp32, kept as the sum of two bf16 (16 bits) ----
+    // ---- the item's queries, rotated in fp32 and kept as the sum of two 16-bit parts: bf16 (16
+    // bits), or for q4 fp16 after a power of two per head has brought the largest to [1/2, 1) ----
     {
-      const int i = tid % (D / 2);
-      float cs = 1.f, sn = 0.f;
+      const int i = tid % (D / 2), j0 = tid / (D / 2);
+      float x[JN], y[JN];
+#pragma unroll
+      for (int k = 0; k < JN; ++k) {
+        x[k] = y[k] = 0.f;
+        if (j0 + k * JS < rows) {
+          const __nv_bfloat16* q = p.q + w.b * p.q_sb + (h0 + j0 + k * JS) * p.q_sh + i;
+          x[k] = __bfloat162float(q[0]);
+          y[k] = __bfloat162float(q[D / 2]);
+        }
+      }
       if (p.rope) {
-        const float4 a = turn_cossin(static_cast<float>(w.s.L - 1), p.freqs.f1[i], p.freqs.f2[i], p.freqs.f3[i]);
-        cs = a.x, sn = a.z;
+        const float4 a = turn_cossin(static_cast<float>(w.s.L - 1), freq_at(p.freqs, i));
+        const float cs = a.x + a.y, sn = a.z + a.w;
+#pragma unroll
+        for (int k = 0; k < JN; ++k) {
+          float u, v;
+          rot_pair(x[k], y[k], cs, sn, u, v);
+          x[k] = u, y[k] = v;
+        }
+      }
+      if constexpr (Q4) {
+#pragma unroll
+        for (int k = 0; k < JN; ++k) {
+          uint32_t m = max(__float_as_uint(fabsf(x[k])), __float_as_uint(fabsf(y[k])));
+          m = __reduce_max_sync(0xffffffffu, m);
+          if (lane == 0) ctl->qmax[j0 + k * JS][D == 128 ? warp & 1 : 0] = __uint_as_float(m);
+        }
+        named_bar_sync(1, kConsumers);
       }
 #pragma unroll
-      for (int j = tid / (D / 2); j < C::ROWS; j += kConsumers / (D / 2)) {
-        float x = 0.f, y = 0.f;
-        if (j < rows) {
-          const __nv_bfloat16* q = p.q + w.b * p.q_sb + (h0 + j) * p.q_sh + i;
-          x = __bfloat162float(q[0]);
-          y = __bfloat162float(q[D / 2]);
-          if (p.rope) {
-            float a, b;
-            rot_pair(x, y, cs, sn, a, b);
-            x = a, y = b;
-          }
+      for (int k = 0; k < JN; ++k) {
+        const int j = j0 + k * JS;
+        uint16_t* hi = reinterpret_cast<uint16_t*>(smem + C::OFF_Q + j * C::QROW);
+        uint16_t* lo = reinterpret_cast<uint16_t*>(smem + C::OFF_Q + (C::ROWS + j) * C::QROW);
+        if constexpr (Q4) {
+          const float f = q_scale<D>(ctl, j, true);
+          const float u = x[k] * f, v = y[k] * f;
+          const __half a = __float2half_rn(u), b = __float2half_rn(v);
+          hi[i] = __half_as_ushort(a);
+          hi[i + D / 2] = __half_as_ushort(b);
+          lo[i] = __half_as_ushort(__float2half_rn(u - __half2float(a)));
+          lo[i + D / 2] = __half_as_ushort(__float2half_rn(v - __half2float(b)));
+        } else {
+          const __nv_bfloat16 a = __float2bfloat16_rn(x[k]), b = __float2bfloat16_rn(y[k]);
+          hi[i] = __bfloat16_as_ushort(a);
+          hi[i + D / 2] = __bfloat16_as_ushort(b);
+          lo[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x[k] - __bfloat162float(a)));
+          lo[i + D / 2] = __bfloat16_as_ushort(__float2bfloat16_rn(y[k] - __bfloat162float(b)));
         }
-        __nv_bfloat16* hi = reinterpret_cast<__nv_bfloat16*>(smem + C::OFF_Q + j * C::QROW);
-        __nv_bfloat16* lo = reinterpret_cast<__nv_bfloat16*>(smem + C::OFF_Q + (C::ROWS + j) * C::QROW);
-        hi[i] = __float2bfloat16_rn(x);
-        hi[i + D / 2] = __float2bfloat16_rn(y);
-        lo[i] = __float2bfloat16_rn(x - __bfloat162float(hi[i]));
-        lo[i + D / 2] = __float2bfloat16_rn(y - __bfloat162float(hi[i + D / 2]));
       }
     }
     named_bar_sync(1, kConsumers);
@@ -391,36 +445,20 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
           }
         }
       }
-    // q4: a nibble n = code + 8 enters the product as 1 + n/16 (four bits set into the mantissa of
-    // 1.0), so each group's sum starts at -1.5 times the sum of its q. The sum is itself a
-    // product with ones.
-    float qs[Q4 ? NT : 1][Q4 ? G : 1][2];
-    if constexpr (Q4) {
-      const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          float x[4] = {};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mma_bf16(x, ones, qf[e & 1][nt][2 * g + e / 2][0], qf[e & 1][nt][2 * g + e / 2][1]);
-          qs[nt][g][0] = -1.5f * x[0];
-          qs[nt][g][1] = -1.5f * x[1];
-        }
-    }
-    float slope[NT][2];
+    // Scores stay as the matrix product gives them, S; x = S c2 (log2 units). A bias is added as
+    // bias / c2, and a score renews the maximum where S > th.
+    float c2[NT][2], slope[NT][2], th[NT][2], nm[NT][2], l[NT][2] = {};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int j = nt * 8 + 2 * t + e;
-        slope[nt][e] = p.slopes && j < rows ? __ldg(p.slopes + h0 + j) * kLog2e : 0.f;
+        c2[nt][e] = Q4 ? fmaxf(p.scale_log2 * q_scale<D>(ctl, j, false), 1e-44f) : p.scale_log2;
+        slope[nt][e] = p.slopes && j < rows ? __fdiv_rn(__ldg(p.slopes + h0 + j) * kLog2e, c2[nt][e]) : 0.f;
+        th[nt][e] = kNegInf;
+        nm[nt][e] = 0.f;  // minus the maximum (log2 units); 0 while there is none (th is -inf then)
       }
-
     float o[NT][MT][4] = {};
-    float m[NT][2], l[NT][2] = {};
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = kNegInf;
     // q4: weights p * step go into fp16 as p * step * vmul[g], vmul = 2^-e of the largest step
     // seen so far in group g (it may be exceeded by 2^4 before it is renewed)
     uint32_t vthr[Q4 ? G / 2 : 1] = {};
@@ -434,120 +472,133 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) continue;  // unwind through the same barriers as the other warps
       const uint32_t stage = base + st * C::STAGE;
-      const int n0 = (w.s.t0 + w.t + i) * kTile + warp * 16;
-      const bool loaded = (ctl->frags[st] >> (warp * 16 / p.frag_rows)) & 1;
-      if (loaded && n0 < w.s.L && n0 + 16 > w.s.first) {
-        const bool edge = n0 < w.s.first || n0 + 16 > w.s.L;
-        // ---- scores: s[nt][i], key rows r and r + 8 ----
-        float s[NT][4];
-        uint32_t vs[2][Q4 ? G / 2 : 1];  // q4: steps of V's rows r, r + 8 (two bf16 per word)
+      const int n0 = (w.s.t0 + w.t + i) * C::TILE + warp * (16 * BPW);
+      const uint32_t got = ctl->frags[st] >> (warp * (16 * BPW) / p.frag_rows);
+      bool loaded[BPW], any = false, edge = n0 < w.s.first || n0 + 16 * BPW > w.s.L;
+#pragma unroll
+      for (int u = 0; u < BPW; ++u) {
+        loaded[u] = (got >> (u && p.frag_rows == 16 ? 1 : 0)) & 1;
+        any |= loaded[u] && n0 + 16 * u < w.s.L && n0 + 16 * u + 16 > w.s.first;
+        edge |= !loaded[u];
+      }
+      if (any) {
+        // ---- scores: s[u][nt][i], key rows r and r + 8 of block u ----
+        float s[BPW][NT][4];
+        uint32_t vs[BPW][2][Q4 ? G / 2 : 1];  // q4: steps of V's rows r, r + 8 (two bf16 per word)
         const int ka = key_of<Q4>(r), kb = key_of<Q4>(r + 8);
-        if constexpr (Q4) {
-          uint32_t kw[2][G], ks[2][G / 2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int key = warp * 16 + (e ? kb : ka);
-            if constexpr (D == 128) {
-              const uint4 x = lds128(stage + key * 64 + ((t ^ (key & 2)) * 16));
-              kw[e][0] = __byte_perm(x.x, x.z, 0x5410);
-              kw[e][1] = __byte_perm(x.x, x.z, 0x7632);
-              kw[e][2] = __byte_perm(x.y, x.w, 0x5410);
-              kw[e][3] = __byte_perm(x.y, x.w, 0x7632);
-              const uint2 y = lds64(stage + 2 * C::KB + key * 8);
-              ks[e][0] = y.x, ks[e][1] = y.y;
-              const uint2 z = lds64(stage + 2 * C::KB + C::SB + key * 8);
-              vs[e][0] = z.x, vs[e][1] = z.y;
-            } else {
-              const uint2 x = lds64(stage + key * 32 + t * 8);
-              kw[e][0] = __byte_perm(x.x, x.y, 0x5410);
-              kw[e][1] = __byte_perm(x.x, x.y, 0x7632);
-              ks[e][0] = lds32(stage + 2 * C::KB + key * 4);
-              vs[e][0] = lds32(stage + 2 * C::KB + C::SB + key * 4);
-            }
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
-#pragma unroll
-          for (int g = 0; g < G; ++g) {
-            uint32_t a[2][4];
+        for (int u = 0; u < BPW; ++u) {
+          if constexpr (Q4) {
+            uint32_t kw[2][G], ks[2][G / 2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const uint32_t x = kw[e][g];
-              a[0][e] = ((x << 3) & 0x00780078u) | 0x3F803F80u;
-              a[0][2 + e] = ((x >> 1) & 0x00780078u) | 0x3F803F80u;
-              a[1][e] = ((x >> 5) & 0x00780078u) | 0x3F803F80u;
-              a[1][2 + e] = ((x >> 9) & 0x00780078u) | 0x3F803F80u;
+              const int key = warp * (16 * BPW) + 16 * u + (e ? kb : ka);
+              if constexpr (D == 128) {
+                const uint4 x = lds128(stage + key * 64 + ((t ^ (key & 2)) * 16));
+                kw[e][0] = __byte_perm(x.x, x.z, 0x5410);
+                kw[e][1] = __byte_perm(x.x, x.z, 0x7632);
+                kw[e][2] = __byte_perm(x.y, x.w, 0x5410);
+                kw[e][3] = __byte_perm(x.y, x.w, 0x7632);
+                const uint2 y = lds64(stage + 2 * C::KB + key * 8);
+                ks[e][0] = y.x, ks[e][1] = y.y;
+                const uint2 z = lds64(stage + 2 * C::KB + C::SB + key * 8);
+                vs[u][e][0] = z.x, vs[u][e][1] = z.y;
+              } else {
+                const uint2 x = lds64(stage + key * 32 + t * 8);
+                kw[e][0] = __byte_perm(x.x, x.y, 0x5410);
+                kw[e][1] = __byte_perm(x.x, x.y, 0x7632);
+                ks[e][0] = lds32(stage + 2 * C::KB + key * 4);
+                vs[u][e][0] = lds32(stage + 2 * C::KB + C::SB + key * 4);
+              }
             }
-            const float sa = (g & 1) ? bf16hi_to_f32(ks[0][g / 2]) : bf16lo_to_f32(ks[0][g / 2]);
-            const float sb = (g & 1) ? bf16hi_to_f32(ks[1][g / 2]) : bf16lo_to_f32(ks[1][g / 2]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float x[4] = {qs[nt][g][0], qs[nt][g][1], qs[nt][g][0], qs[nt][g][1]};
+            for (int g = 0; g < G; ++g) {
+              uint32_t a[2][4];
 #pragma unroll
-              for (int part = 0; part < 2; ++part)
+              for (int e = 0; e < 2; ++e) nibbles(kw[e][g], a[0][e], a[0][2 + e], a[1][e], a[1][2 + e]);
+              const float sa = (g & 1) ? bf16hi_to_f32(ks[0][g / 2]) : bf16lo_to_f32(ks[0][g / 2]);
+              const float sb = (g & 1) ? bf16hi_to_f32(ks[1][g / 2]) : bf16lo_to_f32(ks[1][g / 2]);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) mma_bf16(x, a[e], qf[part][nt][2 * g + e][0], qf[part][nt][2 * g + e][1]);
-              s[nt][0] = fmaf(sa, x[0], s[nt][0]);
-              s[nt][1] = fmaf(sa, x[1], s[nt][1]);
-              s[nt][2] = fmaf(sb, x[2], s[nt][2]);
-              s[nt][3] = fmaf(sb, x[3], s[nt][3]);
+              for (int nt = 0; nt < NT; ++nt) {
+                float x[4] = {};
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) mma_f16(x, a[e], qf[part][nt][2 * g + e][0], qf[part][nt][2 * g + e][1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float f = e < 2 ? sa : sb;
+                  s[u][nt][e] = g == 0 ? f * x[e] : fmaf(f, x[e], s[u][nt][e]);
+                }
+              }
             }
-          }
-        } else {
-          float x[2][NT][4] = {};
-          const int row = warp * 16 + (lane & 15);
+          } else {
+            float x[2][NT][4] = {};
+            const int row = warp * (16 * BPW) + 16 * u + (lane & 15);
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            uint32_t a[4];
-            ldsm4(a, stage + (k / 4) * (kTile * 128) + row * 128 + ((((k & 3) * 2 + (lane >> 4)) ^ (row & 7)) * 16));
+            for (int k = 0; k < KS; ++k) {
+              uint32_t a[4];
+              ldsm4(a, stage + (k / 4) * (C::TILE * 128) + row * 128 + ((((k & 3) * 2 + (lane >> 4)) ^ (row & 7)) * 16));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int part = 0; part < 2; ++part) mma_bf16(x[part][nt], a, qf[part][nt][k][0], qf[part][nt][k][1]);
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int part = 0; part < 2; ++part) mma_bf16(x[part][nt], a, qf[part][nt][k][0], qf[part][nt][k][1]);
+              for (int e = 0; e < 4; ++e) s[u][nt][e] = x[0][nt][e] + x[1][nt][e];
           }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[nt][e] = x[0][nt][e] + x[1][nt][e];
         }
-        // ---- log2 units, bias, mask ----
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[nt][e] *= c2;
+        // ---- bias, mask ----
         if (p.slopes) {
-          const float da = static_cast<float>(n0 + ka - (w.s.L - 1)), db = static_cast<float>(n0 + kb - (w.s.L - 1));
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int u = 0; u < BPW; ++u) {
+            const int n = n0 + 16 * u - (w.s.L - 1);
+            const float da = static_cast<float>(n + ka), db = static_cast<float>(n + kb);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[nt][e] = fmaf(slope[nt][e & 1], e < 2 ? da : db, s[nt][e]);
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[u][nt][e] = fmaf(slope[nt][e & 1], e < 2 ? da : db, s[u][nt][e]);
+          }
         }
         if (edge) {
-          const bool va = n0 + ka >= w.s.first && n0 + ka < w.s.L, vb = n0 + kb >= w.s.first && n0 + kb < w.s.L;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int u = 0; u < BPW; ++u) {
+            const int na = n0 + 16 * u + ka, nb = n0 + 16 * u + kb;
+            const bool va = loaded[u] && na >= w.s.first && na < w.s.L, vb = loaded[u] && nb >= w.s.first && nb < w.s.L;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (!(e < 2 ? va : vb)) s[nt][e] = kNegInf;
-          if constexpr (Q4) {
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int q = 0; q < G / 2; ++q) {
-              if (!va) vs[0][q] = 0;
-              if (!vb) vs[1][q] = 0;
+              for (int e = 0; e < 4; ++e)
+                if (!(e < 2 ? va : vb)) s[u][nt][e] = kNegInf;
+            if constexpr (Q4) {
+#pragma unroll
+              for (int q = 0; q < G / 2; ++q) {
+                if (!va) vs[u][0][q] = 0;
+                if (!vb) vs[u][1][q] = 0;
+              }
             }
           }
         }
         // ---- running maximum, renewed only where a score passes it by 2^8 ----
         bool up = false;
+        float mx[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) up |= s[nt][e] > m[nt][e & 1] + kLazy;
+          for (int e = 0; e < 2; ++e) {
+            mx[nt][e] = fmaxf(s[0][nt][e], s[0][nt][e + 2]);
+            if constexpr (BPW == 2) mx[nt][e] = fmaxf(fmaxf(mx[nt][e], s[BPW - 1][nt][e]), s[BPW - 1][nt][e + 2]);
+            up |= mx[nt][e] > th[nt][e];
+          }
+        uint32_t vx[Q4 ? G / 2 : 1];
         if constexpr (Q4) {
 #pragma unroll
-          for (int q = 0; q < G / 2; ++q) up |= __vmaxu2(__vmaxu2(vs[0][q], vs[1][q]), vthr[q]) != vthr[q];
+          for (int q = 0; q < G / 2; ++q) {
+            vx[q] = __vmaxu2(__vmaxu2(vs[0][0][q], vs[0][1][q]), __vmaxu2(vs[BPW - 1][0][q], vs[BPW - 1][1][q]));
+            up |= __vmaxu2(vx[q], vthr[q]) != vthr[q];
+          }
         }
         if (__any_sync(0xffffffffu, up)) {
           float f[NT][2];
@@ -555,19 +606,23 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float x = fmaxf(s[nt][e], s[nt][e + 2]);
+              float x = mx[nt][e];
 #pragma unroll
               for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-              const float mn = fmaxf(m[nt][e], x);
-              f[nt][e] = ex2_approx(m[nt][e] - (mn == kNegInf ? 0.f : mn));
-              m[nt][e] = mn;
-              l[nt][e] *= f[nt][e];
+              f[nt][e] = 1.f;
+              if (x > th[nt][e] - __fdiv_rn(kLazy, c2[nt][e])) {  // above the present maximum
+                const float m = x * c2[nt][e];
+                f[nt][e] = th[nt][e] == kNegInf ? 0.f : ex2_approx(-nm[nt][e] - m);
+                nm[nt][e] = -m;
+                th[nt][e] = x + __fdiv_rn(kLazy, c2[nt][e]);
+                l[nt][e] *= f[nt][e];
+              }
             }
           float fv[Q4 ? G : 1];
           if constexpr (Q4) {
 #pragma unroll
             for (int q = 0; q < G / 2; ++q) {
-              uint32_t x = __vmaxu2(vs[0][q], vs[1][q]);
+              uint32_t x = vx[q];
 #pragma unroll
               for (int off = 4; off < 32; off <<= 1) x = __vmaxu2(x, __shfl_xor_sync(0xffffffffu, x, off));
               uint32_t thr = 0;
@@ -576,15 +631,15 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
                 const uint32_t old = (vthr[q] >> (16 * e)) & 0xFFFFu, now = (x >> (16 * e)) & 0xFFFFu;
                 const int g = 2 * q + e;
                 fv[g] = 1.f;
-                uint32_t th = old;
+                uint32_t lim = old;
                 if (now > old) {
                   const uint32_t ex = min(now >> 7, 253u);  // biased exponent of the largest step
                   const float mul = __uint_as_float((254u - ex) << 23);
                   fv[g] = __fdiv_rn(mul, vmul[g]);
                   vmul[g] = mul;
-                  th = min(((ex + 4) << 7) | 0x7Fu, 0x7FFFu);
+                  lim = min(((ex + 4) << 7) | 0x7Fu, 0x7FFFu);
                 }
-                thr |= th << (16 * e);
+                thr |= lim << (16 * e);
               }
               vthr[q] = thr;
             }
@@ -598,90 +653,89 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
         }
         // ---- weights ----
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float mm = m[nt][e & 1];
-            s[nt][e] = ex2_approx(s[nt][e] - (mm == kNegInf ? 0.f : mm));
-            l[nt][e & 1] += s[nt][e];
-          }
-        // ---- O^T += V^T P^T ----
-        if constexpr (Q4) {
-          uint32_t vw[2][G];  // keys (2t, 2t + 1), (2t + 8, 2t + 9): 4 nibbles of each per group
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int k0 = warp * 16 + key_of<true>(8 * e + 2 * t), k1 = warp * 16 + key_of<true>(8 * e + 2 * t + 1);
-            const uint32_t v0 = stage + C::KB;
-            if constexpr (D == 128) {
-              const uint2 x = lds64(v0 + k0 * 64 + ((r ^ ((k0 & 2) << 1)) * 8));
-              const uint2 y = lds64(v0 + k1 * 64 + ((r ^ ((k1 & 2) << 1)) * 8));
-              vw[e][0] = __byte_perm(x.x, y.x, 0x5410);
-              vw[e][1] = __byte_perm(x.x, y.x, 0x7632);
-              vw[e][2] = __byte_perm(x.y, y.y, 0x5410);
-              vw[e][3] = __byte_perm(x.y, y.y, 0x7632);
-            } else {
-              const uint32_t x = lds32(v0 + k0 * 32 + r * 4), y = lds32(v0 + k1 * 32 + r * 4);
-              vw[e][0] = __byte_perm(x, y, 0x5410);
-              vw[e][1] = __byte_perm(x, y, 0x7632);
-            }
-          }
-#pragma unroll
-          for (int g = 0; g < G; ++g) {
-            uint32_t a[2][4];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              // fp16 bit patterns 1024 + n and 1024 + 16 n; exact down to n - 8 = code
-              const uint32_t x = vw[e][g], y = x >> 8;
-              a[0][2 * e] = hadd2((x & 0x000F000Fu) | 0x64006400u, 0xE408E408u);
-              a[0][2 * e + 1] = hfma2((x & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
-              a[1][2 * e] = hadd2((y & 0x000F000Fu) | 0x64006400u, 0xE408E408u);
-              a[1][2 * e + 1] = hfma2((y & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
-            }
-            const float sa = ((g & 1) ? bf16hi_to_f32(vs[0][g / 2]) : bf16lo_to_f32(vs[0][g / 2])) * vmul[g];
-            const float sb = ((g & 1) ? bf16hi_to_f32(vs[1][g / 2]) : bf16lo_to_f32(vs[1][g / 2])) * vmul[g];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint32_t b0 = movm(pack_f16x2(s[nt][0] * sa, s[nt][1] * sa));
-              const uint32_t b1 = movm(pack_f16x2(s[nt][2] * sb, s[nt][3] * sb));
-              mma_f16(o[nt][2 * g], a[0], b0, b1);
-              mma_f16(o[nt][2 * g + 1], a[1], b0, b1);
-            }
-          }
-        } else {
-          // p as the sum of two bf16: rounded once, its error would be as large as that of the
-          // bf16 output itself
-          uint32_t ph[NT][2], pl[NT][2];
+        for (int u = 0; u < BPW; ++u)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t x = pack_bf16x2(s[nt][2 * e], s[nt][2 * e + 1]);
-              ph[nt][e] = movm(x);
-              pl[nt][e] = movm(pack_bf16x2(s[nt][2 * e] - bf16lo_to_f32(x), s[nt][2 * e + 1] - bf16hi_to_f32(x)));
+            for (int e = 0; e < 4; ++e) {
+              s[u][nt][e] = ex2_approx(fmaf(s[u][nt][e], c2[nt][e & 1], nm[nt][e & 1]));
+              l[nt][e & 1] += s[u][nt][e];
             }
-          uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};  // rows behind the length may hold anything, NaN too
-          if (edge) {
+        // ---- O^T += V^T P^T ----
+#pragma unroll
+        for (int u = 0; u < BPW; ++u) {
+          const int blk = warp * (16 * BPW) + 16 * u;
+          if constexpr (Q4) {
+            uint32_t vw[2][G];  // keys (2t, 2t + 1), (2t + 8, 2t + 9): 4 nibbles of each per group
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int n = n0 + 8 * e + 2 * t;
-              keep[e] = (n >= w.s.first && n < w.s.L ? 0xFFFFu : 0u) |
-                        (n + 1 >= w.s.first && n + 1 < w.s.L ? 0xFFFF0000u : 0u);
+              const int k0 = blk + key_of<true>(8 * e + 2 * t), k1 = blk + key_of<true>(8 * e + 2 * t + 1);
+              const uint32_t v0 = stage + C::KB;
+              if constexpr (D == 128) {
+                const uint2 x = lds64(v0 + k0 * 64 + ((r ^ ((k0 & 2) << 1)) * 8));
+                const uint2 y = lds64(v0 + k1 * 64 + ((r ^ ((k1 & 2) << 1)) * 8));
+                vw[e][0] = __byte_perm(x.x, y.x, 0x5410);
+                vw[e][1] = __byte_perm(x.x, y.x, 0x7632);
+                vw[e][2] = __byte_perm(x.y, y.y, 0x5410);
+                vw[e][3] = __byte_perm(x.y, y.y, 0x7632);
+              } else {
+                const uint32_t x = lds32(v0 + k0 * 32 + r * 4), y = lds32(v0 + k1 * 32 + r * 4);
+                vw[e][0] = __byte_perm(x, y, 0x5410);
+                vw[e][1] = __byte_perm(x, y, 0x7632);
+              }
             }
-          }
-          const int row = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
-          for (int k = 0; k < MT; ++k) {
-            uint32_t a[4];
-            ldsm4t(a, stage + C::KB + (k / 4) * (kTile * 128) + row * 128 +
-                          ((((k & 3) * 2 + ((lane >> 3) & 1)) ^ (row & 7)) * 16));
+            for (int g = 0; g < G; ++g) {
+              uint32_t a[2][4];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) nibbles(vw[e][g], a[0][2 * e], a[0][2 * e + 1], a[1][2 * e], a[1][2 * e + 1]);
+              const float sa = ((g & 1) ? bf16hi_to_f32(vs[u][0][g / 2]) : bf16lo_to_f32(vs[u][0][g / 2])) * vmul[g];
+              const float sb = ((g & 1) ? bf16hi_to_f32(vs[u][1][g / 2]) : bf16lo_to_f32(vs[u][1][g / 2])) * vmul[g];
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const uint32_t b0 = movm(pack_f16x2(s[u][nt][0] * sa, s[u][nt][1] * sa));
+                const uint32_t b1 = movm(pack_f16x2(s[u][nt][2] * sb, s[u][nt][3] * sb));
+                mma_f16(o[nt][2 * g], a[0], b0, b1);
+                mma_f16(o[nt][2 * g + 1], a[1], b0, b1);
+              }
+            }
+          } else {
+            // p as the sum of two bf16: rounded once, its error would be as large as that of the
+            // bf16 output itself
+            uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float a = s[u][nt][2 * e], b = s[u][nt][2 * e + 1];
+                const uint32_t x = pack_bf16x2(a, b);
+                ph[nt][e] = movm(x);
+                pl[nt][e] = movm(pack_bf16x2(a - bf16lo_to_f32(x), b - bf16hi_to_f32(x)));
+              }
+            uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};  // rows behind the length may hold anything, NaN too
             if (edge) {
-              a[0] &= keep[0], a[1] &= keep[0];
-              a[2] &= keep[1], a[3] &= keep[1];
-            }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_bf16(o[nt][k], a, ph[nt][0], ph[nt][1]);
-              mma_bf16(o[nt][k], a, pl[nt][0], pl[nt][1]);
+              for (int e = 0; e < 2; ++e) {
+                const int n = n0 + 16 * u + 8 * e + 2 * t;
+                keep[e] = !loaded[u] ? 0u : (n >= w.s.first && n < w.s.L ? 0xFFFFu : 0u) |
+                                            (n + 1 >= w.s.first && n + 1 < w.s.L ? 0xFFFF0000u : 0u);
+              }
+            }
+            const int row = blk + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+            for (int k = 0; k < MT; ++k) {
+              uint32_t a[4];
+              ldsm4t(a, stage + C::KB + (k / 4) * (C::TILE * 128) + row * 128 +
+                            ((((k & 3) * 2 + ((lane >> 3) & 1)) ^ (row & 7)) * 16));
+              if (edge) {
+                a[0] &= keep[0], a[1] &= keep[0];
+                a[2] &= keep[1], a[3] &= keep[1];
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma_bf16(o[nt][k], a, ph[nt][0], ph[nt][1]);
+                mma_bf16(o[nt][k], a, pl[nt][0], pl[nt][1]);
+              }
             }
           }
         }
@@ -698,7 +752,7 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], off);
         if (r == 0) {
-          ctl->m[warp][nt * 8 + 2 * t + e] = m[nt][e];
+          ctl->m[warp][nt * 8 + 2 * t + e] = th[nt][e] == kNegInf ? kNegInf : -nm[nt][e];
           ctl->l[warp][nt * 8 + 2 * t + e] = l[nt][e];
         }
       }
@@ -718,7 +772,7 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
         for (int k = 0; k < kWarps; ++k) y += ctl->l[k][j] * ex2_approx(ctl->m[k][j] - bs);
         M[nt][e] = x;
         total[nt][e] = y;
-        const float f = ex2_approx(m[nt][e] - bs);
+        const float f = th[nt][e] == kNegInf ? 0.f : ex2_approx(-nm[nt][e] - bs);
 #pragma unroll
         for (int k = 0; k < MT; ++k) {
           const float fk = Q4 ? f * __fdiv_rn(1.f, vmul[Q4 ? k / 2 : 0]) : f;
@@ -815,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, Q4>::CTAS)
   for (int b = tid * share; b < min(B, (tid + 1) * share); ++b) {
     const int L = __ldg(p.lens + b);
     if (blockIdx.x == 0 && (L < 0 || L > p.cache.cap)) atomicOr(p.status, kDevPageRange);
-    mine += span_of(p, b).nt;
+    mine += span_of<C::TILE>(p, b).nt;
   }
   int64_t tiles;
   int64_t before = block_prefix<kThreads>(mine, ctl->wsum, &tiles);
@@ -825,37 +879,38 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, Q4>::CTAS)
   if (lo < hi && before * p.items <= lo && lo < (before + mine) * p.items) {
     int b = tid * share;
     for (;; ++b) {
-      const int nt = span_of(p, b).nt;
+      const int nt = span_of<C::TILE>(p, b).nt;
       if (lo < (before + nt) * p.items) break;
       before += nt;
     }
     ctl->b0 = b;
     ctl->rem0 = static_cast<int>(lo - before * p.items);
   }
+  // every CTA is resident by now: combine_kernel may come in and find its own place in the work
+  // while this grid runs (what both read was complete before this grid's wait returned)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncthreads();
   if (lo < hi) {
-    Walk w(p, ctl->b0, ctl->rem0, static_cast<int>(hi - lo));
+    Walk<C::TILE> w(p, ctl->b0, ctl->rem0, static_cast<int>(hi - lo));
     if (tid >= kConsumers) produce<D, NT, Q4>(p, smem, ctl, w);
     else consume<D, NT, Q4>(p, smem, ctl, w);
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Joins the segments of items that more than one CTA walked, and writes the rows of empty
 // sequences. One CTA per (sequence, query head), thread = output element.
-template <int D>
+template <int D, int TILE>
 __global__ void __launch_bounds__(D) paged_combine_kernel(const __grid_constant__ PagedDecodeParams p) {
   __shared__ int64_t wsum[D / 32];
   __shared__ float w_sh[kPagedMaxCtas];
   __shared__ float red[D / 32];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int rows = p.head_rows;
   // tiles of all sequences, and of those before b
   int64_t all = 0, pre = 0;
   for (int i = tid; i < p.cache.B; i += D) {
-    const int nt = span_of(p, i).nt;
+    const int nt = span_of<TILE>(p, i).nt;
     all += nt;
     if (i < b) pre += nt;
   }
@@ -863,8 +918,10 @@ __global__ void __launch_bounds__(D) paged_combine_kernel(const __grid_constant_
   block_prefix<D>(all, wsum, &tiles);
   __syncthreads();
   block_prefix<D>(pre, wsum, &before);
-  const int nt = span_of(p, b).nt;
+  const int nt = span_of<TILE>(p, b).nt;
   __nv_bfloat16* out = p.out + b * p.o_sb + h * p.o_sh + tid;
+  // partial rows, and the order of writes to out and lse against earlier kernels, from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (nt == 0) {
     *out = __float2bfloat16_rn(0.f);
     if (p.lse && tid == 0) p.lse[blockIdx.x] = kNegInf;
@@ -960,7 +1017,7 @@ cudaError_t launch(PagedDecodeParams p, cudaStream_t stream) {
   cfg.gridDim = dim3(p.cache.B * p.Hq);
   cfg.blockDim = dim3(D);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D>, p);
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, C::TILE>, p);
 }
 
 template <int D, int NT, bool Q4>
@@ -985,8 +1042,13 @@ cudaError_t launch_paged_decode(const PagedDecodeParams& p, int d, int format, c
   return AFX_PAGED_DISPATCH(launch, p, stream);
 }
 
-int paged_frag_rows(int page_size) {
-  int a = page_size, b = kTile;
+template <int D, int NT, bool Q4>
+int tile() {
+  return Cfg<D, NT, Q4>::TILE;
+}
+
+int paged_frag_rows(int page_size, int d, int g, int format) {
+  int a = page_size, b = AFX_PAGED_DISPATCH(tile);
   while (b) {
     const int r = a % b;
     a = b;
