@@ -54,8 +54,9 @@ struct PagedAppendParams {
   int64_t k_sb, k_sh, k_sn, v_sb, v_sh, v_sn;
   const int32_t *first, *count;     // [B]; count may be null: every sequence has N rows
   int N;
-  int64_t rows;                     // B * N
-  int hb;                           // heads of a block (set by the launcher)
+  int64_t rows;                     // B * N, below 2^31
+  uint64_t div_n;                   // ceil(2^64 / N): row / N as a multiplication; 0 for N = 1
+  int hb, rb_log2;                  // heads and (log2) rows of a block, set by the launcher
   PagedFreqs freqs;
   int* status;
 };
@@ -66,6 +67,7 @@ struct PagedGatherParams {
   const int32_t *first, *count;     // [B]; first may be null (0), count too (N)
   int N;
   int64_t rows;
+  uint64_t div_n;
   int heads_per_thread;
   int* status;
 };
@@ -90,6 +92,7 @@ struct PagedDecodeParams {
   float2* part_ml;                  // (max in log2 units, sum)
   int ctas, head_rows;              // query heads per item
   int chunks, items;                // items per KV head, and per sequence
+  int comb_by_run, comb_heads;      // the combine kernel's blocks
   PagedFreqs freqs;
   int* status;
 };

@@ -172,6 +172,7 @@ attnfuse_status attnfuse_paged_append(const attnfuse_paged_cache* cache, const v
   p.count = count;
   p.N = N;
   p.rows = (int64_t)cache->B * N;
+  p.div_n = N > 1 ? ~0ull / N + 1 : 0;  // ceil(2^64 / N)
   if (mode == ATTNFUSE_ROPE_FUSED) p.freqs = paged_freqs(cache->d, rope_theta);
   return done(launch_paged_append(p, cache->d, cache->format, mode == ATTNFUSE_ROPE_FUSED, stream),
               "paged append launch");
@@ -198,6 +199,7 @@ attnfuse_status attnfuse_paged_gather(const attnfuse_paged_cache* cache, const i
   p.count = count;
   p.N = N;
   p.rows = (int64_t)cache->B * N;
+  p.div_n = N > 1 ? ~0ull / N + 1 : 0;  // ceil(2^64 / N)
   return done(launch_paged_gather(p, cache->d, cache->format, stream), "paged gather launch");
 }
 

@@ -15,6 +15,11 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Sequence and row of row number `row` < 2^31 of the call.
+__device__ __forceinline__ int seq_of(uint64_t div_n, int64_t row) {
+  return static_cast<int>(div_n ? __umul64hi(static_cast<uint64_t>(row), div_n) : row);
+}
+
 // Row of this thread: sequence b, row n of the call, position pos; false if there is none.
 struct RowAt {
   int b, n, page, slot;
@@ -57,12 +62,12 @@ struct Place {
 };
 template <int TPR>
 __device__ __forceinline__ Place place_of(const PagedAppendParams& p) {
-  const int rb = kThreads / TPR / p.hb;
+  const int lb = p.rb_log2, k = threadIdx.x / TPR;
   Place w;
   w.t = threadIdx.x % TPR;
-  w.rr = threadIdx.x / TPR % rb;
-  w.row = static_cast<int64_t>(blockIdx.x) * rb + w.rr;
-  w.h = blockIdx.y * p.hb + threadIdx.x / TPR / rb;
+  w.rr = k & ((1 << lb) - 1);
+  w.row = (static_cast<int64_t>(blockIdx.x) << lb) + w.rr;
+  w.h = blockIdx.y * p.hb + (k >> lb);
   return w;
 }
 
@@ -75,12 +80,11 @@ __device__ __forceinline__ int pair_of(int k, int t) {
 template <int D, int TPR, bool Q4>
 __device__ __forceinline__ void block_angles(const PagedAppendParams& p, float4* ang) {
   constexpr int K = D / 2 / TPR;  // pairs per thread of a row
-  const int rb = kThreads / TPR / p.hb;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rb;
-  for (int i = threadIdx.x; i < rb * (D / 2); i += kThreads) {
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) << p.rb_log2;
+  for (int i = threadIdx.x; i < (D / 2) << p.rb_log2; i += kThreads) {
     const int64_t row = row0 + i / (D / 2);
     if (row >= p.rows) break;
-    const int j = i % (D / 2), b = static_cast<int>(row / p.N), n = static_cast<int>(row - static_cast<int64_t>(b) * p.N);
+    const int j = i % (D / 2), b = seq_of(p.div_n, row), n = static_cast<int>(row - static_cast<int64_t>(b) * p.N);
     if (p.count && n >= __ldg(p.count + b)) continue;
     const int64_t pos = static_cast<int64_t>(__ldg(p.first + b)) + n;
     if (pos < 0 || pos >= p.cache.cap) continue;
@@ -114,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) append_bf16_kernel(const __grid_cons
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Place w = place_of<CP>(p);
   const bool in = w.row < p.rows && w.h < p.cache.Hkv;
-  const int b = in ? static_cast<int>(w.row / p.N) : 0;
+  const int b = in ? seq_of(p.div_n, w.row) : 0;
   const int n = in ? static_cast<int>(w.row - static_cast<int64_t>(b) * p.N) : 0;
   RowAt r;
   const bool live = in && n < live_rows(p.count, b, p.N, p.status) &&
@@ -187,7 +191,7 @@ __global__ void __launch_bounds__(kThreads) append_q4_kernel(const __grid_consta
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Place w = place_of<8>(p);
   const bool in = w.row < p.rows && w.h < p.cache.Hkv;
-  const int b = in ? static_cast<int>(w.row / p.N) : 0;
+  const int b = in ? seq_of(p.div_n, w.row) : 0;
   const int n = in ? static_cast<int>(w.row - static_cast<int64_t>(b) * p.N) : 0;
   RowAt r = {};
   const bool live = in && n < live_rows(p.count, b, p.N, p.status) &&
@@ -269,7 +273,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / TPR) + threadIdx.x / TPR;
   const int t = threadIdx.x % TPR;
   if (row >= p.rows) return;
-  const int b = static_cast<int>(row / p.N), n = static_cast<int>(row - static_cast<int64_t>(b) * p.N);
+  const int b = seq_of(p.div_n, row), n = static_cast<int>(row - static_cast<int64_t>(b) * p.N);
   RowAt r;
   const bool live = n < live_rows(p.count, b, p.N, p.status) &&
                     find_row(p.cache, b, n, p.first ? __ldg(p.first + b) : 0, p.status, &r);
@@ -343,6 +347,8 @@ cudaError_t launch_paged_append(PagedAppendParams p, int d, int format, bool rop
   const int tpr = format == kPagedQ4 ? 8 : d / 16;
   p.hb = append_heads(p.cache.Hkv);
   const int rb = kThreads / tpr / p.hb;
+  p.rb_log2 = 0;
+  while (1 << p.rb_log2 < rb) ++p.rb_log2;  // a power of two, as its factors
   void (*kern)(PagedAppendParams) = nullptr;
   if (format == kPagedQ4)
     kern = d == 128 ? (rope ? append_q4_kernel<128, true> : append_q4_kernel<128, false>)

@@ -3,24 +3,33 @@
 //   O_h = sum_n p_n v_n,  p = softmax over n in [max(0, L - W), L) of
 //   s_n = scale <R_{L-1} q_h, k_n> + slope_h (n - (L - 1)),  L = lens[b].
 //
-// The cache is read once, from HBM, and that bounds the kernel: 2 d g multiply-adds per pair of
-// K and V elements is far below what the tensor cores do meanwhile, on either path. So the
-// matrix instructions are warp-level ones with the KEYS as rows (S^T = K Q^T, O^T = V^T P^T):
-// their operands come straight from registers, which is where 4-bit codes have to be expanded
-// (writing them back to shared memory as bf16 for tcgen05 would move 94 of the 128 bytes per
-// cycle that shared memory has, and as much again to read them), and a group of 8 query heads
-// fills the instruction's 8 columns, where a 128-row query tile would be padding.
+// The cache is read once, from HBM, and that bounds the bf16 kernel (8 sequences of 32768 keys,
+// Hq = 64, Hkv = 8, d = 128: 164 us, 97% of a copy's rate). The matrix instructions are warp-level
+// ones with the KEYS as rows (S^T = K Q^T, O^T = V^T P^T): their operands come straight from
+// registers, which is where 4-bit codes have to be expanded (writing them back to shared memory as
+// 16-bit values for tcgen05 would move 94 of the 128 bytes per cycle that shared memory has, and as
+// much again to read them), and a group of 8 query heads fills the instruction's 8 columns, where
+// a 128-row query tile would be padding.
 //
-// Work. Sequences are cut into 64-key tiles; the tiles of the whole batch, ordered by (sequence,
-// KV head, chunk of query heads), are dealt to the CTAs in equal runs, from lengths read on the
-// device. A CTA walks the segments of its run. A segment that is a whole item (all tiles of one
-// (sequence, head chunk)) is finished in place; otherwise its (max, sum, acc) goes to the
-// workspace, at most two per CTA, and combine_kernel joins them in a fixed order.
+// The 4-bit kernel (the same sequences: 86 us, 52% of a copy's rate) is bound by its arithmetic.
+// Measured on GB300, a warp-level product takes a sub-partition 8 cycles and no FMA-pipe
+// instruction runs beside it (packed fp16 takes that pipe 2 cycles), while integer logic (2 cycles
+// each) does. So codes are expanded by logic alone, and what that leaves out, the offset of the
+// codes, is taken out by products of a constant.
 //
-// CTA: 4 consumer warps, each with 16 keys of every tile and its own running (max, sum, acc)
-// (joined once per segment), and a producer warp that looks pages up and fills a ring of tiles:
-// TMA boxes of one page's rows (bf16, 128-byte swizzle) or bulk copies (q4: codes and steps of a
-// page's rows are contiguous).
+// Work. Sequences are cut into tiles of 64 or 128 keys; the tiles of the whole batch, ordered by
+// (sequence, KV head, chunk of query heads), are dealt to the CTAs in equal runs, from lengths read
+// on the device; an item counts for its tiles and for what its two ends cost (without that, 64
+// sequences of 1 to 8192 keys took 121 us from the 4-bit cache, with it 98). A CTA walks the
+// segments of its run. A segment that is a whole item (all tiles of one (sequence, head chunk)) is
+// finished in place; otherwise its (max, sum, acc) goes to the workspace, at most two per CTA, and
+// the combine kernel joins them in a fixed order.
+//
+// CTA: 4 consumer warps, each with its own keys of every tile and its own running (max, sum, acc)
+// (joined once per segment), and a producer warp that looks pages up and fills a ring of tiles: TMA
+// boxes of one page's rows (bf16, 128-byte swizzle) or bulk copies (q4: codes and steps of a
+// page's rows are contiguous). Warps that filled rings of their own, without a producer, took 8%
+// (bf16) and 14% (q4) longer.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -45,14 +54,21 @@ struct Cfg {
   // work; rows of 256 bytes (bf16, d = 128) keep the HBM busy with one.
   static constexpr int BPW = Q4 || D == 64 ? 2 : 1;
   static constexpr int TILE = kWarps * 16 * BPW;                        // keys
+  // What the two ends of a segment cost, in tiles: items count as so many more when work is dealt.
+  static constexpr int ENDS = Q4 ? 2 : 1;
   static constexpr uint32_t KB = TILE * (Q4 ? D / 2 : 2 * D);           // K (and V) bytes of a tile
   static constexpr uint32_t SB = Q4 ? TILE * (D / 16) : 0;              // and their steps
   static constexpr uint32_t STAGE = 2 * KB + 2 * SB;
-  static constexpr int STAGES = Q4 ? 3 : (NT == 1 || D == 64 ? 3 : 5);
-  static constexpr int CTAS = Q4 ? (NT == 1 ? 3 : 2) : (NT == 1 || D == 64 ? 2 : 1);
+  // bf16 with one column tile keeps its query operands in registers, the others read them again
+  // for every tile (of 16 heads, d = 128: one CTA per SM with, two CTAs without, 193 and 172 us for
+  // 8 x 32k keys)
+  static constexpr bool QREG = !Q4 && NT == 1;
+  static constexpr int CTAS = Q4 ? (NT == 1 ? 3 : 2) : 2;
+  static constexpr int STAGES = Q4 || (NT == 2 && D == 128) ? 2 : 3;
   static constexpr uint32_t QROW = 2 * D + 16;                          // padded query row
+  static constexpr uint32_t QFRAG = 512 * (D / 32);                     // q4: a column tile's fragments
   static constexpr uint32_t OFF_Q = STAGES * STAGE;
-  static constexpr uint32_t OFF_O = OFF_Q + 2 * ROWS * QROW;            // two warps' accumulators
+  static constexpr uint32_t OFF_O = OFF_Q + (Q4 ? 2 * NT * QFRAG : 3 * ROWS * QROW);  // two warps' accumulators
   static constexpr uint32_t OBUF = (D / 16) * NT * 512;
   static constexpr uint32_t OFF_CTL = OFF_O + 2 * OBUF;
 };
@@ -65,6 +81,8 @@ struct Ctl {
   int rem0;                            // before the run
   int64_t wsum[kThreads / 32];
   float m[kWarps][16], l[kWarps][16];
+  float slope[16];                     // ALiBi slopes over c2
+  float2 qsum[2][4][4];                // q4: minus 8 times the sum of q, per column tile, group, column pair
   float qmax[16][2];                   // q4: largest |q| of a head, by half rows
 };
 
@@ -101,26 +119,37 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The same from zero.
+__device__ __forceinline__ void mma_bf16_0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void mma_f16_0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The same from c0, c1 in both row halves.
+__device__ __forceinline__ void mma_f16_c(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
+                                          float c1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %11, %10, %11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t w;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
   return w;
-}
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
@@ -189,46 +218,72 @@ __device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t* wsum, int64_
   return before + x - v;
 }
 
-// The run of CTA i over T units and the CTA that a unit belongs to, where G = min(CTAs, T) CTAs
-// share the units (so no run is empty).
-__device__ __forceinline__ int sharers(int64_t T, int ctas) { return T < ctas ? static_cast<int>(T) : ctas; }
-__device__ __forceinline__ int64_t run_start(int64_t T, int i, int G) { return T * i / G; }
-__device__ __forceinline__ int run_of(int64_t T, int64_t unit, int G) {
-  return static_cast<int>(((unit + 1) * G - 1) / T);
+__device__ __forceinline__ int64_t div_units(int64_t a, int64_t b) {  // a / b, a >= 0, b > 0
+  return (a | b) >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
 }
 
-// Walks the segments of a run: all roles step through the same ones.
-template <int TILE>
+// T units in equal runs over min(ctas, T) CTAs, so that no run is empty; the first `more` runs are
+// one unit longer.
+struct Deal {
+  int64_t each, more;
+  int runs;
+  __device__ Deal(int64_t T, int ctas) {
+    runs = T < ctas ? static_cast<int>(T) : ctas;
+    each = runs ? div_units(T, runs) : 0;
+    more = T - each * runs;
+  }
+  __device__ int64_t start(int i) const { return i * each + min(static_cast<int64_t>(i), more); }
+  __device__ int run_of(int64_t unit) const {
+    const int64_t longer = more * (each + 1);
+    return static_cast<int>(unit < longer ? div_units(unit, each + 1) : more + div_units(unit - longer, each));
+  }
+};
+
+// An item is `ends` units without tiles, then one per tile.
+template <class C>
+__device__ __forceinline__ int units_of(const Span& s) {
+  return s.nt ? s.nt + C::ENDS : 0;
+}
+
+// Walks the segments of a run that have tiles: all roles step through the same ones.
+template <class C>
 struct Walk {
   const PagedDecodeParams& p;
   Span s;
-  int b, hh, t, left, n;  // item (b, hh), first tile of the segment (within the item), its tiles
-  bool head;              // the segment starts the run
-  __device__ Walk(const PagedDecodeParams& p_, int b0, int rem0, int left_) : p(p_), b(b0), left(left_), head(true) {
-    n = 0;
+  int b, hh, u, left;     // item (b, hh), and in units: where in it the run goes on, what the run has left
+  int t, n;               // first tile of the segment (within the item), its tiles
+  bool head;              // the segment is the run's first
+  __device__ Walk(const PagedDecodeParams& p_, int b0, int rem0, int left_) : p(p_), b(b0), left(left_), n(0), head(true) {
     if (left <= 0) return;
-    s = span_of<TILE>(p, b);
-    hh = rem0 / s.nt;
-    t = rem0 - hh * s.nt;
-    n = min(left, s.nt - t);
+    s = span_of<C::TILE>(p, b);
+    hh = rem0 / units_of<C>(s);
+    u = rem0 - hh * units_of<C>(s);
+    find();
   }
   __device__ bool live() const { return n > 0; }
-  __device__ bool whole() const { return t == 0 && n == s.nt; }
+  __device__ bool whole() const { return n == s.nt; }
   __device__ void next() {
-    left -= n;
     head = false;
-    t += n;
-    n = 0;
-    if (left <= 0) return;
-    if (t == s.nt) {
-      t = 0;
-      if (++hh == p.items) {
-        hh = 0;
-        do s = span_of<TILE>(p, ++b);
-        while (s.nt == 0);
+    find();
+  }
+
+ private:
+  __device__ void find() {
+    for (n = 0; n == 0 && left > 0;) {
+      if (u == units_of<C>(s)) {
+        u = 0;
+        if (++hh == p.items) {
+          hh = 0;
+          do s = span_of<C::TILE>(p, ++b);
+          while (s.nt == 0);
+        }
       }
+      const int take = min(left, units_of<C>(s) - u);
+      t = max(0, u - C::ENDS);
+      n = max(0, u + take - C::ENDS) - t;
+      u += take;
+      left -= take;
     }
-    n = min(left, s.nt - t);
   }
 };
 
@@ -237,13 +292,14 @@ struct Walk {
 // ---------------------------------------------------------------------------------------------
 template <int D, int NT, bool Q4>
 __device__ __forceinline__ void produce(const PagedDecodeParams& p, uint8_t* smem, Ctl* ctl,
-                                        Walk<Cfg<D, NT, Q4>::TILE> w) {
+                                        Walk<Cfg<D, NT, Q4>> w) {
   using C = Cfg<D, NT, Q4>;
   constexpr int kTile = C::TILE;
   const int lane = threadIdx.x % 32;
   const PagedDev& c = p.cache;
   const int F = p.frag_rows, nf = kTile / F;
-  int it = 0;
+  int it = 0, st = 0;
+  uint32_t phase = 1;  // of `empty`: the first round finds every stage free
   bool ok = true;
   for (; w.live() && ok; w.next()) {
     const int kvh = w.hh / p.chunks;
@@ -262,16 +318,14 @@ __device__ __forceinline__ void produce(const PagedDecodeParams& p, uint8_t* sme
     bool bad, bad_n;
     int page = look(base + lane, &slot, &bad);
     int page_n = look(base + 32 + lane, &slot_n, &bad_n);
-    for (int i = 0; i < w.n; ++i, ++it) {
+    for (int i = 0; i < w.n; ++i, ++it, st = st + 1 == C::STAGES ? 0 : st + 1, phase ^= st == 0) {
       const int f0 = (w.s.t0 + w.t + i) * nf;
       if (f0 == base + 32) {
         base += 32;
         page = page_n, slot = slot_n, bad = bad_n;
         page_n = look(base + 32 + lane, &slot_n, &bad_n);
       }
-      const int st = it % C::STAGES;
-      if (it >= C::STAGES)
-        ok = mbar_wait(&ctl->empty[st], ((it / C::STAGES) - 1) & 1, p.status, &ctl->abort_flag);
+      if (it >= C::STAGES) ok = mbar_wait(&ctl->empty[st], phase, p.status, &ctl->abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const int src = (f0 - base + lane) & 31;
@@ -329,29 +383,32 @@ __device__ __forceinline__ int key_of(int i) {
   return (i & 8) + ((j & 1) ? 4 + ((j >> 1) ^ 1) : j >> 1);
 }
 
-// A word of 4 nibbles n (bits 4i, in both halves) -> the fp16 pairs of n - 8. Set into the mantissa
-// of 1024, a nibble at bits 0-3 makes 1024 + n and one at bits 4-7 makes 1024 + 16 n; one
-// fp16 operation, exact, takes that to n - 8.
-__device__ __forceinline__ void nibbles(uint32_t x, uint32_t& a0, uint32_t& a1, uint32_t& a2, uint32_t& a3) {
-  const uint32_t y = x >> 8;
-  a0 = hadd2((x & 0x000F000Fu) | 0x64006400u, 0xE408E408u);
-  a1 = hfma2((x & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
-  a2 = hadd2((y & 0x000F000Fu) | 0x64006400u, 0xE408E408u);
-  a3 = hfma2((y & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
+// A word of 4 nibbles n (bits 4i, in both halves) as fp16 pairs, by bits alone: a nibble moved to
+// bits 2-5 is the subnormal n 2^-22, one at bits 6-9 is n 2^-18 (whose q carry 1/16). What enters
+// a product so is n = code + 8; the 8 is taken out by another product, of the constant 8. (At
+// bits 0-3 and 4-7 one shift would do for two, but products of numbers that far below the type's
+// normal range lose bits in the tensor core: scores were off by 1.5e-6 instead of 4e-7.)
+__device__ __forceinline__ void raw_nibbles(uint32_t x, uint32_t& a0, uint32_t& a1, uint32_t& a2, uint32_t& a3) {
+  const uint32_t y = x << 2, z = x >> 6;
+  a0 = y & 0x003C003Cu;
+  a1 = y & 0x03C003C0u;
+  a2 = z & 0x003C003Cu;
+  a3 = z & 0x03C003C0u;
 }
 
-// q4: the power of two that takes the largest |q| of head j to [1/2, 1) (or its reciprocal).
+// q4: the power of two that takes the largest |q| of head j to [2^14, 2^15) (or 2^22 over it, what
+// turns a product with raw nibbles back into q).
 template <int D>
-__device__ __forceinline__ float q_scale(const Ctl* ctl, int j, bool down) {
+__device__ __forceinline__ float q_scale(const Ctl* ctl, int j, bool up) {
   const float m = D == 128 ? fmaxf(ctl->qmax[j][0], ctl->qmax[j][1]) : ctl->qmax[j][0];
-  const uint32_t ex = __float_as_uint(m) >> 23;                 // biased; 0: zero or subnormal, 255: not finite
-  const uint32_t e = ex == 0 || ex == 255 ? 126u : min(ex, 252u);  // 2^(e - 126) > m
-  return __uint_as_float((down ? 253u - e : 1u + e) << 23);
+  const uint32_t ex = __float_as_uint(m) >> 23;  // biased; 0: zero or subnormal, 255: not finite
+  const uint32_t e = ex == 0 || ex == 255 ? 127u : min(max(ex, 16u), 240u);  // m in [2^(e - 127), 2^(e - 126))
+  return __uint_as_float((up ? 127u + 14u + 127u - e : 127u + 22u - 14u + e - 127u) << 23);
 }
 
 template <int D, int NT, bool Q4>
 __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* smem, Ctl* ctl,
-                                        Walk<Cfg<D, NT, Q4>::TILE> w) {
+                                        Walk<Cfg<D, NT, Q4>> w) {
   using C = Cfg<D, NT, Q4>;
   constexpr int BPW = C::BPW;
   constexpr int KS = D / 16;       // 16-element steps of a row
@@ -360,13 +417,32 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
   constexpr int JS = kConsumers / (D / 2), JN = C::ROWS / JS;  // query heads a thread prepares
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, r = lane / 4, t = lane % 4;
   const uint32_t base = smem_u32(smem);
-  int it = 0;
+  // this lane's places in a stage, block 0 of its warp; block u and keys + 8 are constants away
+  constexpr int RB = Q4 ? D / 2 : 128;  // bytes of a row (bf16: of a 64-element panel)
+  const int ka = key_of<Q4>(r), kb = ka + 8;  // the keys of its S rows r and r + 8
+  uint32_t koff, soff = 0, voff, voff1 = 0;
+  {
+    const uint32_t wrow = warp * (16 * BPW);
+    if constexpr (Q4) {
+      const int k0 = key_of<true>(2 * t), k1 = key_of<true>(2 * t + 1);  // its V rows 2t, 2t + 1
+      koff = (wrow + ka) * RB + (D == 128 ? (t ^ (ka & 2)) * 16 : t * 8);
+      soff = 2 * C::KB + (wrow + ka) * (D / 16);
+      voff = C::KB + (wrow + k0) * RB + (D == 128 ? (r ^ ((k0 & 2) << 1)) * 8 : r * 4);
+      voff1 = C::KB + (wrow + k1) * RB + (D == 128 ? (r ^ ((k1 & 2) << 1)) * 8 : r * 4);
+    } else {
+      // chunk index c ^ (row & 7): c = 2 (k & 3) + 0 or 1 enters as an exclusive or of 32 (k & 3)
+      koff = (wrow + (lane & 15)) * RB + (((lane >> 4) ^ (lane & 7)) * 16);
+      voff = C::KB + (wrow + (lane & 7) + ((lane >> 4) << 3)) * RB + ((((lane >> 3) & 1) ^ (lane & 7)) * 16);
+    }
+  }
+  int st = 0;
+  uint32_t phase = 0;
   bool ok = true;
   for (; w.live(); w.next()) {
     const int kvh = w.hh / p.chunks, h0 = kvh * p.g + (w.hh % p.chunks) * C::ROWS;
     const int rows = min(C::ROWS, kvh * p.g + p.g - h0);
-    // ---- the item's queries, rotated in fp32 and kept as the sum of two 16-bit parts: bf16 (16
-    // bits), or for q4 fp16 after a power of two per head has brought the largest to [1/2, 1) ----
+    // ---- the item's queries, rotated in fp32 and kept as the sum of 16-bit parts: three of bf16,
+    // or for q4 two of fp16 after a power of two per head has taken the largest to [2^14, 2^15) ----
     {
       const int i = tid % (D / 2), j0 = tid / (D / 2);
       float x[JN], y[JN];
@@ -401,74 +477,97 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
 #pragma unroll
       for (int k = 0; k < JN; ++k) {
         const int j = j0 + k * JS;
-        uint16_t* hi = reinterpret_cast<uint16_t*>(smem + C::OFF_Q + j * C::QROW);
-        uint16_t* lo = reinterpret_cast<uint16_t*>(smem + C::OFF_Q + (C::ROWS + j) * C::QROW);
         if constexpr (Q4) {
+          // element c of head j goes where the lane that feeds it to the product reads 16 bytes per
+          // group: lane 4 (j % 8) + (c % 32) / 8, pairs (e, e + 4) of its 8 elements
           const float f = q_scale<D>(ctl, j, true);
-          const float u = x[k] * f, v = y[k] * f;
+          const float f16 = (i & 1) ? f * 0.0625f : f;  // elements 1 and 3 of 4 meet 16 times their nibble
+          const float u = x[k] * f16, v = y[k] * f16;
           const __half a = __float2half_rn(u), b = __float2half_rn(v);
-          hi[i] = __half_as_ushort(a);
-          hi[i + D / 2] = __half_as_ushort(b);
-          lo[i] = __half_as_ushort(__float2half_rn(u - __half2float(a)));
-          lo[i + D / 2] = __half_as_ushort(__float2half_rn(v - __half2float(b)));
+          uint8_t* at = smem + C::OFF_Q + (j / 8) * C::QFRAG + (i / 32) * 512 + ((j & 7) * 4 + (i & 31) / 8) * 16 +
+                        (i & 3) * 4 + ((i >> 2) & 1) * 2;
+          *reinterpret_cast<__half*>(at) = a;
+          *reinterpret_cast<__half*>(at + D / 64 * 512) = b;
+          *reinterpret_cast<__half*>(at + NT * C::QFRAG) = __float2half_rn(u - __half2float(a));
+          *reinterpret_cast<__half*>(at + NT * C::QFRAG + D / 64 * 512) = __float2half_rn(v - __half2float(b));
         } else {
+          uint16_t* hi = reinterpret_cast<uint16_t*>(smem + C::OFF_Q + j * C::QROW);
+          uint16_t* lo = reinterpret_cast<uint16_t*>(smem + C::OFF_Q + (C::ROWS + j) * C::QROW);
           const __nv_bfloat16 a = __float2bfloat16_rn(x[k]), b = __float2bfloat16_rn(y[k]);
           hi[i] = __bfloat16_as_ushort(a);
           hi[i + D / 2] = __bfloat16_as_ushort(b);
-          lo[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x[k] - __bfloat162float(a)));
-          lo[i + D / 2] = __bfloat16_as_ushort(__float2bfloat16_rn(y[k] - __bfloat162float(b)));
+          const float u = x[k] - __bfloat162float(a), v = y[k] - __bfloat162float(b);
+          const __nv_bfloat16 c = __float2bfloat16_rn(u), d = __float2bfloat16_rn(v);
+          lo[i] = __bfloat16_as_ushort(c);
+          lo[i + D / 2] = __bfloat16_as_ushort(d);
+          uint16_t* rest = reinterpret_cast<uint16_t*>(smem + C::OFF_Q + (2 * C::ROWS + j) * C::QROW);
+          rest[i] = __bfloat16_as_ushort(__float2bfloat16_rn(u - __bfloat162float(c)));
+          rest[i + D / 2] = __bfloat16_as_ushort(__float2bfloat16_rn(v - __bfloat162float(d)));
         }
       }
     }
     named_bar_sync(1, kConsumers);
-    uint32_t qf[2][NT][KS][2];  // [hi, lo]
+    // bf16 keeps the fragments in registers; q4, short of those, reads them again for every tile
+    uint32_t qf[2][NT][C::QREG ? KS : 1][2];  // [hi, lo]
+    if constexpr (C::QREG) {
 #pragma unroll
-    for (int part = 0; part < 2; ++part)
+      for (int part = 0; part < 2; ++part)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const uint32_t row = base + C::OFF_Q + (part * C::ROWS + nt * 8 + r) * C::QROW;
-        if constexpr (Q4) {
-          // group g, step s: the pairs (e, e + 4) of elements 32g + 8t + e, e = 2s and 2s + 1
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint32_t row = base + C::OFF_Q + (part * C::ROWS + nt * 8 + r) * C::QROW;
 #pragma unroll
-          for (int g = 0; g < G; ++g) {
-            const uint4 x = lds128(row + g * 64 + t * 16);
-            qf[part][nt][2 * g][0] = __byte_perm(x.x, x.z, 0x5410);
-            qf[part][nt][2 * g][1] = __byte_perm(x.x, x.z, 0x7632);
-            qf[part][nt][2 * g + 1][0] = __byte_perm(x.y, x.w, 0x5410);
-            qf[part][nt][2 * g + 1][1] = __byte_perm(x.y, x.w, 0x7632);
-          }
-        } else {
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            qf[part][nt][ks][0] = lds32(row + ks * 32 + t * 4);
-            qf[part][nt][ks][1] = lds32(row + ks * 32 + t * 4 + 16);
+          for (int k = 0; k < KS; ++k) {
+            qf[part][nt][k][0] = lds32(row + k * 32 + t * 4);
+            qf[part][nt][k][1] = lds32(row + k * 32 + t * 4 + 16);
           }
         }
-      }
+    }
+    // q4: raw nibbles are code + 8, so each group's sum starts at minus that of 8 everywhere
+    if constexpr (Q4) {
+      const uint32_t eight[4] = {0x00200020u, 0x00200020u, 0x02000200u, 0x02000200u};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          float x[4];
+          const uint4 h = lds128(base + C::OFF_Q + nt * C::QFRAG + g * 512 + lane * 16);
+          const uint4 v = lds128(base + C::OFF_Q + (NT + nt) * C::QFRAG + g * 512 + lane * 16);
+          mma_f16_0(x, eight, h.x, h.y);
+          mma_f16(x, eight, h.z, h.w);
+          mma_f16(x, eight, v.x, v.y);
+          mma_f16(x, eight, v.z, v.w);
+          if (r == 0) ctl->qsum[nt][g][t] = make_float2(-x[0], -x[1]);
+        }
+    }
+    const uint32_t qrest = base + C::OFF_Q + (2 * C::ROWS + r) * C::QROW + t * 4;
     // Scores stay as the matrix product gives them, S; x = S c2 (log2 units). A bias is added as
     // bias / c2, and a score renews the maximum where S > th.
-    float c2[NT][2], slope[NT][2], th[NT][2], nm[NT][2], l[NT][2] = {};
+    float c2[NT][2], th[NT][2], nm[NT][2], l[NT][2] = {};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int j = nt * 8 + 2 * t + e;
         c2[nt][e] = Q4 ? fmaxf(p.scale_log2 * q_scale<D>(ctl, j, false), 1e-44f) : p.scale_log2;
-        slope[nt][e] = p.slopes && j < rows ? __fdiv_rn(__ldg(p.slopes + h0 + j) * kLog2e, c2[nt][e]) : 0.f;
+        // (every warp writes the same values, and reads its own)
+        if (p.slopes && r == 0) ctl->slope[j] = j < rows ? __fdiv_rn(__ldg(p.slopes + h0 + j) * kLog2e, c2[nt][e]) : 0.f;
         th[nt][e] = kNegInf;
         nm[nt][e] = 0.f;  // minus the maximum (log2 units); 0 while there is none (th is -inf then)
       }
+    __syncwarp();
     float o[NT][MT][4] = {};
-    // q4: weights p * step go into fp16 as p * step * vmul[g], vmul = 2^-e of the largest step
+    // q4: O rows r come out 2^-22 and rows r + 8 2^-18 times what they should be. After the products
+    // with 16 keys' n, the same with -8: the sums never carry more than one block's 8 w.
+    const uint32_t minus8[4] = {0x80208020u, 0x82008200u, 0x80208020u, 0x82008200u};
+    // Weights p * step go into fp16 as p * step * vmul[g], vmul = 2^-e of the largest step
     // seen so far in group g (it may be exceeded by 2^4 before it is renewed)
     uint32_t vthr[Q4 ? G / 2 : 1] = {};
     float vmul[Q4 ? G : 1];
 #pragma unroll
     for (int g = 0; g < (Q4 ? G : 1); ++g) vmul[g] = 1.f;
 
-    for (int i = 0; i < w.n; ++i, ++it) {
-      const int st = it % C::STAGES;
-      if (ok) ok = mbar_wait(&ctl->full[st], (it / C::STAGES) & 1, p.status, &ctl->abort_flag);
+    for (int i = 0; i < w.n; ++i, st = st + 1 == C::STAGES ? 0 : st + 1, phase ^= st == 0) {
+      if (ok) ok = mbar_wait(&ctl->full[st], phase, p.status, &ctl->abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) continue;  // unwind through the same barriers as the other warps
       const uint32_t stage = base + st * C::STAGE;
@@ -485,46 +584,55 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
         // ---- scores: s[u][nt][i], key rows r and r + 8 of block u ----
         float s[BPW][NT][4];
         uint32_t vs[BPW][2][Q4 ? G / 2 : 1];  // q4: steps of V's rows r, r + 8 (two bf16 per word)
-        const int ka = key_of<Q4>(r), kb = key_of<Q4>(r + 8);
+        if constexpr (Q4) {
+          uint32_t kw[BPW][2][G], ks[BPW][2][G / 2];
 #pragma unroll
-        for (int u = 0; u < BPW; ++u) {
-          if constexpr (Q4) {
-            uint32_t kw[2][G], ks[2][G / 2];
+          for (int u = 0; u < BPW; ++u)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int key = warp * (16 * BPW) + 16 * u + (e ? kb : ka);
+              const uint32_t kat = stage + koff + (16 * u + 8 * e) * RB, sat = stage + soff + (16 * u + 8 * e) * (D / 16);
               if constexpr (D == 128) {
-                const uint4 x = lds128(stage + key * 64 + ((t ^ (key & 2)) * 16));
-                kw[e][0] = __byte_perm(x.x, x.z, 0x5410);
-                kw[e][1] = __byte_perm(x.x, x.z, 0x7632);
-                kw[e][2] = __byte_perm(x.y, x.w, 0x5410);
-                kw[e][3] = __byte_perm(x.y, x.w, 0x7632);
-                const uint2 y = lds64(stage + 2 * C::KB + key * 8);
-                ks[e][0] = y.x, ks[e][1] = y.y;
-                const uint2 z = lds64(stage + 2 * C::KB + C::SB + key * 8);
+                const uint4 x = lds128(kat);
+                kw[u][e][0] = __byte_perm(x.x, x.z, 0x5410);
+                kw[u][e][1] = __byte_perm(x.x, x.z, 0x7632);
+                kw[u][e][2] = __byte_perm(x.y, x.w, 0x5410);
+                kw[u][e][3] = __byte_perm(x.y, x.w, 0x7632);
+                const uint2 y = lds64(sat);
+                ks[u][e][0] = y.x, ks[u][e][1] = y.y;
+                const uint2 z = lds64(sat + C::SB);
                 vs[u][e][0] = z.x, vs[u][e][1] = z.y;
               } else {
-                const uint2 x = lds64(stage + key * 32 + t * 8);
-                kw[e][0] = __byte_perm(x.x, x.y, 0x5410);
-                kw[e][1] = __byte_perm(x.x, x.y, 0x7632);
-                ks[e][0] = lds32(stage + 2 * C::KB + key * 4);
-                vs[u][e][0] = lds32(stage + 2 * C::KB + C::SB + key * 4);
+                const uint2 x = lds64(kat);
+                kw[u][e][0] = __byte_perm(x.x, x.y, 0x5410);
+                kw[u][e][1] = __byte_perm(x.x, x.y, 0x7632);
+                ks[u][e][0] = lds32(sat);
+                vs[u][e][0] = lds32(sat + C::SB);
               }
             }
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
+          for (int g = 0; g < G; ++g) {
+            uint4 qh[NT], ql[NT];
+            uint2 qs[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              qh[nt] = lds128(base + C::OFF_Q + nt * C::QFRAG + g * 512 + lane * 16);
+              ql[nt] = lds128(base + C::OFF_Q + (NT + nt) * C::QFRAG + g * 512 + lane * 16);
+              qs[nt] = lds64(smem_u32(&ctl->qsum[nt][g][t]));
+            }
+#pragma unroll
+            for (int u = 0; u < BPW; ++u) {
               uint32_t a[2][4];
 #pragma unroll
-              for (int e = 0; e < 2; ++e) nibbles(kw[e][g], a[0][e], a[0][2 + e], a[1][e], a[1][2 + e]);
-              const float sa = (g & 1) ? bf16hi_to_f32(ks[0][g / 2]) : bf16lo_to_f32(ks[0][g / 2]);
-              const float sb = (g & 1) ? bf16hi_to_f32(ks[1][g / 2]) : bf16lo_to_f32(ks[1][g / 2]);
+              for (int e = 0; e < 2; ++e) raw_nibbles(kw[u][e][g], a[0][e], a[0][2 + e], a[1][e], a[1][2 + e]);
+              const float sa = (g & 1) ? bf16hi_to_f32(ks[u][0][g / 2]) : bf16lo_to_f32(ks[u][0][g / 2]);
+              const float sb = (g & 1) ? bf16hi_to_f32(ks[u][1][g / 2]) : bf16lo_to_f32(ks[u][1][g / 2]);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                float x[4] = {};
-#pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                  for (int e = 0; e < 2; ++e) mma_f16(x, a[e], qf[part][nt][2 * g + e][0], qf[part][nt][2 * g + e][1]);
+                float x[4];
+                mma_f16_c(x, a[0], qh[nt].x, qh[nt].y, __uint_as_float(qs[nt].x), __uint_as_float(qs[nt].y));
+                mma_f16(x, a[1], qh[nt].z, qh[nt].w);
+                mma_f16(x, a[0], ql[nt].x, ql[nt].y);
+                mma_f16(x, a[1], ql[nt].z, ql[nt].w);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   const float f = e < 2 ? sa : sb;
@@ -532,17 +640,36 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
                 }
               }
             }
-          } else {
-            float x[2][NT][4] = {};
-            const int row = warp * (16 * BPW) + 16 * u + (lane & 15);
+          }
+        } else {
+#pragma unroll
+          for (int u = 0; u < BPW; ++u) {
+            float x[2][NT][4];
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
               uint32_t a[4];
-              ldsm4(a, stage + (k / 4) * (C::TILE * 128) + row * 128 + ((((k & 3) * 2 + (lane >> 4)) ^ (row & 7)) * 16));
+              ldsm4(a, stage + (koff ^ ((k & 3) * 32)) + (k / 4) * (C::TILE * 128) + u * 2048);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int part = 0; part < 2; ++part) mma_bf16(x[part][nt], a, qf[part][nt][k][0], qf[part][nt][k][1]);
+                for (int part = 0; part < 2; ++part) {
+                  uint32_t b0, b1;
+                  if constexpr (C::QREG) {
+                    b0 = qf[part][nt][k][0], b1 = qf[part][nt][k][1];
+                  } else {
+                    const uint32_t row = qrest - (2 - part) * C::ROWS * C::QROW + nt * 8 * C::QROW + k * 32;
+                    b0 = lds32(row), b1 = lds32(row + 16);
+                  }
+                  if (k == 0) mma_bf16_0(x[part][nt], a, b0, b1);
+                  else mma_bf16(x[part][nt], a, b0, b1);
+                }
+              if (p.rope) {  // the last part, zero where q was not rotated
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  const uint32_t row = qrest + nt * 8 * C::QROW + k * 32;
+                  mma_bf16(x[1][nt], a, lds32(row), lds32(row + 16));
+                }
+              }
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -552,6 +679,11 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
         }
         // ---- bias, mask ----
         if (p.slopes) {
+          float slope[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) slope[nt][e] = ctl->slope[nt * 8 + 2 * t + e];
 #pragma unroll
           for (int u = 0; u < BPW; ++u) {
             const int n = n0 + 16 * u - (w.s.L - 1);
@@ -610,11 +742,12 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
 #pragma unroll
               for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
               f[nt][e] = 1.f;
-              if (x > th[nt][e] - __fdiv_rn(kLazy, c2[nt][e])) {  // above the present maximum
+              const float lazy = __fdividef(kLazy, c2[nt][e]);
+              if (x > th[nt][e] - lazy) {  // above the present maximum
                 const float m = x * c2[nt][e];
                 f[nt][e] = th[nt][e] == kNegInf ? 0.f : ex2_approx(-nm[nt][e] - m);
                 nm[nt][e] = -m;
-                th[nt][e] = x + __fdiv_rn(kLazy, c2[nt][e]);
+                th[nt][e] = x + lazy;
                 l[nt][e] *= f[nt][e];
               }
             }
@@ -635,7 +768,7 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
                 if (now > old) {
                   const uint32_t ex = min(now >> 7, 253u);  // biased exponent of the largest step
                   const float mul = __uint_as_float((254u - ex) << 23);
-                  fv[g] = __fdiv_rn(mul, vmul[g]);
+                  fv[g] = mul * __fdiv_rn(1.f, vmul[g]);
                   vmul[g] = mul;
                   lim = min(((ex + 4) << 7) | 0x7Fu, 0x7FFFu);
                 }
@@ -664,22 +797,19 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
         // ---- O^T += V^T P^T ----
 #pragma unroll
         for (int u = 0; u < BPW; ++u) {
-          const int blk = warp * (16 * BPW) + 16 * u;
           if constexpr (Q4) {
             uint32_t vw[2][G];  // keys (2t, 2t + 1), (2t + 8, 2t + 9): 4 nibbles of each per group
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int k0 = blk + key_of<true>(8 * e + 2 * t), k1 = blk + key_of<true>(8 * e + 2 * t + 1);
-              const uint32_t v0 = stage + C::KB;
+              const uint32_t a0 = stage + voff + (16 * u + 8 * e) * RB, a1 = stage + voff1 + (16 * u + 8 * e) * RB;
               if constexpr (D == 128) {
-                const uint2 x = lds64(v0 + k0 * 64 + ((r ^ ((k0 & 2) << 1)) * 8));
-                const uint2 y = lds64(v0 + k1 * 64 + ((r ^ ((k1 & 2) << 1)) * 8));
+                const uint2 x = lds64(a0), y = lds64(a1);
                 vw[e][0] = __byte_perm(x.x, y.x, 0x5410);
                 vw[e][1] = __byte_perm(x.x, y.x, 0x7632);
                 vw[e][2] = __byte_perm(x.y, y.y, 0x5410);
                 vw[e][3] = __byte_perm(x.y, y.y, 0x7632);
               } else {
-                const uint32_t x = lds32(v0 + k0 * 32 + r * 4), y = lds32(v0 + k1 * 32 + r * 4);
+                const uint32_t x = lds32(a0), y = lds32(a1);
                 vw[e][0] = __byte_perm(x, y, 0x5410);
                 vw[e][1] = __byte_perm(x, y, 0x7632);
               }
@@ -688,7 +818,7 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
             for (int g = 0; g < G; ++g) {
               uint32_t a[2][4];
 #pragma unroll
-              for (int e = 0; e < 2; ++e) nibbles(vw[e][g], a[0][2 * e], a[0][2 * e + 1], a[1][2 * e], a[1][2 * e + 1]);
+              for (int e = 0; e < 2; ++e) raw_nibbles(vw[e][g], a[0][2 * e], a[0][2 * e + 1], a[1][2 * e], a[1][2 * e + 1]);
               const float sa = ((g & 1) ? bf16hi_to_f32(vs[u][0][g / 2]) : bf16lo_to_f32(vs[u][0][g / 2])) * vmul[g];
               const float sb = ((g & 1) ? bf16hi_to_f32(vs[u][1][g / 2]) : bf16lo_to_f32(vs[u][1][g / 2])) * vmul[g];
 #pragma unroll
@@ -697,6 +827,8 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
                 const uint32_t b1 = movm(pack_f16x2(s[u][nt][2] * sb, s[u][nt][3] * sb));
                 mma_f16(o[nt][2 * g], a[0], b0, b1);
                 mma_f16(o[nt][2 * g + 1], a[1], b0, b1);
+                mma_f16(o[nt][2 * g], minus8, b0, b1);
+                mma_f16(o[nt][2 * g + 1], minus8, b0, b1);
               }
             }
           } else {
@@ -721,12 +853,10 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
                                             (n + 1 >= w.s.first && n + 1 < w.s.L ? 0xFFFF0000u : 0u);
               }
             }
-            const int row = blk + (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
             for (int k = 0; k < MT; ++k) {
               uint32_t a[4];
-              ldsm4t(a, stage + C::KB + (k / 4) * (C::TILE * 128) + row * 128 +
-                            ((((k & 3) * 2 + ((lane >> 3) & 1)) ^ (row & 7)) * 16));
+              ldsm4t(a, stage + (voff ^ ((k & 3) * 32)) + (k / 4) * (C::TILE * 128) + u * 2048);
               if (edge) {
                 a[0] &= keep[0], a[1] &= keep[0];
                 a[2] &= keep[1], a[3] &= keep[1];
@@ -776,6 +906,8 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
 #pragma unroll
         for (int k = 0; k < MT; ++k) {
           const float fk = Q4 ? f * __fdiv_rn(1.f, vmul[Q4 ? k / 2 : 0]) : f;
+          o[nt][k][e] *= Q4 ? 0x1p22f : 1.f;
+          o[nt][k][e + 2] *= Q4 ? 0x1p18f : 1.f;
           o[nt][k][e] *= fk;
           o[nt][k][e + 2] *= fk;
         }
@@ -863,111 +995,142 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, Q4>::CTAS)
   }
   // Launched as a programmatic dependent: global memory is touched only from here on.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // this CTA's run: thread j sums the tiles of its share of the sequences
+  // this CTA's run: thread j sums the units of its share of the sequences
   const int B = p.cache.B, share = (B + kThreads - 1) / kThreads;
   int64_t mine = 0;
   for (int b = tid * share; b < min(B, (tid + 1) * share); ++b) {
     const int L = __ldg(p.lens + b);
     if (blockIdx.x == 0 && (L < 0 || L > p.cache.cap)) atomicOr(p.status, kDevPageRange);
-    mine += span_of<C::TILE>(p, b).nt;
+    mine += units_of<C>(span_of<C::TILE>(p, b));
   }
-  int64_t tiles;
-  int64_t before = block_prefix<kThreads>(mine, ctl->wsum, &tiles);
-  const int64_t T = tiles * p.items;
-  const int G = sharers(T, gridDim.x), cta = blockIdx.x;
-  const int64_t lo = cta < G ? run_start(T, cta, G) : 0, hi = cta < G ? run_start(T, cta + 1, G) : 0;
-  if (lo < hi && before * p.items <= lo && lo < (before + mine) * p.items) {
+  int64_t units;
+  int64_t before = block_prefix<kThreads>(mine, ctl->wsum, &units);
+  const Deal deal(units * p.items, gridDim.x);
+  const int cta = blockIdx.x;
+  const int64_t lo = deal.start(cta);
+  const int len = cta < deal.runs ? static_cast<int>(deal.start(cta + 1) - lo) : 0;
+  if (len > 0 && before * p.items <= lo && lo < (before + mine) * p.items) {
     int b = tid * share;
     for (;; ++b) {
-      const int nt = span_of<C::TILE>(p, b).nt;
-      if (lo < (before + nt) * p.items) break;
-      before += nt;
+      const int units = units_of<C>(span_of<C::TILE>(p, b));
+      if (lo < (before + units) * p.items) break;
+      before += units;
     }
     ctl->b0 = b;
     ctl->rem0 = static_cast<int>(lo - before * p.items);
   }
-  // every CTA is resident by now: combine_kernel may come in and find its own place in the work
-  // while this grid runs (what both read was complete before this grid's wait returned)
+  // every CTA is resident by now: the combine kernel may come in and find its own place in the
+  // work while this grid runs (what both read was complete before this grid's wait returned)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncthreads();
-  if (lo < hi) {
-    Walk<C::TILE> w(p, ctl->b0, ctl->rem0, static_cast<int>(hi - lo));
+  if (len > 0) {
+    const Walk<C> w(p, ctl->b0, ctl->rem0, len);
     if (tid >= kConsumers) produce<D, NT, Q4>(p, smem, ctl, w);
     else consume<D, NT, Q4>(p, smem, ctl, w);
   }
 }
 
 // Joins the segments of items that more than one CTA walked, and writes the rows of empty
-// sequences. One CTA per (sequence, query head), thread = output element.
-template <int D, int TILE>
-__global__ void __launch_bounds__(D) paged_combine_kernel(const __grid_constant__ PagedDecodeParams p) {
-  __shared__ int64_t wsum[D / 32];
-  __shared__ float w_sh[kPagedMaxCtas];
-  __shared__ float red[D / 32];
-  const int b = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq;
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const int rows = p.head_rows;
-  // tiles of all sequences, and of those before b
-  int64_t all = 0, pre = 0;
-  for (int i = tid; i < p.cache.B; i += D) {
-    const int nt = span_of<TILE>(p, i).nt;
-    all += nt;
-    if (i < b) pre += nt;
+// sequences. There are at most as many such items as items, or as places where runs meet,
+// whichever are fewer: block x takes item x, or (by_run) the item that run x + 1 begins within if
+// run x has its first tiles. Block y: its query heads p.comb_heads y and on. Little shared memory,
+// so that blocks fit beside the decode kernel's.
+template <class C, int D>
+__global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constant__ PagedDecodeParams p) {
+  constexpr int N = 256, KG = N / D;  // threads; groups that share an element's partials
+  __shared__ int64_t wsum[N / 32];
+  __shared__ int64_t item_before;
+  __shared__ int item_b;
+  __shared__ float part[KG][D];
+  // the stream's next kernel may come in and wait
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid % 32;
+  const int B = p.cache.B, share = (B + N - 1) / N;
+  const bool by_run = p.comb_by_run;
+  const int want_b = by_run ? -1 : static_cast<int>(blockIdx.x) / p.items;
+  int64_t mine = 0;
+  for (int b = tid * share; b < min(B, (tid + 1) * share); ++b) mine += units_of<C>(span_of<C::TILE>(p, b));
+  int64_t units;
+  int64_t before = block_prefix<N>(mine, wsum, &units);
+  const Deal deal(units * p.items, p.ctas);
+  const int run = blockIdx.x + 1;
+  const int64_t lo = by_run && run < deal.runs ? deal.start(run) : -1;
+  if (by_run ? lo >= 0 && before * p.items <= lo && lo < (before + mine) * p.items : tid == want_b / share) {
+    int b = tid * share;
+    for (;; ++b) {
+      const int n = units_of<C>(span_of<C::TILE>(p, b));
+      if (by_run ? lo < (before + n) * p.items : b == want_b) break;
+      before += n;
+    }
+    item_b = b;
+    item_before = before;
   }
-  int64_t tiles, before;
-  block_prefix<D>(all, wsum, &tiles);
   __syncthreads();
-  block_prefix<D>(pre, wsum, &before);
-  const int nt = span_of<TILE>(p, b).nt;
-  __nv_bfloat16* out = p.out + b * p.o_sb + h * p.o_sh + tid;
+  int b = 0, n = 0, i0 = 0, first_slot = 0, h0 = 0, j1 = 0;
+  if (!by_run || lo >= 0) {
+    b = item_b;
+    const int len = units_of<C>(span_of<C::TILE>(p, b));
+    if (len) {
+      const int hh = by_run ? static_cast<int>(div_units(lo - item_before * p.items, len)) : static_cast<int>(blockIdx.x) % p.items;
+      const int64_t s = item_before * p.items + static_cast<int64_t>(hh) * len;  // the item's first unit
+      i0 = deal.run_of(s + C::ENDS);                                             // runs with tiles of it
+      const int i1 = deal.run_of(s + len - 1);
+      if (i1 > i0 && (!by_run || i0 == run - 1)) n = i1 - i0 + 1;
+      first_slot = deal.start(i0) < s ? 1 : 0;
+      const int kvh = hh / p.chunks;
+      h0 = kvh * p.g + (hh % p.chunks) * p.head_rows;
+      j1 = min(min(static_cast<int>(blockIdx.y + 1) * p.comb_heads, p.head_rows), kvh * p.g + p.g - h0);
+    }
+  }
   // partial rows, and the order of writes to out and lse against earlier kernels, from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (nt == 0) {
-    *out = __float2bfloat16_rn(0.f);
-    if (p.lse && tid == 0) p.lse[blockIdx.x] = kNegInf;
-    return;
+  if (blockIdx.y == 0) {
+    for (int e = blockIdx.x; e < B; e += gridDim.x) {
+      if (span_of<C::TILE>(p, e).nt) continue;
+      for (int i = tid; i < p.Hq * D; i += N) p.out[e * p.o_sb + (i / D) * p.o_sh + i % D] = __float2bfloat16_rn(0.f);
+      if (p.lse)
+        for (int h = tid; h < p.Hq; h += N) p.lse[static_cast<int64_t>(e) * p.Hq + h] = kNegInf;
+    }
   }
-  const int kvh = h / p.g, j0 = h % p.g;
-  const int hh = kvh * p.chunks + j0 / rows, j = j0 % rows;
-  const int64_t T = tiles * p.items;
-  const int64_t s = before * p.items + static_cast<int64_t>(hh) * nt, e = s + nt;
-  const int G = sharers(T, p.ctas);
-  const int i0 = run_of(T, s, G), i1 = run_of(T, e - 1, G);
-  if (i0 == i1) return;  // finished by that CTA
-  const int n = i1 - i0 + 1;
-  const int first_slot = run_start(T, i0, G) < s ? 1 : 0;
-  auto row_of = [&](int k) { return (static_cast<int64_t>(i0 + k) * 2 + (k == 0 ? first_slot : 0)) * rows + j; };
-  float mx = kNegInf;
-  for (int k = tid; k < n; k += D) mx = fmaxf(mx, p.part_ml[row_of(k)].x);
+  if (n == 0) return;
+  auto row_of = [&](int k, int j) { return (static_cast<int64_t>(i0 + k) * 2 + (k == 0 ? first_slot : 0)) * p.head_rows + j; };
+  // A warp finds the runs' weights 32 at a time, a run per lane. The groups share the runs of one
+  // head, or each take heads of their own.
+  const int c = tid % D, group = tid / D;
+  const bool share_runs = p.comb_heads == 1;
+  const int step = share_runs ? KG : 1, j_step = share_runs ? 1 : KG;
+  for (int j = blockIdx.y * p.comb_heads + (share_runs ? 0 : group); j < j1; j += j_step) {
+    float mx = kNegInf;
+    for (int k = lane; k < n; k += 32) mx = fmaxf(mx, p.part_ml[row_of(k, j)].x);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if (lane == 0) red[warp] = mx;
-  __syncthreads();
-  float M = red[0];
-#pragma unroll
-  for (int k = 1; k < D / 32; ++k) M = fmaxf(M, red[k]);
-  const float base = M == kNegInf ? 0.f : M;
-  __syncthreads();
-  float sum = 0.f;
-  for (int k = tid; k < n; k += D) {
-    const float2 ml = p.part_ml[row_of(k)];
-    const float w = ex2_approx(ml.x - base);
-    w_sh[k] = w;
-    sum += w * ml.y;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) red[warp] = sum;
-  __syncthreads();
-  float total = 0.f;
-#pragma unroll
-  for (int k = 0; k < D / 32; ++k) total += red[k];
-  float acc = 0.f;
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float base = mx == kNegInf ? 0.f : mx;
+    float acc = 0.f, sum = 0.f;
+    for (int k0 = 0; k0 < n; k0 += 32) {
+      float w = 0.f;
+      if (k0 + lane < n) {
+        const float2 ml = p.part_ml[row_of(k0 + lane, j)];
+        w = ex2_approx(ml.x - base);
+        sum += w * ml.y;
+      }
+      const int kn = min(32, n - k0);
 #pragma unroll 8
-  for (int k = 0; k < n; ++k) acc += w_sh[k] * p.part_acc[row_of(k) * D + tid];
-  const bool any = !(total == 0.f);
-  *out = __float2bfloat16_rn(any ? acc / total : 0.f);
-  if (p.lse && tid == 0) p.lse[blockIdx.x] = any ? (M + log2f(total)) * kLn2 : kNegInf;
+      for (int k = share_runs ? group : 0; k < kn; k += step)
+        acc += __shfl_sync(0xffffffffu, w, k) * p.part_acc[row_of(k0 + k, j) * D + c];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (share_runs) {
+      part[group][c] = acc;
+      __syncthreads();
+      if (group > 0) break;  // one head per block
+#pragma unroll
+      for (int k = 1; k < KG; ++k) acc += part[k][c];
+    }
+    const bool any = !(sum == 0.f);  // a NaN goes to the output
+    p.out[b * p.o_sb + (h0 + j) * p.o_sh + c] = __float2bfloat16_rn(any ? acc / sum : 0.f);
+    if (p.lse && c == 0) p.lse[static_cast<int64_t>(b) * p.Hq + h0 + j] = any ? (mx + log2f(sum)) * kLn2 : kNegInf;
+  }
 }
 
 int sm_count() {
@@ -1014,10 +1177,16 @@ cudaError_t launch(PagedDecodeParams p, cudaStream_t stream) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, p);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(p.cache.B * p.Hq);
-  cfg.blockDim = dim3(D);
+  // about two blocks per SM where that many have work
+  const int64_t all_items = (int64_t)p.cache.B * p.items;
+  p.comb_by_run = all_items > p.ctas;
+  const int heads = std::min(p.g, C::ROWS);
+  p.comb_heads = p.comb_by_run ? std::min(heads, 4) : (int)std::max<int64_t>(1, std::min<int64_t>(heads, all_items * heads / 304));
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(all_items, p.ctas),
+                     (heads + p.comb_heads - 1) / p.comb_heads);
+  cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, C::TILE>, p);
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<C, D>, p);
 }
 
 template <int D, int NT, bool Q4>
