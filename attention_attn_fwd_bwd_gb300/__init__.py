@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 __all__ = [
@@ -109,7 +110,6 @@ def load():
         P, I, F, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
         ST = ctypes.POINTER(ctypes.c_int64)
         VP = ctypes.POINTER(CVariant)
-        CP = ctypes.POINTER(CPagedCache)
         sig = {
             "attnfuse_last_error": ([], ctypes.c_char_p),
             "attnfuse_version": ([], I),
@@ -125,10 +125,10 @@ def load():
             "attnfuse_decode_auto_splits": ([I, I, I, ctypes.POINTER(I)], I),
             "attnfuse_decode_noalloc": ([P, ST, P, ST, P, ST, P, ST, P, I, I, I, I, I, I, F, F, I,
                                          I, P], I),
-            "attnfuse_paged_append": ([CP, P, ST, P, ST, P, P, I, F, I, P], I),
-            "attnfuse_paged_gather": ([CP, P, P, P, ST, P, ST, I, P], I),
+            "attnfuse_paged_append": ([P, P, P, P, P, P, P, I, F, I, P], I),
+            "attnfuse_paged_gather": ([P, P, P, P, P, P, P, I, P], I),
             "attnfuse_paged_decode_workspace_size": ([I, I, I, I, ctypes.POINTER(S)], I),
-            "attnfuse_paged_decode": ([CP, P, ST, P, P, ST, P, I, F, F, I, I, P, P, S, P], I),
+            "attnfuse_paged_decode": ([P, P, P, P, P, P, P, I, F, F, I, I, P, P, S, P], I),
             "attnfuse_rope_prerotate": ([P, ST, P, I, I, I, I, F, P, S, P], I),
             "attnfuse_debug_wait_timeout": ([ctypes.c_uint64, P], I),
             "attnfuse_rope_table": ([P, S, I, I, F, P], I),
@@ -594,23 +594,26 @@ def rope_prerotate(x, rope_theta, out=None, workspace=None, stream=None):
 
 # Paged caches. A decode step on a small batch is a few microseconds on the GPU, so the binding's
 # own cost counts here: checks that pass touch each tensor once (_need runs for the message of
-# one that does not), a cache's C struct is built once, and pointers go to ctypes as integers.
-_I3, _I4 = ctypes.c_int64 * 3, ctypes.c_int64 * 4
+# one that does not), and what goes to the C ABI by address is packed into bytes: a cache's struct
+# once, strides per call.
+_S3, _S4 = struct.Struct("@3q").pack, struct.Struct("@4q").pack
+_CACHE = struct.Struct("@7i2P8q2P8qPq")  # the fields of CPagedCache
+assert _CACHE.size == ctypes.sizeof(CPagedCache)
 
 
-def _live_strides(t, n):
+def _live_strides(t):
     """Element strides with those of one-element dimensions, which address nothing and may hold
     any value, replaced by what a contiguous tensor would have."""
     st, shape = t.stride(), t.shape
     if 1 in shape:
         st = list(st)
         inner = 1
-        for i in range(n - 1, -1, -1):
+        for i in range(len(st) - 1, -1, -1):
             if shape[i] == 1:
                 st[i] = inner
             elif st[i] * shape[i] > inner:
                 inner = st[i] * shape[i]
-    return _I4(*st) if n == 4 else _I3(*st)
+    return st
 
 
 def _want(t, name, dtype, shape, device, contiguous=False):
@@ -619,27 +622,21 @@ def _want(t, name, dtype, shape, device, contiguous=False):
         _need(t, name, (dtype,), shape, device, contiguous)
 
 
-def _launch_stream(device, stream):
-    """(context manager or None, stream handle): _launch_context, without a context manager where
-    the tensors' device is the current one already."""
+def _launch(fn, args, device, stream):
+    """fn(*args, stream) on `device`: as in _launch_context, but without making the device current
+    where it is."""
     import torch
 
     if stream is None and device.index == torch.cuda.current_device():
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         if raw is not None:
-            return None, raw(device.index)
-    return _launch_context(device, stream)
-
-
-def _launch(fn, args, device, stream):
-    ctx, st = _launch_stream(device, stream)
-    if ctx is None:
-        rc = fn(*args, st)
-    else:
-        with ctx:
-            rc = fn(*args, st)
-    if rc:
-        _check(rc)
+            rc = fn(*args, raw(device.index))
+            if rc:
+                _check(rc)
+            return
+    ctx, st = _launch_context(device, stream)
+    with ctx:
+        _check(fn(*args, st))
 
 
 class PagedCache:
@@ -653,39 +650,42 @@ class PagedCache:
     over the same pools) and keeps the lengths. page_size: a multiple of 16.
     """
 
+    __slots__ = ("_tensors", "_c", "q4", "format", "device", "num_pages", "Hkv", "page_size", "d", "B", "max_pages")
+
     def __init__(self, k, v, page_table, k_scales=None, v_scales=None):
         import torch
 
         bf16 = torch.bfloat16
-        q4 = getattr(k, "dtype", None) is torch.uint8
-        if not (q4 or getattr(k, "dtype", None) is bf16) or k.dim() != 4 or k.device.type != "cuda":
+        dt = getattr(k, "dtype", None)
+        q4 = dt is torch.uint8
+        if not (q4 or dt is bf16) or k.dim() != 4 or not k.is_cuda:
             _need(k, "cache k", (torch.uint8,) if q4 else (bf16, torch.uint8), ndim=4,
                   dims="[num_pages, Hkv, page_size, d/2]" if q4 else "[num_pages, Hkv, page_size, d]")
         shape, dev = k.shape, k.device
-        P, H, S, row = shape
-        d = 2 * row if q4 else row
-        _want(v, "cache v", k.dtype, shape, dev)
+        P, H, S, d = shape
+        _want(v, "cache v", dt, shape, dev)
         if q4:
-            _want(k_scales, "cache k_scales", bf16, (P, H, S, d // 32), dev)
-            _want(v_scales, "cache v_scales", bf16, (P, H, S, d // 32), dev)
+            d *= 2
+            steps = (P, H, S, d // 32)
+            _want(k_scales, "cache k_scales", bf16, steps, dev)
+            _want(v_scales, "cache v_scales", bf16, steps, dev)
+            scales = (k_scales.data_ptr(), v_scales.data_ptr(), *_live_strides(k_scales), *_live_strides(v_scales))
         elif k_scales is not None or v_scales is not None:
             raise ValueError("k_scales, v_scales belong to the 4-bit format (uint8 pools)")
+        else:
+            scales = _NO_SCALES
         if getattr(page_table, "dtype", None) is not torch.int32 or page_table.dim() != 2 or page_table.device != dev:
             _need(page_table, "page_table", (torch.int32,), ndim=2, dims="[B, max_pages]", device=dev)
         B, max_pages = page_table.shape
-        ts = page_table.stride()
-        if max_pages > 1 and ts[1] != 1:
+        row, one = page_table.stride()
+        if max_pages > 1 and one != 1:
             raise ValueError("page_table: rows must be contiguous")
         self._tensors = (k, v, page_table, k_scales, v_scales)
-        self.q4, self.format, self.device = q4, CACHE_Q4 if q4 else CACHE_BF16, dev
+        self.q4, self.device = q4, dev
+        self.format = fmt = CACHE_Q4 if q4 else CACHE_BF16
         self.num_pages, self.Hkv, self.page_size, self.d, self.B, self.max_pages = P, H, S, d, B, max_pages
-        none = _NO_STRIDES
-        self._c = CPagedCache(
-            self.format, P, H, S, d, B, max_pages, k.data_ptr(), v.data_ptr(), _live_strides(k, 4), _live_strides(v, 4),
-            k_scales.data_ptr() if q4 else None, v_scales.data_ptr() if q4 else None,
-            _live_strides(k_scales, 4) if q4 else none, _live_strides(v_scales, 4) if q4 else none,
-            page_table.data_ptr(), ts[0])
-        self._ref = ctypes.byref(self._c)
+        self._c = _CACHE.pack(fmt, P, H, S, d, B, max_pages, k.data_ptr(), v.data_ptr(), *_live_strides(k), *_live_strides(v),
+                              *scales, page_table.data_ptr(), row)
 
     k = property(lambda self: self._tensors[0])
     v = property(lambda self: self._tensors[1])
@@ -706,12 +706,11 @@ class PagedCache:
                    new(d // 32, torch.bfloat16), new(d // 32, torch.bfloat16))
 
 
-_NO_STRIDES = _I4(0, 0, 0, 0)
+_NO_SCALES = (0,) * 10
 
 
 def _need_cache(cache):
-    if not isinstance(cache, PagedCache):
-        raise TypeError(f"cache: expected a PagedCache, got {type(cache).__name__}")
+    raise TypeError(f"cache: expected a PagedCache, got {type(cache).__name__}")
 
 
 def _index(t, name, cache):
@@ -730,7 +729,8 @@ def paged_append(cache, k, v, start, count=None, rope_theta=10000.0, rope_mode=R
     rotated at its position on the way (rope_mode ROPE_FUSED) or taken as it is (ROPE_NONE)."""
     import torch
 
-    _need_cache(cache)
+    if not isinstance(cache, PagedCache):
+        _need_cache(cache)
     bf16, dev = torch.bfloat16, cache.device
     if getattr(k, "dtype", None) is not bf16 or k.dim() != 4:
         _need(k, "k", (bf16,), ndim=4, dims="[B, Hkv, N, d]")
@@ -741,7 +741,7 @@ def paged_append(cache, k, v, start, count=None, rope_theta=10000.0, rope_mode=R
     if start is None:
         raise TypeError("start: expected an int32 [B] tensor")
     _launch(load().attnfuse_paged_append,
-            (cache._ref, k.data_ptr(), _live_strides(k, 4), v.data_ptr(), _live_strides(v, 4),
+            (cache._c, k.data_ptr(), _S4(*_live_strides(k)), v.data_ptr(), _S4(*_live_strides(v)),
              _index(start, "start", cache), _index(count, "count", cache), N, rope_theta, rope_mode), dev, stream)
 
 
@@ -750,16 +750,24 @@ def paged_gather(cache, start, count, N, k=None, v=None, stream=None):
     N rows) into rows 0 .. of k, v [B, Hkv, N, d] bf16, zeros behind. Returns (k, v)."""
     import torch
 
-    _need_cache(cache)
+    if not isinstance(cache, PagedCache):
+        _need_cache(cache)
     bf16, dev, N = torch.bfloat16, cache.device, int(N)
     shape = (cache.B, cache.Hkv, N, cache.d)
-    k = torch.empty(shape, dtype=bf16, device=dev) if k is None else k
-    v = torch.empty(shape, dtype=bf16, device=dev) if v is None else v
-    _want(k, "k", bf16, shape, dev)
-    _want(v, "v", bf16, shape, dev)
+    dense = N * cache.d
+    if k is None:
+        k, ks = torch.empty(shape, dtype=bf16, device=dev), _S4(cache.Hkv * dense, dense, cache.d, 1)
+    else:
+        _want(k, "k", bf16, shape, dev)
+        ks = _S4(*_live_strides(k))
+    if v is None:
+        v, vs = torch.empty(shape, dtype=bf16, device=dev), _S4(cache.Hkv * dense, dense, cache.d, 1)
+    else:
+        _want(v, "v", bf16, shape, dev)
+        vs = _S4(*_live_strides(v))
     _launch(load().attnfuse_paged_gather,
-            (cache._ref, _index(start, "start", cache), _index(count, "count", cache), k.data_ptr(), _live_strides(k, 4),
-             v.data_ptr(), _live_strides(v, 4), N), dev, stream)
+            (cache._c, _index(start, "start", cache), _index(count, "count", cache), k.data_ptr(), ks, v.data_ptr(), vs, N),
+            dev, stream)
     return k, v
 
 
@@ -776,10 +784,8 @@ _paged_sizes = {}  # (device index, Hq, Hkv, d, format) -> workspace bytes
 def _paged_workspace_size(device, *key):
     import torch
 
-    n = _paged_sizes.get((device.index,) + key)
-    if n is None:
-        with torch.cuda.device(device):
-            n = _paged_sizes[(device.index,) + key] = paged_decode_workspace_size(*key)
+    with torch.cuda.device(device):
+        n = _paged_sizes[(device.index,) + key] = paged_decode_workspace_size(*key)
     return n
 
 
@@ -791,7 +797,8 @@ def paged_decode(q, cache, lens, scale=None, rope_theta=10000.0, rope_mode=ROPE_
     slope_h (n - (lens[b] - 1)) to the scores."""
     import torch
 
-    _need_cache(cache)
+    if not isinstance(cache, PagedCache):
+        _need_cache(cache)
     bf16, f32, dev, B, d = torch.bfloat16, torch.float32, cache.device, cache.B, cache.d
     if getattr(q, "dtype", None) is not bf16 or q.dim() != 3:
         _need(q, "q", (bf16,), ndim=3, dims="[B, Hq, d]")
@@ -804,23 +811,25 @@ def paged_decode(q, cache, lens, scale=None, rope_theta=10000.0, rope_mode=ROPE_
         _want(alibi_slopes, "alibi_slopes", f32, (Hq,), dev, contiguous=True)
         alibi_slopes = alibi_slopes.data_ptr()
     if out is None:
-        out = torch.empty(shape, dtype=bf16, device=dev)
+        out, os_ = torch.empty(shape, dtype=bf16, device=dev), _S3(Hq * d, d, 1)
     else:
         _want(out, "out", bf16, shape, dev)
-    if lse is None:
-        if with_lse:
-            lse = torch.empty((B, Hq), dtype=f32, device=dev)
-    else:
+        os_ = _S3(*_live_strides(out))
+    if lse is not None:
         _want(lse, "lse", f32, (B, Hq), dev, contiguous=True)
-    ws_n = _paged_workspace_size(dev, Hq, cache.Hkv, d, cache.format)
+    elif with_lse:
+        lse = torch.empty((B, Hq), dtype=f32, device=dev)
+    ws_n = _paged_sizes.get((dev.index, Hq, cache.Hkv, d, cache.format))
+    if ws_n is None:
+        ws_n = _paged_workspace_size(dev, Hq, cache.Hkv, d, cache.format)
     if workspace is None:
-        ws = torch.empty(ws_n, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(ws_n, dtype=torch.uint8, device=dev)
     else:
-        ws = _workspace(ws_n, dev, workspace)
+        workspace = _workspace(ws_n, dev, workspace)
     _launch(load().attnfuse_paged_decode,
-            (cache._ref, q.data_ptr(), _live_strides(q, 3), _index(lens, "lens", cache), out.data_ptr(),
-             _live_strides(out, 3), None if lse is None else lse.data_ptr(), Hq, d ** -0.5 if scale is None else scale,
-             rope_theta, rope_mode, window, alibi_slopes, ws.data_ptr(), ws_n), dev, stream)
+            (cache._c, q.data_ptr(), _S3(*_live_strides(q)), _index(lens, "lens", cache), out.data_ptr(), os_,
+             None if lse is None else lse.data_ptr(), Hq, d ** -0.5 if scale is None else scale, rope_theta, rope_mode,
+             min(window, 0x7FFFFFFF), alibi_slopes, workspace.data_ptr(), ws_n), dev, stream)
     return out, lse
 
 

@@ -116,15 +116,23 @@ int check_rope(int* mode, float theta) {
   return ATTNFUSE_OK;
 }
 
-PagedFreqs paged_freqs(int d, float theta) {
-  PagedFreqs f;
-  memset(&f, 0, sizeof(f));
-  const double two_pi = 6.283185307179586476925286766559;
-  for (int i = 0; i < d / 2; ++i) {
-    double x = std::pow((double)theta, -2.0 * i / d) / two_pi;
-    x -= (f.f[i].x = (float)x);
-    x -= (f.f[i].y = (float)x);
-    f.f[i].z = (float)x;
+// The frequencies of a theta; a thread keeps those of its last call (64 pow cost as much as a
+// launch).
+const PagedFreqs& paged_freqs(int d, float theta) {
+  static thread_local PagedFreqs f;
+  static thread_local int have_d = 0;
+  static thread_local float have_theta = 0.f;
+  if (have_d != d || have_theta != theta) {
+    memset(&f, 0, sizeof(f));
+    const double two_pi = 6.283185307179586476925286766559;
+    for (int i = 0; i < d / 2; ++i) {
+      double x = std::pow((double)theta, -2.0 * i / d) / two_pi;
+      x -= (f.f[i].x = (float)x);
+      x -= (f.f[i].y = (float)x);
+      f.f[i].z = (float)x;
+    }
+    have_d = d;
+    have_theta = theta;
   }
   return f;
 }

@@ -1157,8 +1157,16 @@ cudaError_t launch(PagedDecodeParams p, cudaStream_t stream) {
                 "shared memory of the resident CTAs");
   static_assert(C::STAGES <= 8, "barriers");
   auto kern = paged_decode_kernel<D, NT, Q4>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D, NT, Q4>());
+  static std::atomic<uint64_t> ready;  // devices that the kernel's shared memory was allowed on
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready.load(std::memory_order_acquire) & bit) || dev > 63) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D, NT, Q4>());
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
   p.head_rows = C::ROWS;
   p.chunks = (p.g + C::ROWS - 1) / C::ROWS;
   p.items = p.cache.Hkv * p.chunks;

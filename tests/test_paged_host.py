@@ -124,12 +124,12 @@ def test_binding_refuses_cpu_tensors_and_types():
 
 def test_one_element_dimensions_take_any_stride():
     x = torch.zeros(3, 4, 8, 16)
-    assert list(af._live_strides(x, 4)) == list(x.stride())
+    assert list(af._live_strides(x)) == list(x.stride())
     odd = torch.as_strided(x, (3, 1, 1, 16), (16, 1, 1, 1))
-    assert list(af._live_strides(odd, 4)) == [16, 16, 16, 1]
-    assert list(af._live_strides(torch.as_strided(x, (1, 4, 8, 16), (0, 128, 16, 1)), 4)) == [512, 128, 16, 1]
+    assert list(af._live_strides(odd)) == [16, 16, 16, 1]
+    assert list(af._live_strides(torch.as_strided(x, (1, 4, 8, 16), (0, 128, 16, 1)))) == [512, 128, 16, 1]
     wide = x.transpose(1, 2)[:, :1]  # slots one, heads behind each other
-    assert list(af._live_strides(wide, 4)) == [512, 512, 128, 1]
+    assert list(af._live_strides(wide)) == [512, 512, 128, 1]
 
 
 @pytest.mark.parametrize("d", [64, 128])
