@@ -1,7 +1,11 @@
 // Writing rows into a paged cache (with the rotation of K and, for q4, the quantisation on the
 // way) and reading them back out as dense bf16 rows.
 //
-// Both are bound by HBM: a row of K and V is read once and written once.
+// A row of K and V is read once and written once, and HBM bounds the gather (187 MB of bf16 rows,
+// d = 64: 31 us, 89% of a copy's rate) and, with the launch's ragged end, the bf16 append (138 MB,
+// 18.5k rows of 8 heads, d = 128, rotated: 28 us, 72%). Appending to 4 bits (12k rows of 8 heads,
+// d = 128: 24 us, 37%) is bound by its instructions: 566 per warp, the idle rows' included, keep
+// the schedulers issuing 68% of the time.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -156,32 +160,48 @@ __global__ void __launch_bounds__(kThreads) append_bf16_kernel(const __grid_cons
 // ---------------------------------------------------------------------------------------------
 
 // 4 elements (two bf16x2 words) -> 4 nibbles code + 8 in the low 16 bits, lowest first.
-// inv = (1 + 2^-20) / s. x and s have 8 significant bits each, so |x| / s is a tie k + 1/2 or at
-// least 2^-12 (relative) away from one; the reciprocal's error (1 ulp) and a rounding stay within
-// 2^-22, so the factor puts ties, and only them, past the middle. |x| / s < 7.03: no clamp.
-// Added to 1.5 2^23 + 8, the rounded quotient is the sum's low bits; those of four sums, shifted
-// by multiplications, add up without carries.
-__device__ __forceinline__ uint32_t q4_codes(uint32_t w0, uint32_t w1, float inv) {
-  constexpr float kAt = 12582920.0f;
-  const uint32_t n0 = __float_as_uint(__fmaf_rn(bf16lo_to_f32(w0), inv, kAt));
-  const uint32_t n1 = __float_as_uint(__fmaf_rn(bf16hi_to_f32(w0), inv, kAt));
-  const uint32_t n2 = __float_as_uint(__fmaf_rn(bf16lo_to_f32(w1), inv, kAt));
-  const uint32_t n3 = __float_as_uint(__fmaf_rn(bf16hi_to_f32(w1), inv, kAt));
-  return n0 + n1 * 16u + n2 * 256u + n3 * 4096u;
+// inv = (1 + 2^-20) / s, twice. x and s have 8 significant bits each, so |x| / s is a tie k + 1/2
+// or at least 2^-12 (relative) away from one; the reciprocal's error (1 ulp) and a rounding stay
+// within 2^-22, so the factor puts ties, and only them, past the middle. |x| / s < 7.03: no clamp.
+// Added to M + 8, M = 1.5 2^23, a quotient is rounded to an integer n in the sum's low bits, and
+// sums M + n0 + 16 n1 (and M + a + 256 b of two such) are exact: 16 (M + n1) - 16 M is.
+__device__ __forceinline__ uint32_t q4_codes(uint32_t w0, uint32_t w1, uint64_t inv) {
+  constexpr float kM = 12582912.0f;
+  const uint64_t at = f2_pack(kM + 8.0f, kM + 8.0f);
+  const uint64_t even = fma2(f2_pack(bf16lo_to_f32(w0), bf16lo_to_f32(w1)), inv, at);
+  const uint64_t odd = fma2(f2_pack(bf16hi_to_f32(w0), bf16hi_to_f32(w1)), inv, at);
+  const uint64_t two = add2(even, fma2(odd, f2_pack(16.0f, 16.0f), f2_pack(-16.0f * kM, -16.0f * kM)));
+  return __float_as_uint(__fadd_rn(f2_lo(two), __fmaf_rn(f2_hi(two), 256.0f, -256.0f * kM)));
 }
 
-// Largest magnitudes of a row's groups as bf16 bits (their integers order like the values, NaN
-// above infinity), two groups per word, the same in all 8 threads of the row.
+// The largest magnitude of the group that thread t of a row answers for, group t % G of K
+// (t % 2G < G) or V, as bf16 bits (their integers order like the values, NaN above infinity).
+// Words of two groups each; a thread hands on half of its words at each step, so that 8 threads
+// reduce 8 groups with 4 shuffles.
 template <int G>
-__device__ __forceinline__ void q4_amax(const uint2 (&w)[G], uint32_t (&a)[G / 2]) {
+__device__ __forceinline__ uint32_t q4_amax(const uint2 (&x)[2][G], int t) {
+  uint32_t a[2][G / 2];
 #pragma unroll
-  for (int q = 0; q < G / 2; ++q) {
-    const uint32_t x = __vmaxu2(w[2 * q].x & 0x7FFF7FFFu, w[2 * q].y & 0x7FFF7FFFu);
-    const uint32_t y = __vmaxu2(w[2 * q + 1].x & 0x7FFF7FFFu, w[2 * q + 1].y & 0x7FFF7FFFu);
-    a[q] = __vmaxu2(__byte_perm(x, y, 0x5410), __byte_perm(x, y, 0x7632));
+  for (int w = 0; w < 2; ++w)
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) a[q] = __vmaxu2(a[q], __shfl_xor_sync(0xffffffffu, a[q], o));
+    for (int q = 0; q < G / 2; ++q) {
+      const uint32_t e = __vmaxu2(x[w][2 * q].x & 0x7FFF7FFFu, x[w][2 * q].y & 0x7FFF7FFFu);
+      const uint32_t o = __vmaxu2(x[w][2 * q + 1].x & 0x7FFF7FFFu, x[w][2 * q + 1].y & 0x7FFF7FFFu);
+      a[w][q] = __vmaxu2(__byte_perm(e, o, 0x5410), __byte_perm(e, o, 0x7632));
+    }
+  uint32_t k0, k1;  // after the first step: words 0 and 1 of K or V; K's and V's word
+  if constexpr (G == 4) {
+    const bool up = t & 4;
+    k0 = __vmaxu2(up ? a[1][0] : a[0][0], __shfl_xor_sync(0xffffffffu, up ? a[0][0] : a[1][0], 4));
+    k1 = __vmaxu2(up ? a[1][1] : a[0][1], __shfl_xor_sync(0xffffffffu, up ? a[0][1] : a[1][1], 4));
+  } else {
+    k0 = __vmaxu2(a[0][0], __shfl_xor_sync(0xffffffffu, a[0][0], 4));
+    k1 = __vmaxu2(a[1][0], __shfl_xor_sync(0xffffffffu, a[1][0], 4));
   }
+  const bool up = t & 2;
+  uint32_t k = __vmaxu2(up ? k1 : k0, __shfl_xor_sync(0xffffffffu, up ? k0 : k1, 2));
+  k = __vmaxu2(k, __shfl_xor_sync(0xffffffffu, k, 1));
+  return (t & 1) ? k >> 16 : k & 0xFFFFu;
 }
 
 template <int D, bool ROPE>
@@ -221,14 +241,7 @@ __global__ void __launch_bounds__(kThreads) append_q4_kernel(const __grid_consta
   // Steps: thread t finds the step of group t % G, of K (t < G) or V, stores it, and hands its
   // reciprocal to the row's other threads. amax / 7 is never a tie of bf16 (or is exact), and at
   // least 2^-12 (relative) away from one, so the product with 1/7 rounds to the same step.
-  uint32_t am[2][G / 2];
-  q4_amax<G>(x[0], am[0]);
-  q4_amax<G>(x[1], am[1]);
-  const int mine = w.t % (2 * G);
-  uint32_t bits = 0;
-#pragma unroll
-  for (int j = 0; j < 2 * G; ++j)
-    if (mine == j) bits = (am[j / G][(j % G) / 2] >> (16 * (j & 1))) & 0xFFFFu;
+  const uint32_t bits = q4_amax<G>(x, w.t);
   const float amax = __uint_as_float(bits << 16);
   uint32_t s = __bfloat16_as_ushort(__float2bfloat16_rn(amax * (1.0f / 7.0f)));
   float inv;
@@ -242,7 +255,10 @@ __global__ void __launch_bounds__(kThreads) append_q4_kernel(const __grid_consta
   for (int which = 0; which < 2; ++which)
 #pragma unroll
     for (int g = 0; g < G; ++g)
-      code[which][g] = q4_codes(x[which][g].x, x[which][g].y, __shfl_sync(0xffffffffu, inv, row0 + which * G + g));
+    {
+      const float i = __shfl_sync(0xffffffffu, inv, row0 + which * G + g);
+      code[which][g] = q4_codes(x[which][g].x, x[which][g].y, f2_pack(i, i));
+    }
   if (live) {
     const int64_t at = static_cast<int64_t>(r.slot) * (D / 2) + q4_place<D>(w.t, r.slot) * (D / 16);
     uint8_t* kd = p.cache.k + r.page * p.cache.k_sp + w.h * p.cache.k_sh + at;
@@ -266,6 +282,11 @@ __global__ void __launch_bounds__(kThreads) append_q4_kernel(const __grid_consta
 // ---------------------------------------------------------------------------------------------
 // Gather: cache rows first[b] .. first[b] + count[b] - 1 -> dense rows 0 .. N - 1, zeros behind
 // ---------------------------------------------------------------------------------------------
+// A thread moves its piece of K and V for up to two heads, all loads before the first store.
+// Eight heads in turn, a load at a time: 34.6 us for 187 MB of bf16 rows; one head, two, or four
+// at a time: 31 each. 343 MB from 4-bit rows: one head 61.0 us, two 54.8, four (64 registers) 55.7.
+constexpr int kGatherHeads = 2;
+
 template <int D, bool Q4>
 __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant__ PagedGatherParams p) {
   constexpr int TPR = Q4 ? 8 : D / 8;  // threads per row: q4 chunks, or 16-byte pieces
@@ -278,55 +299,79 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
   const bool live = n < live_rows(p.count, b, p.N, p.status) &&
                     find_row(p.cache, b, n, p.first ? __ldg(p.first + b) : 0, p.status, &r);
   const int h0 = blockIdx.y * p.heads_per_thread, h1 = min(p.cache.Hkv, h0 + p.heads_per_thread);
-  uint8_t* ko = p.k + b * p.k_sb + n * p.k_sn;
-  uint8_t* vo = p.v + b * p.v_sb + n * p.v_sn;
-  for (int h = h0; h < h1; ++h) {
+  uint8_t* const out[2] = {p.k + b * p.k_sb + n * p.k_sn, p.v + b * p.v_sb + n * p.v_sn};
+  const int64_t out_sh[2] = {p.k_sh, p.v_sh};
+  const uint8_t *src[2] = {}, *steps[2] = {};
+  const int64_t src_sh[2] = {p.cache.k_sh, p.cache.v_sh}, steps_sh[2] = {p.cache.ks_sh, p.cache.vs_sh};
+  if (live) {
+    const int64_t at = Q4 ? static_cast<int64_t>(r.slot) * (D / 2) + q4_place<D>(t, r.slot) * (D / 16) : t * 16;
+    src[0] = p.cache.k + r.page * p.cache.k_sp + (Q4 ? at : r.slot * p.cache.k_st + at);
+    src[1] = p.cache.v + r.page * p.cache.v_sp + (Q4 ? at : r.slot * p.cache.v_st + at);
+    if (Q4) {
+      steps[0] = p.cache.ks + r.page * p.cache.ks_sp + r.slot * (D / 16);
+      steps[1] = p.cache.vs + r.page * p.cache.vs_sp + r.slot * (D / 16);
+    }
+  }
+  if constexpr (!Q4) {
+    uint4 x[2][kGatherHeads];
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      uint8_t* out = which ? vo + h * p.v_sh : ko + h * p.k_sh;
-      if (!Q4) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (live) {
-          const uint8_t* src = which ? p.cache.v + r.page * p.cache.v_sp + r.slot * p.cache.v_st + h * p.cache.v_sh
-                                     : p.cache.k + r.page * p.cache.k_sp + r.slot * p.cache.k_st + h * p.cache.k_sh;
-          x = *reinterpret_cast<const uint4*>(src + t * 16);
-        }
-        *reinterpret_cast<uint4*>(out + t * 16) = x;
-      } else {
-        uint32_t w[G / 2] = {}, sc[G / 2] = {};
-        if (live) {
-          const int64_t at = static_cast<int64_t>(r.slot) * (D / 2) + q4_place<D>(t, r.slot) * (D / 16);
-          const uint8_t* src = which ? p.cache.v + r.page * p.cache.v_sp + h * p.cache.v_sh + at
-                                     : p.cache.k + r.page * p.cache.k_sp + h * p.cache.k_sh + at;
-          const uint8_t* ss = which ? p.cache.vs + r.page * p.cache.vs_sp + h * p.cache.vs_sh + r.slot * (D / 16)
-                                    : p.cache.ks + r.page * p.cache.ks_sp + h * p.cache.ks_sh + r.slot * (D / 16);
+    for (int i = 0; i < kGatherHeads; ++i)
 #pragma unroll
-          for (int q = 0; q < G / 2; ++q) {
-            w[q] = reinterpret_cast<const uint32_t*>(src)[q];
-            sc[q] = reinterpret_cast<const uint32_t*>(ss)[q];
+      for (int w = 0; w < 2; ++w) {
+        x[w][i] = make_uint4(0, 0, 0, 0);
+        if (live && h0 + i < h1) x[w][i] = *reinterpret_cast<const uint4*>(src[w] + (h0 + i) * src_sh[w]);
+      }
+#pragma unroll
+    for (int i = 0; i < kGatherHeads; ++i)
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+        if (h0 + i < h1) *reinterpret_cast<uint4*>(out[w] + (h0 + i) * out_sh[w] + t * 16) = x[w][i];
+  } else {
+    uint32_t c[2][kGatherHeads][G / 2], s[2][kGatherHeads][G / 2];
+#pragma unroll
+    for (int i = 0; i < kGatherHeads; ++i)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+#pragma unroll
+        for (int q = 0; q < G / 2; ++q) c[w][i][q] = s[w][i][q] = 0;
+        if (live && h0 + i < h1) {
+          const uint8_t* from = src[w] + (h0 + i) * src_sh[w];
+          const uint8_t* step = steps[w] + (h0 + i) * steps_sh[w];
+          if constexpr (G == 4) {
+            const uint2 a = *reinterpret_cast<const uint2*>(from), d = *reinterpret_cast<const uint2*>(step);
+            c[w][i][0] = a.x, c[w][i][1] = a.y, s[w][i][0] = d.x, s[w][i][1] = d.y;
+          } else {
+            c[w][i][0] = *reinterpret_cast<const uint32_t*>(from);
+            s[w][i][0] = *reinterpret_cast<const uint32_t*>(step);
           }
         }
+      }
+#pragma unroll
+    for (int i = 0; i < kGatherHeads; ++i)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        if (h0 + i >= h1) continue;
+        uint8_t* to = out[w] + (h0 + i) * out_sh[w] + t * 8;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          const uint32_t h4 = (w[g / 2] >> (16 * (g & 1))) & 0xFFFFu;
-          const float s = (g & 1) ? bf16hi_to_f32(sc[g / 2]) : bf16lo_to_f32(sc[g / 2]);
+          const uint32_t h4 = c[w][i][g / 2] >> (16 * (g & 1));
+          const float step = (g & 1) ? bf16hi_to_f32(s[w][i][g / 2]) : bf16lo_to_f32(s[w][i][g / 2]);
           float x[4];
+          // code times step: 12 significant bits, rounded once; the code becomes a float as the
+          // low bits of 2^23 + code
 #pragma unroll
-          for (int i = 0; i < 4; ++i)  // code times step: 12 significant bits, rounded once
-            x[i] = s * static_cast<float>(static_cast<int>((h4 >> (4 * i)) & 15) - 8);
-          *reinterpret_cast<uint2*>(out + g * 64 + t * 8) =
+          for (int e = 0; e < 4; ++e)
+            x[e] = step * (__uint_as_float(0x4B000000u | ((h4 >> (4 * e)) & 15)) - 8388616.0f);
+          *reinterpret_cast<uint2*>(to + g * 64) =
               live ? make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])) : make_uint2(0, 0);
         }
       }
-    }
   }
 }
 
-// Heads per thread of the gather: a run of heads shares one row's lookup, but the launch should
-// still fill the GPU's thread slots.
+// Heads per thread of the gather: two, unless their threads would not fill the GPU's slots.
 int gather_heads(int64_t rows, int tpr, int Hkv) {
-  const int64_t h = rows * tpr * Hkv / (152 * 1024);
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(h, std::min(Hkv, 8))));
+  return Hkv > 1 && rows * tpr * Hkv >= 2 * 152 * 1024 ? kGatherHeads : 1;
 }
 
 // Heads per block of the append: angles (about 2.6 times a row-head's other work, per row) are
