@@ -323,8 +323,10 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
       tc_fence_before();
       mbar_arrive(&ctl->p_full);
     }
+    // Not pv_done of the last tile: where V(ntiles - 2) is late, PV(ntiles - 3) is the last one done
+    // here, and its phase has the same parity.
     if (ok && ntiles > 0) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&ctl->pv_done, (ntiles - 1) & 1, status, abort_flag));
+      ok = __all_sync(0xffffffffu, mbar_wait(&ctl->mma_final, 0, status, abort_flag) && !*abort_flag);
       tc_fence_after();
     }
     // ---- partials of this chunk: acc (unnormalised), max (log2 units), sum ----
