@@ -12,6 +12,7 @@ and call them on the current CUDA stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -622,6 +623,18 @@ def _want(t, name, dtype, shape, device, contiguous=False):
         _need(t, name, (dtype,), shape, device, contiguous)
 
 
+def _on(stream, device):
+    """Context for allocations that a call on `stream` uses: made on another stream, their memory
+    could be handed to that stream's work again while the call still runs."""
+    import torch
+
+    if stream is None:
+        return contextlib.nullcontext()
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream)
+
+
 def _launch(fn, args, device, stream):
     """fn(*args, stream) on `device`: as in _launch_context, but without making the device current
     where it is."""
@@ -755,16 +768,16 @@ def paged_gather(cache, start, count, N, k=None, v=None, stream=None):
     bf16, dev, N = torch.bfloat16, cache.device, int(N)
     shape = (cache.B, cache.Hkv, N, cache.d)
     dense = N * cache.d
-    if k is None:
-        k, ks = torch.empty(shape, dtype=bf16, device=dev), _S4(cache.Hkv * dense, dense, cache.d, 1)
-    else:
+    ks = vs = _S4(cache.Hkv * dense, dense, cache.d, 1)
+    if k is not None:
         _want(k, "k", bf16, shape, dev)
         ks = _S4(*_live_strides(k))
-    if v is None:
-        v, vs = torch.empty(shape, dtype=bf16, device=dev), _S4(cache.Hkv * dense, dense, cache.d, 1)
-    else:
+    if v is not None:
         _want(v, "v", bf16, shape, dev)
         vs = _S4(*_live_strides(v))
+    with _on(stream, dev):
+        k = torch.empty(shape, dtype=bf16, device=dev) if k is None else k
+        v = torch.empty(shape, dtype=bf16, device=dev) if v is None else v
     _launch(load().attnfuse_paged_gather,
             (cache._c, _index(start, "start", cache), _index(count, "count", cache), k.data_ptr(), ks, v.data_ptr(), vs, N),
             dev, stream)
@@ -794,7 +807,8 @@ def paged_decode(q, cache, lens, scale=None, rope_theta=10000.0, rope_mode=ROPE_
     """Decode over a paged cache: q [B, Hq, d] bf16 at position lens[b] - 1 against positions
     n < lens[b] (window > 0: the last `window` of them) -> (out [B, Hq, d], lse [B, Hq]).
     lens: int32 [B] device tensor (0: out 0, lse -inf); alibi_slopes: fp32 [Hq], adds
-    slope_h (n - (lens[b] - 1)) to the scores."""
+    slope_h (n - (lens[b] - 1)) to the scores. With a stream, what the call allocates belongs to
+    that stream."""
     import torch
 
     if not isinstance(cache, PagedCache):
@@ -810,22 +824,24 @@ def paged_decode(q, cache, lens, scale=None, rope_theta=10000.0, rope_mode=ROPE_
     if alibi_slopes is not None:
         _want(alibi_slopes, "alibi_slopes", f32, (Hq,), dev, contiguous=True)
         alibi_slopes = alibi_slopes.data_ptr()
-    if out is None:
-        out, os_ = torch.empty(shape, dtype=bf16, device=dev), _S3(Hq * d, d, 1)
-    else:
+    os_ = _S3(Hq * d, d, 1)
+    if out is not None:
         _want(out, "out", bf16, shape, dev)
         os_ = _S3(*_live_strides(out))
     if lse is not None:
         _want(lse, "lse", f32, (B, Hq), dev, contiguous=True)
-    elif with_lse:
-        lse = torch.empty((B, Hq), dtype=f32, device=dev)
     ws_n = _paged_sizes.get((dev.index, Hq, cache.Hkv, d, cache.format))
     if ws_n is None:
         ws_n = _paged_workspace_size(dev, Hq, cache.Hkv, d, cache.format)
-    if workspace is None:
-        workspace = torch.empty(ws_n, dtype=torch.uint8, device=dev)
-    else:
-        workspace = _workspace(ws_n, dev, workspace)
+    with _on(stream, dev):
+        if out is None:
+            out = torch.empty(shape, dtype=bf16, device=dev)
+        if lse is None and with_lse:
+            lse = torch.empty((B, Hq), dtype=f32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(ws_n, dtype=torch.uint8, device=dev)
+        else:
+            workspace = _workspace(ws_n, dev, workspace)
     _launch(load().attnfuse_paged_decode,
             (cache._c, q.data_ptr(), _S3(*_live_strides(q)), _index(lens, "lens", cache), out.data_ptr(), os_,
              None if lse is None else lse.data_ptr(), Hq, d ** -0.5 if scale is None else scale, rope_theta, rope_mode,

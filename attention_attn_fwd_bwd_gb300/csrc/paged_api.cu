@@ -63,6 +63,7 @@ int check_cache(const attnfuse_paged_cache* c, PagedDev* out) {
   if (c->num_pages <= 0 || c->Hkv <= 0 || c->B <= 0 || c->max_pages <= 0)
     return fail(ATTNFUSE_ERR_INVALID_ARG, "cache sizes must be positive (num_pages=%d Hkv=%d B=%d max_pages=%d)",
                 c->num_pages, c->Hkv, c->B, c->max_pages);
+  if (c->Hkv > 4096) return fail(ATTNFUSE_ERR_UNSUPPORTED, "Hkv=%d (at most 4096)", c->Hkv);
   if (c->d != 64 && c->d != 128) return fail(ATTNFUSE_ERR_UNSUPPORTED, "head dim %d (need 64 or 128)", c->d);
   if (c->page_size <= 0 || c->page_size % 16 || c->page_size > kPagedMaxPage)
     return fail(ATTNFUSE_ERR_UNSUPPORTED, "page_size %d (need a multiple of 16 up to %d)", c->page_size, kPagedMaxPage);

@@ -385,9 +385,10 @@ attnfuse_status attnfuse_paged_gather(const attnfuse_paged_cache* cache, const i
  * s_n = scale <R q, k_n> [+ alibi_slopes[h] (n - (lens[b] - 1))]; alibi_slopes [Hq] fp32 or NULL.
  * out [B, Hq, d] bf16 (strides as in attnfuse_decode), lse [B, Hq] fp32 or NULL. lens[b] = 0:
  * out 0, lse -inf. rope_mode NONE or FUSED (AUTO means FUSED): q is rotated in fp32 and keeps
- * 16 or more significant bits. Hq any multiple of Hkv. Sequences of any mix of lengths share the
- * GPU evenly: the work is cut into equal runs of 64-key tiles over the whole batch. Results do
- * not vary from run to run. workspace: attnfuse_paged_decode_workspace_size bytes, 16-byte
+ * 22 or more significant bits. Hq: a multiple of Hkv up to 4096, and B * Hq * max_pages *
+ * page_size at most 2^42. Sequences of any mix of lengths share the GPU evenly: the work is cut
+ * into equal runs of tiles of 64 or 128 keys over the whole batch. Results do not vary from run
+ * to run. workspace: attnfuse_paged_decode_workspace_size bytes, 16-byte
  * aligned; it depends on the device, d and Hq / Hkv only, not on lengths. Calls that may
  * overlap need workspaces of their own. */
 attnfuse_status attnfuse_paged_decode_workspace_size(int Hq, int Hkv, int d, int format, size_t* bytes);

@@ -522,6 +522,104 @@ def test_prompt_then_decode_together(q4):
     assert torch.isfinite(prompt).all() and af.device_status() == 0
 
 
+@pytest.mark.parametrize("q4", [False, True])
+def test_calls_on_a_given_stream_own_what_they_allocate(q4):
+    """A call on a busy stream is still queued when the caller goes on: memory that the call
+    allocated may not reach the current stream's next tensors before it has run."""
+    lens = [9000, 300]
+    cache = make_cache(lens, 2, 64, 128, q4, seed=51)
+    q, ln = randn(2, 8, 128, seed=52), i32(lens)
+    want, rows = af.paged_decode(q, cache, ln), af.paged_gather(cache, None, ln, 9000)
+    n = af.paged_decode_workspace_size(8, 2, 128, cache.format)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        got = af.paged_decode(q, cache, ln, stream=side)
+        dense = af.paged_gather(cache, None, ln, 9000, stream=side)
+        keep = [torch.full((n,), 0x7F, dtype=torch.uint8, device=DEV) for _ in range(4)]
+        side.synchronize()
+        torch.cuda.synchronize()
+        for x, y in zip(got + dense, want + rows):
+            assert torch.equal(x, y)
+        assert all((x == 0x7F).all() for x in keep)
+        del keep
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_steps_on_two_streams_at_once(q4):
+    """Two batches over one pool of pages, each stepped on a stream of its own."""
+    Hkv, Hq, page, d, steps = 2, 16, 32, 128, 12
+    first = [[700, 0, 33, 5000], [1, 2900, 64, 128]]
+    both = make_cache([n + steps for part in first for n in part], Hkv, page, d, q4, seed=53, garbage=False)
+    copies = [x.clone() for x in both._tensors if x is not None]
+    ks, vs, qs = (randn(2, steps, 4, h, d, seed=54 + i) for i, h in enumerate((Hkv, Hkv, Hq)))
+
+    def run(streams):
+        outs = [[], []]
+        caches = [af.PagedCache(both.k, both.v, both.page_table[4 * i:4 * i + 4], both.k_scales, both.v_scales) for i in (0, 1)]
+        lens = [i32(x) for x in first]
+        torch.cuda.synchronize()
+        for n in range(steps):
+            for i, s in enumerate(streams):
+                with torch.cuda.stream(s):
+                    start = lens[i].clone()
+                    lens[i].add_(1)
+                    af.paged_append(caches[i], ks[i, n][:, :, None], vs[i, n][:, :, None], start, rope_theta=5e5)
+                    outs[i].append(af.paged_decode(qs[i, n], caches[i], lens[i], rope_theta=5e5))
+        torch.cuda.synchronize()
+        return outs
+
+    one = torch.cuda.current_stream()
+    alone = run([one, one])
+    for x, y in zip((x for x in both._tensors if x is not None), copies):
+        x.copy_(y)
+    at_once = run([torch.cuda.Stream(), torch.cuda.Stream()])
+    for a, b in zip(alone, at_once):
+        for x, y in zip(a, b):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+    assert af.device_status() == 0
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_decode_many_sequences_of_large_groups(q4):
+    """More items than CTAs with two passes of query heads each, the second of them ragged."""
+    r = random.Random(55)
+    lens = [r.choice([0, 1, r.randint(1, 64), r.randint(1, 700)]) for _ in range(90)]
+    run_decode(lens, 80, 4, 32, 64, q4, theta=1e4, seed=55)
+    run_decode(lens[:40] + [4000], 40, 2, 16, 128, q4, seed=56)
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_sequences_may_share_pages(q4):
+    """One row of the table for all sequences: its stride is 0."""
+    own = make_cache([600], 2, 16, 128, q4, seed=57)
+    shared = af.PagedCache(own.k, own.v, own.page_table.expand(3, -1), own.k_scales, own.v_scales)
+    lens = [600, 37, 599]
+    got = run_decode(lens, 4, 2, 16, 128, q4, theta=1e4, cache=shared, seed=8)
+    rows = af.PagedCache(own.k, own.v, shared.page_table.clone(), own.k_scales, own.v_scales)
+    again = run_decode(lens, 4, 2, 16, 128, q4, theta=1e4, cache=rows, seed=8)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+    first, count = [0, 16, 500], [100, 21, 99]
+    for dense, which in zip(af.paged_gather(shared, i32(first), i32(count), 100), "kv"):
+        pool = P.values(shared, which)
+        for b in range(3):
+            assert torch.equal(dense[b, :, :count[b]], P.rows(pool, shared.page_table, b, first[b], count[b]).float().bfloat16())
+            assert (dense[b, :, count[b]:] == 0).all()
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_windows_past_the_sequence_are_none(q4):
+    lens = [700, 1, 130]
+    cache = make_cache(lens, 2, 32, 64, q4, seed=59)
+    q = randn(3, 4, 64, seed=60)
+    want = af.paged_decode(q, cache, i32(lens))
+    for window in (700, 1 << 24, (1 << 31) - 1, 1 << 31, 1 << 40):
+        got = af.paged_decode(q, cache, i32(lens), window=window)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), window
+
+
 def test_refusals_on_the_gpu():
     """What only a CUDA tensor lets the binding see; every call fails before a launch."""
     Hkv, page, d = 2, 16, 64

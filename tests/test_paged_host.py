@@ -151,3 +151,12 @@ def test_reference_quantiser_on_known_groups():
     assert codes[0, :5].tolist() == [7, 4, -4, 0, -1] and steps[0, 0] == 1
     assert steps[1, 0] == 0 and codes[1].abs().sum() == 0
     assert torch.isnan(steps[2, 1]) and steps[2, 0] == 0
+
+
+def test_more_kv_heads_than_a_grid_holds_are_refused(lib):
+    """Heads are a grid dimension of the append and the gather."""
+    for q4 in (False, True):
+        c = _cache(q4, Hkv=4097)
+        assert _append(lib, c) == UNSUPPORTED
+        assert lib.attnfuse_paged_gather(ctypes.byref(c), None, None, FAKE, X, FAKE, X, 5, None) == UNSUPPORTED
+        assert _decode(lib, c, Hq=4097) == UNSUPPORTED
