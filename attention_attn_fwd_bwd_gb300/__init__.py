@@ -623,13 +623,16 @@ def _want(t, name, dtype, shape, device, contiguous=False):
         _need(t, name, (dtype,), shape, device, contiguous)
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(stream, device):
     """Context for allocations that a call on `stream` uses: made on another stream, their memory
     could be handed to that stream's work again while the call still runs."""
     import torch
 
     if stream is None:
-        return contextlib.nullcontext()
+        return _HERE
     if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     return torch.cuda.stream(stream)
@@ -640,13 +643,12 @@ def _launch(fn, args, device, stream):
     where it is."""
     import torch
 
-    if stream is None and device.index == torch.cuda.current_device():
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None:
-            rc = fn(*args, raw(device.index))
-            if rc:
-                _check(rc)
-            return
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if stream is None and raw is not None and device.index == torch._C._cuda_getDevice():
+        rc = fn(*args, raw(device.index))
+        if rc:
+            _check(rc)
+        return
     ctx, st = _launch_context(device, stream)
     with ctx:
         _check(fn(*args, st))

@@ -71,28 +71,31 @@ struct PagedGatherParams {
   int heads_per_thread;
   int* status;
 };
-struct PagedDecodeParams {
+// What the combine kernel needs of them, too.
+struct PagedCombineParams {
   PagedDev cache;
-  const __nv_bfloat16* q;           // [B, Hq, d], element strides
-  int64_t q_sb, q_sh;
-  __nv_bfloat16* out;
+  __nv_bfloat16* out;               // [B, Hq, d], element strides
   int64_t o_sb, o_sh;
   float* lse;                       // [B, Hq] or null
   const int32_t* lens;              // [B]
   int Hq, g;
   int window;                       // 0: none
+  // set by the launcher
+  int ctas, head_rows;              // query heads per item
+  int chunks, items;                // items per KV head, and per sequence
+  int comb_by_run, comb_heads;      // the combine kernel's blocks
+  float* part_acc;                  // [ctas][2][head_rows][d]: partial rows of a run's ends
+  float2* part_ml;                  // (max in log2 units, sum)
+};
+struct PagedDecodeParams : PagedCombineParams {
+  const __nv_bfloat16* q;           // [B, Hq, d]
+  int64_t q_sb, q_sh;
   const float* slopes;              // [Hq] or null
   int rope;
   float scale_log2;
   CUtensorMap tmK, tmV;             // bf16: pools [num_pages, Hkv, page_size, d], box (64, frag_rows)
   int frag_rows;                    // rows of a page that one copy takes
   void* workspace;
-  // set by the launcher
-  float* part_acc;                  // [ctas][2][head_rows][d]: partial rows of a run's ends
-  float2* part_ml;                  // (max in log2 units, sum)
-  int ctas, head_rows;              // query heads per item
-  int chunks, items;                // items per KV head, and per sequence
-  int comb_by_run, comb_heads;      // the combine kernel's blocks
   PagedFreqs freqs;
   int* status;
 };

@@ -187,7 +187,7 @@ struct Span {
 };
 
 template <int TILE>
-__device__ __forceinline__ Span span_of(const PagedDecodeParams& p, int b) {
+__device__ __forceinline__ Span span_of(const PagedCombineParams& p, int b) {
   Span s;
   s.L = min(max(__ldg(p.lens + b), 0), p.cache.cap);
   s.first = p.window > 0 && s.L > p.window ? s.L - p.window : 0;
@@ -1036,7 +1036,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, Q4>::CTAS)
 // run x has its first tiles. Block y: its query heads p.comb_heads y and on. Little shared memory,
 // so that blocks fit beside the decode kernel's.
 template <class C, int D>
-__global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constant__ PagedDecodeParams p) {
+__global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constant__ PagedCombineParams p) {
   constexpr int N = 256, KG = N / D;  // threads; groups that share an element's partials
   __shared__ int64_t wsum[N / 32];
   __shared__ int64_t item_before;
@@ -1194,7 +1194,7 @@ cudaError_t launch(PagedDecodeParams p, cudaStream_t stream) {
                      (heads + p.comb_heads - 1) / p.comb_heads);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<C, D>, p);
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<C, D>, static_cast<const PagedCombineParams&>(p));
 }
 
 template <int D, int NT, bool Q4>
