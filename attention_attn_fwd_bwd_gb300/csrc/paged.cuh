@@ -134,7 +134,7 @@ __device__ __forceinline__ int q4_place(int r, int slot) {
 // rotated key is defined as the exact R_p k rounded to fp32 and then to bf16, whatever
 // computes it. fp32 alone would move about one element in 10^6 across such a border, and the
 // GPU's fp64 units are few (a first version recomputed doubtful elements in fp64: 126 us for
-// 18.5k rows of 8 heads, d = 128, against 20 us of traffic). So angles and products are carried as the
+// 18.5k rows of 8 heads, d = 128, of which 20 are traffic; now 28). So angles and products are carried as the
 // sum of two floats, to about 2^-37: some 60 instructions per angle, shared by the heads of a
 // block, and 11 packed ones per pair and head.
 // ---------------------------------------------------------------------------------------------

@@ -20,7 +20,7 @@
 // Work. Sequences are cut into tiles of 64 or 128 keys; the tiles of the whole batch, ordered by
 // (sequence, KV head, chunk of query heads), are dealt to the CTAs in equal runs, from lengths read
 // on the device; an item counts for its tiles and for what its two ends cost (without that, 64
-// sequences of 1 to 8192 keys took 121 us from the 4-bit cache, with it 98). A CTA walks the
+// sequences of 1 to 8192 keys took 121 us from the 4-bit cache, with it 97). A CTA walks the
 // segments of its run. A segment that is a whole item (all tiles of one (sequence, head chunk)) is
 // finished in place; otherwise its (max, sum, acc) goes to the workspace, at most two per CTA, and
 // the combine kernel joins them in a fixed order.
@@ -51,7 +51,8 @@ template <int D, int NT, bool Q4>
 struct Cfg {
   static constexpr int ROWS = 8 * NT;                                   // query heads per item
   // 16-key blocks of a tile per warp: two hide each other's latencies and share the per-tile
-  // work; rows of 256 bytes (bf16, d = 128) keep the HBM busy with one.
+  // work (q4, 8 x 32k keys, 64 heads: 86 us, with one 105); rows of 256 bytes (bf16, d = 128) keep
+  // the HBM busy with one.
   static constexpr int BPW = Q4 || D == 64 ? 2 : 1;
   static constexpr int TILE = kWarps * 16 * BPW;                        // keys
   // What the two ends of a segment cost, in tiles: items count as so many more when work is dealt.
@@ -63,6 +64,8 @@ struct Cfg {
   // for every tile (of 16 heads, d = 128: one CTA per SM with, two CTAs without, 193 and 172 us for
   // 8 x 32k keys)
   static constexpr bool QREG = !Q4 && NT == 1;
+  // (q4, one column tile: four CTAs, of 96 registers a thread, 117 us; 8 consumer warps in each of
+  // two CTAs 103)
   static constexpr int CTAS = Q4 ? (NT == 1 ? 3 : 2) : 2;
   static constexpr int STAGES = Q4 || (NT == 2 && D == 128) ? 2 : 3;
   static constexpr uint32_t QROW = 2 * D + 16;                          // padded query row

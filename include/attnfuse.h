@@ -332,12 +332,13 @@ attnfuse_status attnfuse_decode_auto_splits(int B, int Hkv, int L, int* num_spli
  *         lowest nibble first; with d = 128, slots with bit 1 set hold chunk r at place r ^ 4.
  *         Slots of a (page, head) are contiguous (slot strides d/2 bytes and d/32 steps); page
  *         and head strides are positive multiples of 16 bytes.
- * page_size: a multiple of 16, at most 65536. max_pages * page_size <= 2^24 positions.
+ * page_size: a multiple of 16, at most 65536. max_pages * page_size <= 2^24 positions. Hkv: at
+ * most 4096.
  * Values read from the device (page_table, start, count, lens) are checked by the kernels: a
  * row on a page outside [0, num_pages), a start or length outside the table, or a count outside
  * [0, N] is skipped (lengths and counts are clamped), never accessed, and sets
  * ATTNFUSE_ERR_PAGE_RANGE in the device status word. Nothing on the host depends on them, so a
- * captured call follows them at every replay.
+ * captured call follows them at every replay; they must not change while a call runs.
  * ------------------------------------------------------------------------------------------ */
 typedef enum { ATTNFUSE_CACHE_BF16 = 0, ATTNFUSE_CACHE_Q4 = 1 } attnfuse_cache_format;
 
