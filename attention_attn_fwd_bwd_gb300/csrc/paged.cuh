@@ -83,6 +83,7 @@ struct PagedCombineParams {
   // set by the launcher
   int ctas, head_rows;              // query heads per item
   int chunks, items;                // items per KV head, and per sequence
+  int whole;                        // items are not cut: no partial rows, no combine kernel
   int comb_by_run, comb_heads;      // the combine kernel's blocks
   float* part_acc;                  // [ctas][2][head_rows][d]: partial rows of a run's ends
   float2* part_ml;                  // (max in log2 units, sum)

@@ -23,7 +23,8 @@
 // sequences of 1 to 8192 keys took 121 us from the 4-bit cache, with it 97). A CTA walks the
 // segments of its run. A segment that is a whole item (all tiles of one (sequence, head chunk)) is
 // finished in place; otherwise its (max, sum, acc) goes to the workspace, at most two per CTA, and
-// the combine kernel joins them in a fixed order.
+// the combine kernel joins them in a fixed order. In caches of short sequences every segment is a
+// whole item, and there is no second kernel.
 //
 // CTA: 4 consumer warps, each with its own keys of every tile and its own running (max, sum, acc)
 // (joined once per segment), and a producer warp that looks pages up and fills a ring of tiles: TMA
@@ -242,10 +243,10 @@ struct Deal {
   }
 };
 
-// An item is `ends` units without tiles, then one per tile.
+// An item is `ends` units without tiles, then one per tile; or one unit where items are not cut.
 template <class C>
-__device__ __forceinline__ int units_of(const Span& s) {
-  return s.nt ? s.nt + C::ENDS : 0;
+__device__ __forceinline__ int units_of(const PagedCombineParams& p, const Span& s) {
+  return s.nt ? (p.whole ? 1 : s.nt + C::ENDS) : 0;
 }
 
 // Walks the segments of a run that have tiles: all roles step through the same ones.
@@ -259,8 +260,8 @@ struct Walk {
   __device__ Walk(const PagedDecodeParams& p_, int b0, int rem0, int left_) : p(p_), b(b0), left(left_), n(0), head(true) {
     if (left <= 0) return;
     s = span_of<C::TILE>(p, b);
-    hh = rem0 / units_of<C>(s);
-    u = rem0 - hh * units_of<C>(s);
+    hh = rem0 / units_of<C>(p, s);
+    u = rem0 - hh * units_of<C>(p, s);
     find();
   }
   __device__ bool live() const { return n > 0; }
@@ -273,7 +274,7 @@ struct Walk {
  private:
   __device__ void find() {
     for (n = 0; n == 0 && left > 0;) {
-      if (u == units_of<C>(s)) {
+      if (u == units_of<C>(p, s)) {
         u = 0;
         if (++hh == p.items) {
           hh = 0;
@@ -281,9 +282,9 @@ struct Walk {
           while (s.nt == 0);
         }
       }
-      const int take = min(left, units_of<C>(s) - u);
-      t = max(0, u - C::ENDS);
-      n = max(0, u + take - C::ENDS) - t;
+      const int take = min(left, units_of<C>(p, s) - u);
+      t = p.whole ? 0 : max(0, u - C::ENDS);
+      n = p.whole ? s.nt : max(0, u + take - C::ENDS) - t;
       u += take;
       left -= take;
     }
@@ -980,6 +981,18 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
   }
 }
 
+// The rows of this block's share of the sequences that are empty.
+template <class C, int D>
+__device__ __forceinline__ void empty_rows(const PagedCombineParams& p) {
+  for (int e = blockIdx.x; e < p.cache.B; e += gridDim.x) {
+    if (span_of<C::TILE>(p, e).nt) continue;
+    for (int i = threadIdx.x; i < p.Hq * D; i += blockDim.x)
+      p.out[e * p.o_sb + (i / D) * p.o_sh + i % D] = __float2bfloat16_rn(0.f);
+    if (p.lse)
+      for (int h = threadIdx.x; h < p.Hq; h += blockDim.x) p.lse[static_cast<int64_t>(e) * p.Hq + h] = kNegInf;
+  }
+}
+
 template <int D, int NT, bool Q4>
 __global__ void __launch_bounds__(kThreads, Cfg<D, NT, Q4>::CTAS)
     paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
@@ -1004,7 +1017,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, Q4>::CTAS)
   for (int b = tid * share; b < min(B, (tid + 1) * share); ++b) {
     const int L = __ldg(p.lens + b);
     if (blockIdx.x == 0 && (L < 0 || L > p.cache.cap)) atomicOr(p.status, kDevPageRange);
-    mine += units_of<C>(span_of<C::TILE>(p, b));
+    mine += units_of<C>(p, span_of<C::TILE>(p, b));
   }
   int64_t units;
   int64_t before = block_prefix<kThreads>(mine, ctl->wsum, &units);
@@ -1015,7 +1028,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, Q4>::CTAS)
   if (len > 0 && before * p.items <= lo && lo < (before + mine) * p.items) {
     int b = tid * share;
     for (;; ++b) {
-      const int units = units_of<C>(span_of<C::TILE>(p, b));
+      const int units = units_of<C>(p, span_of<C::TILE>(p, b));
       if (lo < (before + units) * p.items) break;
       before += units;
     }
@@ -1026,6 +1039,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, Q4>::CTAS)
   // work while this grid runs (what both read was complete before this grid's wait returned)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncthreads();
+  if (p.whole) empty_rows<C, D>(p);
   if (len > 0) {
     const Walk<C> w(p, ctl->b0, ctl->rem0, len);
     if (tid >= kConsumers) produce<D, NT, Q4>(p, smem, ctl, w);
@@ -1052,7 +1066,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
   const bool by_run = p.comb_by_run;
   const int want_b = by_run ? -1 : static_cast<int>(blockIdx.x) / p.items;
   int64_t mine = 0;
-  for (int b = tid * share; b < min(B, (tid + 1) * share); ++b) mine += units_of<C>(span_of<C::TILE>(p, b));
+  for (int b = tid * share; b < min(B, (tid + 1) * share); ++b) mine += units_of<C>(p, span_of<C::TILE>(p, b));
   int64_t units;
   int64_t before = block_prefix<N>(mine, wsum, &units);
   const Deal deal(units * p.items, p.ctas);
@@ -1061,7 +1075,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
   if (by_run ? lo >= 0 && before * p.items <= lo && lo < (before + mine) * p.items : tid == want_b / share) {
     int b = tid * share;
     for (;; ++b) {
-      const int n = units_of<C>(span_of<C::TILE>(p, b));
+      const int n = units_of<C>(p, span_of<C::TILE>(p, b));
       if (by_run ? lo < (before + n) * p.items : b == want_b) break;
       before += n;
     }
@@ -1072,7 +1086,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
   int b = 0, n = 0, i0 = 0, first_slot = 0, h0 = 0, j1 = 0;
   if (!by_run || lo >= 0) {
     b = item_b;
-    const int len = units_of<C>(span_of<C::TILE>(p, b));
+    const int len = units_of<C>(p, span_of<C::TILE>(p, b));
     if (len) {
       const int hh = by_run ? static_cast<int>(div_units(lo - item_before * p.items, len)) : static_cast<int>(blockIdx.x) % p.items;
       const int64_t s = item_before * p.items + static_cast<int64_t>(hh) * len;  // the item's first unit
@@ -1087,14 +1101,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
   }
   // partial rows, and the order of writes to out and lse against earlier kernels, from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (blockIdx.y == 0) {
-    for (int e = blockIdx.x; e < B; e += gridDim.x) {
-      if (span_of<C::TILE>(p, e).nt) continue;
-      for (int i = tid; i < p.Hq * D; i += N) p.out[e * p.o_sb + (i / D) * p.o_sh + i % D] = __float2bfloat16_rn(0.f);
-      if (p.lse)
-        for (int h = tid; h < p.Hq; h += N) p.lse[static_cast<int64_t>(e) * p.Hq + h] = kNegInf;
-    }
-  }
+  if (blockIdx.y == 0) empty_rows<C, D>(p);
   if (n == 0) return;
   auto row_of = [&](int k, int j) { return (static_cast<int64_t>(i0 + k) * 2 + (k == 0 ? first_slot : 0)) * p.head_rows + j; };
   // A warp finds the runs' weights 32 at a time, a run per lane. The groups share the runs of one
@@ -1148,6 +1155,13 @@ int sm_count() {
   return n;
 }
 
+// In caches whose sequences cannot be long, items are not cut, and a call is one launch instead of
+// two (eagerly 22 us instead of 25): up to kFewCap keys, or kManyCap where items alone fill a
+// quarter of the CTAs. On the GPU, 32 heads on 8, d = 128, bf16, lengths up to the capacity, uncut
+// against cut: 16 sequences at 512 10.3 and 11.8 us, at 1024 16.5 and 13.8; 64 at 512 19.1 and
+// 22.6, at 1024 37.3 and 31.7; one at 256 7.0 and 7.5, at 512 9.9 and 8.2; 4-bit caches alike.
+constexpr int kFewCap = 320, kManyCap = 640;
+
 template <int D, int NT, bool Q4>
 int cta_count() {
   return std::min(sm_count() * Cfg<D, NT, Q4>::CTAS, kPagedMaxCtas);
@@ -1173,9 +1187,12 @@ cudaError_t launch(PagedDecodeParams p, cudaStream_t stream) {
   p.head_rows = C::ROWS;
   p.chunks = (p.g + C::ROWS - 1) / C::ROWS;
   p.items = p.cache.Hkv * p.chunks;
+  const int64_t all_items = (int64_t)p.cache.B * p.items;
   p.ctas = cta_count<D, NT, Q4>();
+  p.whole = p.cache.cap <= (4 * all_items >= p.ctas ? kManyCap : kFewCap);
   p.part_acc = static_cast<float*>(p.workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_acc + (int64_t)p.ctas * 2 * C::ROWS * D);
+  if (p.whole) p.ctas = (int)std::min<int64_t>(p.ctas, all_items);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1187,9 +1204,8 @@ cudaError_t launch(PagedDecodeParams p, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, p);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.whole) return e;
   // about two blocks per SM where that many have work
-  const int64_t all_items = (int64_t)p.cache.B * p.items;
   p.comb_by_run = all_items > p.ctas;
   const int heads = std::min(p.g, C::ROWS);
   p.comb_heads = p.comb_by_run ? std::min(heads, 4) : (int)std::max<int64_t>(1, std::min<int64_t>(heads, all_items * heads / 304));

@@ -592,6 +592,21 @@ def test_decode_many_sequences_of_large_groups(q4):
 
 
 @pytest.mark.parametrize("q4", [False, True])
+@pytest.mark.parametrize("pages", [10, 20, 40, 41, 64])
+def test_decode_caches_of_short_sequences(q4, pages):
+    """Capacities on both sides of where sequences are cut, for few and for many of them."""
+    page, Hkv, Hq, d = 16, 2, 6, 128
+    full = pages * page
+    lens = [full, 0, 1, full - 1, 17, full // 2] + [37] * 60
+    wide = make_cache(lens, Hkv, page, d, q4, seed=61 + pages)
+    slopes = torch.tensor([0.5, 0.25, 0.0, 2.0 ** -6, 2.0 ** -9, -0.125], device=DEV)
+    for n in (1, 6, len(lens)):
+        small = af.PagedCache(wide.k, wide.v, wide.page_table[:n, :pages], wide.k_scales, wide.v_scales)
+        for kw in (dict(theta=1e4), dict(window=100, slopes=slopes)):
+            run_decode(lens[:n], Hq, Hkv, page, d, q4, cache=small, seed=62, **kw)
+
+
+@pytest.mark.parametrize("q4", [False, True])
 def test_sequences_may_share_pages(q4):
     """One row of the table for all sequences: its stride is 0."""
     own = make_cache([600], 2, 16, 128, q4, seed=57)
