@@ -20,7 +20,7 @@
 // Work. Sequences are cut into tiles of 64 or 128 keys; the tiles of the whole batch, ordered by
 // (sequence, KV head, chunk of query heads), are dealt to the CTAs in equal runs, from lengths read
 // on the device; an item counts for its tiles and for what its two ends cost (without that, 64
-// sequences of 1 to 8192 keys took 121 us from the 4-bit cache, with it 97). A CTA walks the
+// sequences of 1 to 8192 keys took 121 us from the 4-bit cache, with it 98). A CTA walks the
 // segments of its run. A segment that is a whole item (all tiles of one (sequence, head chunk)) is
 // finished in place; otherwise its (max, sum, acc) goes to the workspace, at most two per CTA, and
 // the combine kernel joins them in a fixed order. In caches of short sequences every segment is a
@@ -48,9 +48,12 @@ constexpr int kConsumers = kWarps * 32;
 constexpr int kThreads = kConsumers + 32;
 constexpr float kLazy = 8.0f;          // the running maximum may lag by 2^8
 
-template <int D, int NT, bool Q4>
+template <int D, int NT, bool Q4, bool PK>
 struct Cfg {
-  static constexpr int ROWS = 8 * NT;                                   // query heads per item
+  // PK (q4, at most 4 heads): columns 0-3 of the column tile take the heads' first parts of q,
+  // columns 4-7 the second ones, and the scores of both are added. One product then does for two
+  // (64 sequences of 1 to 8192 keys, 4 heads on each KV head: 90 us, without 97).
+  static constexpr int ROWS = PK ? 4 : 8 * NT;                          // query heads per item
   // 16-key blocks of a tile per warp: two hide each other's latencies and share the per-tile
   // work (q4, 8 x 32k keys, 64 heads: 86 us, with one 105); rows of 256 bytes (bf16, d = 128) keep
   // the HBM busy with one.
@@ -86,13 +89,13 @@ struct Ctl {
   int64_t wsum[kThreads / 32];
   float m[kWarps][16], l[kWarps][16];
   float slope[16];                     // ALiBi slopes over c2
-  float2 qsum[2][4][4];                // q4: minus 8 times the sum of q, per column tile, group, column pair
+  float2 qsum[2][4][4];                // q4: minus 8 times a column's sum, per column tile, group, column pair
   float qmax[16][2];                   // q4: largest |q| of a head, by half rows
 };
 
-template <int D, int NT, bool Q4>
+template <int D, int NT, bool Q4, bool PK>
 constexpr size_t smem_bytes() {
-  return 1024 + Cfg<D, NT, Q4>::OFF_CTL + sizeof(Ctl);
+  return 1024 + Cfg<D, NT, Q4, PK>::OFF_CTL + sizeof(Ctl);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -294,10 +297,10 @@ struct Walk {
 // ---------------------------------------------------------------------------------------------
 // Producer
 // ---------------------------------------------------------------------------------------------
-template <int D, int NT, bool Q4>
+template <int D, int NT, bool Q4, bool PK>
 __device__ __forceinline__ void produce(const PagedDecodeParams& p, uint8_t* smem, Ctl* ctl,
-                                        Walk<Cfg<D, NT, Q4>> w) {
-  using C = Cfg<D, NT, Q4>;
+                                        Walk<Cfg<D, NT, Q4, PK>> w) {
+  using C = Cfg<D, NT, Q4, PK>;
   constexpr int kTile = C::TILE;
   const int lane = threadIdx.x % 32;
   const PagedDev& c = p.cache;
@@ -410,10 +413,10 @@ __device__ __forceinline__ float q_scale(const Ctl* ctl, int j, bool up) {
   return __uint_as_float((up ? 127u + 14u + 127u - e : 127u + 22u - 14u + e - 127u) << 23);
 }
 
-template <int D, int NT, bool Q4>
+template <int D, int NT, bool Q4, bool PK>
 __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* smem, Ctl* ctl,
-                                        Walk<Cfg<D, NT, Q4>> w) {
-  using C = Cfg<D, NT, Q4>;
+                                        Walk<Cfg<D, NT, Q4, PK>> w) {
+  using C = Cfg<D, NT, Q4, PK>;
   constexpr int BPW = C::BPW;
   constexpr int KS = D / 16;       // 16-element steps of a row
   constexpr int G = D / kQ4Group;
@@ -492,8 +495,9 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
                         (i & 3) * 4 + ((i >> 2) & 1) * 2;
           *reinterpret_cast<__half*>(at) = a;
           *reinterpret_cast<__half*>(at + D / 64 * 512) = b;
-          *reinterpret_cast<__half*>(at + NT * C::QFRAG) = __float2half_rn(u - __half2float(a));
-          *reinterpret_cast<__half*>(at + NT * C::QFRAG + D / 64 * 512) = __float2half_rn(v - __half2float(b));
+          uint8_t* rest = at + (PK ? 4 * 4 * 16 : NT * C::QFRAG);
+          *reinterpret_cast<__half*>(rest) = __float2half_rn(u - __half2float(a));
+          *reinterpret_cast<__half*>(rest + D / 64 * 512) = __float2half_rn(v - __half2float(b));
         } else {
           uint16_t* hi = reinterpret_cast<uint16_t*>(smem + C::OFF_Q + j * C::QROW);
           uint16_t* lo = reinterpret_cast<uint16_t*>(smem + C::OFF_Q + (C::ROWS + j) * C::QROW);
@@ -535,11 +539,13 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
         for (int g = 0; g < G; ++g) {
           float x[4];
           const uint4 h = lds128(base + C::OFF_Q + nt * C::QFRAG + g * 512 + lane * 16);
-          const uint4 v = lds128(base + C::OFF_Q + (NT + nt) * C::QFRAG + g * 512 + lane * 16);
           mma_f16_0(x, eight, h.x, h.y);
           mma_f16(x, eight, h.z, h.w);
-          mma_f16(x, eight, v.x, v.y);
-          mma_f16(x, eight, v.z, v.w);
+          if constexpr (!PK) {
+            const uint4 v = lds128(base + C::OFF_Q + (NT + nt) * C::QFRAG + g * 512 + lane * 16);
+            mma_f16(x, eight, v.x, v.y);
+            mma_f16(x, eight, v.z, v.w);
+          }
           if (r == 0) ctl->qsum[nt][g][t] = make_float2(-x[0], -x[1]);
         }
     }
@@ -551,10 +557,10 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int j = nt * 8 + 2 * t + e;
-        c2[nt][e] = Q4 ? fmaxf(p.scale_log2 * q_scale<D>(ctl, j, false), 1e-44f) : p.scale_log2;
+        const int j = nt * 8 + 2 * t + e, head = PK ? j & 3 : j;
+        c2[nt][e] = Q4 ? fmaxf(p.scale_log2 * q_scale<D>(ctl, head, false), 1e-44f) : p.scale_log2;
         // (every warp writes the same values, and reads its own)
-        if (p.slopes && r == 0) ctl->slope[j] = j < rows ? __fdiv_rn(__ldg(p.slopes + h0 + j) * kLog2e, c2[nt][e]) : 0.f;
+        if (p.slopes && r == 0) ctl->slope[j] = head < rows ? __fdiv_rn(__ldg(p.slopes + h0 + head) * kLog2e, c2[nt][e]) : 0.f;
         th[nt][e] = kNegInf;
         nm[nt][e] = 0.f;  // minus the maximum (log2 units); 0 while there is none (th is -inf then)
       }
@@ -620,7 +626,7 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               qh[nt] = lds128(base + C::OFF_Q + nt * C::QFRAG + g * 512 + lane * 16);
-              ql[nt] = lds128(base + C::OFF_Q + (NT + nt) * C::QFRAG + g * 512 + lane * 16);
+              if constexpr (!PK) ql[nt] = lds128(base + C::OFF_Q + (NT + nt) * C::QFRAG + g * 512 + lane * 16);
               qs[nt] = lds64(smem_u32(&ctl->qsum[nt][g][t]));
             }
 #pragma unroll
@@ -635,8 +641,10 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
                 float x[4];
                 mma_f16_c(x, a[0], qh[nt].x, qh[nt].y, __uint_as_float(qs[nt].x), __uint_as_float(qs[nt].y));
                 mma_f16(x, a[1], qh[nt].z, qh[nt].w);
-                mma_f16(x, a[0], ql[nt].x, ql[nt].y);
-                mma_f16(x, a[1], ql[nt].z, ql[nt].w);
+                if constexpr (!PK) {
+                  mma_f16(x, a[0], ql[nt].x, ql[nt].y);
+                  mma_f16(x, a[1], ql[nt].z, ql[nt].w);
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   const float f = e < 2 ? sa : sb;
@@ -644,6 +652,12 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
                 }
               }
             }
+          }
+          if constexpr (PK) {  // both parts of q; columns j and j + 4 are the same head from here on
+#pragma unroll
+            for (int u = 0; u < BPW; ++u)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[u][0][e] += __shfl_xor_sync(0xffffffffu, s[u][0][e], 2);
           }
         } else {
 #pragma unroll
@@ -993,10 +1007,10 @@ __device__ __forceinline__ void empty_rows(const PagedCombineParams& p) {
   }
 }
 
-template <int D, int NT, bool Q4>
-__global__ void __launch_bounds__(kThreads, Cfg<D, NT, Q4>::CTAS)
+template <int D, int NT, bool Q4, bool PK>
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT, Q4, PK>::CTAS)
     paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
-  using C = Cfg<D, NT, Q4>;
+  using C = Cfg<D, NT, Q4, PK>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + C::OFF_CTL);
@@ -1042,8 +1056,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, Q4>::CTAS)
   if (p.whole) empty_rows<C, D>(p);
   if (len > 0) {
     const Walk<C> w(p, ctl->b0, ctl->rem0, len);
-    if (tid >= kConsumers) produce<D, NT, Q4>(p, smem, ctl, w);
-    else consume<D, NT, Q4>(p, smem, ctl, w);
+    if (tid >= kConsumers) produce<D, NT, Q4, PK>(p, smem, ctl, w);
+    else consume<D, NT, Q4, PK>(p, smem, ctl, w);
   }
 }
 
@@ -1162,25 +1176,25 @@ int sm_count() {
 // 22.6, at 1024 37.3 and 31.7; one at 256 7.0 and 7.5, at 512 9.9 and 8.2; 4-bit caches alike.
 constexpr int kFewCap = 320, kManyCap = 640;
 
-template <int D, int NT, bool Q4>
+template <int D, int NT, bool Q4, bool PK>
 int cta_count() {
-  return std::min(sm_count() * Cfg<D, NT, Q4>::CTAS, kPagedMaxCtas);
+  return std::min(sm_count() * Cfg<D, NT, Q4, PK>::CTAS, kPagedMaxCtas);
 }
 
-template <int D, int NT, bool Q4>
+template <int D, int NT, bool Q4, bool PK>
 cudaError_t launch(PagedDecodeParams p, cudaStream_t stream) {
-  using C = Cfg<D, NT, Q4>;
-  static_assert(smem_bytes<D, NT, Q4>() <= 232448 && (smem_bytes<D, NT, Q4>() + 1024) * C::CTAS <= 233472,
+  using C = Cfg<D, NT, Q4, PK>;
+  static_assert(smem_bytes<D, NT, Q4, PK>() <= 232448 && (smem_bytes<D, NT, Q4, PK>() + 1024) * C::CTAS <= 233472,
                 "shared memory of the resident CTAs");
   static_assert(C::STAGES <= 8, "barriers");
-  auto kern = paged_decode_kernel<D, NT, Q4>;
+  auto kern = paged_decode_kernel<D, NT, Q4, PK>;
   static std::atomic<uint64_t> ready;  // devices that the kernel's shared memory was allowed on
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load(std::memory_order_acquire) & bit) || dev > 63) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D, NT, Q4>());
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D, NT, Q4, PK>());
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_release);
   }
@@ -1188,7 +1202,7 @@ cudaError_t launch(PagedDecodeParams p, cudaStream_t stream) {
   p.chunks = (p.g + C::ROWS - 1) / C::ROWS;
   p.items = p.cache.Hkv * p.chunks;
   const int64_t all_items = (int64_t)p.cache.B * p.items;
-  p.ctas = cta_count<D, NT, Q4>();
+  p.ctas = cta_count<D, NT, Q4, PK>();
   p.whole = p.cache.cap <= (4 * all_items >= p.ctas ? kManyCap : kFewCap);
   p.part_acc = static_cast<float*>(p.workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_acc + (int64_t)p.ctas * 2 * C::ROWS * D);
@@ -1199,7 +1213,7 @@ cudaError_t launch(PagedDecodeParams p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.ctas);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes<D, NT, Q4>();
+  cfg.dynamicSmemBytes = smem_bytes<D, NT, Q4, PK>();
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -1216,20 +1230,24 @@ cudaError_t launch(PagedDecodeParams p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, paged_combine_kernel<C, D>, static_cast<const PagedCombineParams&>(p));
 }
 
-template <int D, int NT, bool Q4>
+template <int D, int NT, bool Q4, bool PK>
 size_t workspace() {
-  return (size_t)cta_count<D, NT, Q4>() * 2 * Cfg<D, NT, Q4>::ROWS * (D * sizeof(float) + sizeof(float2));
+  return (size_t)cta_count<D, NT, Q4, PK>() * 2 * Cfg<D, NT, Q4, PK>::ROWS * (D * sizeof(float) + sizeof(float2));
 }
 
 }  // namespace
 
 // Up to 8 query heads per KV head fill one column tile; more take two (16 heads a pass), and
-// groups above 16 read the cache once per 16 heads (through L2).
-#define AFX_PAGED_DISPATCH(fn, ...)                                                              \
-  (format == kPagedQ4 ? (d == 128 ? (g <= 8 ? fn<128, 1, true>(__VA_ARGS__) : fn<128, 2, true>(__VA_ARGS__))     \
-                                  : (g <= 8 ? fn<64, 1, true>(__VA_ARGS__) : fn<64, 2, true>(__VA_ARGS__)))      \
-                      : (d == 128 ? (g <= 8 ? fn<128, 1, false>(__VA_ARGS__) : fn<128, 2, false>(__VA_ARGS__))   \
-                                  : (g <= 8 ? fn<64, 1, false>(__VA_ARGS__) : fn<64, 2, false>(__VA_ARGS__))))
+// groups above 16 read the cache once per 16 heads (through L2). Up to 4 heads, with a 4-bit
+// cache, put the two parts of q side by side.
+#define AFX_PAGED_DISPATCH(fn, ...)                                                                                    \
+  (format == kPagedQ4                                                                                                  \
+       ? (d == 128 ? (g <= 4 ? fn<128, 1, true, true>(__VA_ARGS__)                                                     \
+                             : g <= 8 ? fn<128, 1, true, false>(__VA_ARGS__) : fn<128, 2, true, false>(__VA_ARGS__))   \
+                   : (g <= 4 ? fn<64, 1, true, true>(__VA_ARGS__)                                                      \
+                             : g <= 8 ? fn<64, 1, true, false>(__VA_ARGS__) : fn<64, 2, true, false>(__VA_ARGS__)))    \
+       : (d == 128 ? (g <= 8 ? fn<128, 1, false, false>(__VA_ARGS__) : fn<128, 2, false, false>(__VA_ARGS__))          \
+                   : (g <= 8 ? fn<64, 1, false, false>(__VA_ARGS__) : fn<64, 2, false, false>(__VA_ARGS__))))
 
 size_t paged_decode_workspace(int d, int g, int format) { return AFX_PAGED_DISPATCH(workspace); }
 
@@ -1238,9 +1256,9 @@ cudaError_t launch_paged_decode(const PagedDecodeParams& p, int d, int format, c
   return AFX_PAGED_DISPATCH(launch, p, stream);
 }
 
-template <int D, int NT, bool Q4>
+template <int D, int NT, bool Q4, bool PK>
 int tile() {
-  return Cfg<D, NT, Q4>::TILE;
+  return Cfg<D, NT, Q4, PK>::TILE;
 }
 
 int paged_frag_rows(int page_size, int d, int g, int format) {
