@@ -144,7 +144,7 @@ int check_index(const int32_t* p, bool need, const char* name) {
   return ATTNFUSE_OK;
 }
 
-// One thread block per 8 to 32 rows of the call and run of heads: B * N rows stay below 2^31.
+// One thread block per 2 to 32 rows of the call and run of heads: B * N rows stay below 2^31.
 int check_n(int B, int N) {
   if (N <= 0) return fail(ATTNFUSE_ERR_INVALID_ARG, "N=%d must be positive", N);
   if ((int64_t)B * N > 0x7fffffff) return fail(ATTNFUSE_ERR_UNSUPPORTED, "B * N too large");

@@ -4,7 +4,7 @@
 // A row of K and V is read once and written once, and HBM bounds the gather (187 MB of bf16 rows,
 // d = 64: 31 us, 89% of a copy's rate) and, with the launch's ragged end, the bf16 append (138 MB,
 // 18.5k rows of 8 heads, d = 128, rotated: 28 us, 72%). Appending to 4 bits (12k rows of 8 heads,
-// d = 128: 24 us, 37%) is bound by its instructions: 566 per warp, the idle rows' included, keep
+// d = 128: 23 us, 38%) is bound by its instructions: 566 per warp, the idle rows' included, keep
 // the schedulers issuing 68% of the time.
 #include <cuda_runtime.h>
 
@@ -17,7 +17,10 @@ namespace afx {
 
 namespace {
 
-constexpr int kThreads = 256;
+// The threads that a block's barrier and its slowest load hold up. Prompts to bf16 and to 4 bits
+// (with their gather), one token: 128 threads 28.1, 33.5, 2.4 us; 64 (one row of 8 heads shares its
+// angles) 36.6, 34.2, 2.4; 256 28.1, 34.6, 2.6; 512 32.9, 38.5, 2.9.
+constexpr int kThreads = 128;
 
 // Sequence and row of row number `row` < 2^31 of the call.
 __device__ __forceinline__ int seq_of(uint64_t div_n, int64_t row) {
