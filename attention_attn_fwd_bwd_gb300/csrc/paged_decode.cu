@@ -48,6 +48,21 @@ constexpr int kConsumers = kWarps * 32;
 constexpr int kThreads = kConsumers + 32;
 constexpr float kLazy = 8.0f;          // the running maximum may lag by 2^8
 
+// Weights from a 4-bit cache enter the second product as ONE fp16 of p * step * mul, mul a power of
+// two for each head and group (a second fp16 would cost 16 more products per 16 keys, of 32). mul
+// takes the largest p * step that the warp has seen in its segment, not the largest step, to
+// 2^kWeightBits or more: a key of large values that a head gives no weight leaves the other keys
+// their bits. It is renewed where a step * mul passes 2^kStepBits or the maximum is renewed, which
+// may lag by 2^kLazyQ4, so weights stay below 2^15. They have their 11 bits down to 2^-14 and are
+// off by at most 2^-25 below that: n keys together by n 2^-(25 + kWeightBits) of the largest.
+// (8 x 32k keys, 64 heads, normal values: 86.5 us, with one mul for all heads, from the largest
+// step alone, 85; values of sizes e^(2z), z normal: 90 and 85; a first key 2^10 above the others
+// with values 1/64 of theirs, after which every tile of its segment renews mul: 104 and 85.
+// kLazyQ4, kWeightBits, kStepBits 3, 5, 11: 87, 94, 107; 5, 3, 10: 86.5, 89, 105; 3, 4, 12: 87, 89, 88.)
+constexpr float kLazyQ4 = 4.0f;
+constexpr uint32_t kWeightBits = 4, kStepBits = 11;
+constexpr uint32_t kFirstMul = 253;    // biased exponent before any key: every step renews it
+
 template <int D, int NT, bool Q4, bool PK>
 struct Cfg {
   // PK (q4, at most 4 heads): columns 0-3 of the column tile take the heads' first parts of q,
@@ -153,9 +168,15 @@ __device__ __forceinline__ void mma_f16_c(float (&d)[4], const uint32_t (&a)[4],
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t w;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(w) : "r"(x), "r"(y));
+  return w;
+}
+// (saturating: scores past 2^25, whose neighbours lie 4 apart in fp32, may pass a lagging maximum by more)
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t w;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
   return w;
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
@@ -569,12 +590,13 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
     // q4: O rows r come out 2^-22 and rows r + 8 2^-18 times what they should be. After the products
     // with 16 keys' n, the same with -8: the sums never carry more than one block's 8 w.
     const uint32_t minus8[4] = {0x80208020u, 0x82008200u, 0x80208020u, 0x82008200u};
-    // Weights p * step go into fp16 as p * step * vmul[g], vmul = 2^-e of the largest step
-    // seen so far in group g (it may be exceeded by 2^4 before it is renewed)
-    uint32_t vthr[Q4 ? G / 2 : 1] = {};
-    float vmul[Q4 ? G : 1];
+    uint32_t mul[NT][2][Q4 ? G / 2 : 1];  // of this lane's columns, for two groups each as bf16
 #pragma unroll
-    for (int g = 0; g < (Q4 ? G : 1); ++g) vmul[g] = 1.f;
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int q = 0; q < (Q4 ? G / 2 : 1); ++q) mul[nt][e][q] = kFirstMul * 0x00800080u;
 
     for (int i = 0; i < w.n; ++i, st = st + 1 == C::STAGES ? 0 : st + 1, phase ^= st == 0) {
       if (ok) ok = mbar_wait(&ctl->full[st], phase, p.status, &ctl->abort_flag);
@@ -742,13 +764,18 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
             if constexpr (BPW == 2) mx[nt][e] = fmaxf(fmaxf(mx[nt][e], s[BPW - 1][nt][e]), s[BPW - 1][nt][e + 2]);
             up |= mx[nt][e] > th[nt][e];
           }
-        uint32_t vx[Q4 ? G / 2 : 1];
         if constexpr (Q4) {
+          constexpr uint32_t kMost = (127 + kStepBits) * 0x00800080u;
+          uint32_t most = kMost;
 #pragma unroll
           for (int q = 0; q < G / 2; ++q) {
-            vx[q] = __vmaxu2(__vmaxu2(vs[0][0][q], vs[0][1][q]), __vmaxu2(vs[BPW - 1][0][q], vs[BPW - 1][1][q]));
-            up |= __vmaxu2(vx[q], vthr[q]) != vthr[q];
+            const uint32_t x = __vmaxu2(__vmaxu2(vs[0][0][q], vs[0][1][q]), __vmaxu2(vs[BPW - 1][0][q], vs[BPW - 1][1][q]));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) most = __vmaxu2(most, mul_bf16x2(x, mul[nt][e][q]));
           }
+          up |= most != kMost;
         }
         if (__any_sync(0xffffffffu, up)) {
           float f[NT][2];
@@ -760,7 +787,7 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
 #pragma unroll
               for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
               f[nt][e] = 1.f;
-              const float lazy = __fdividef(kLazy, c2[nt][e]);
+              const float lazy = __fdividef(Q4 ? kLazyQ4 : kLazy, c2[nt][e]);
               if (x > th[nt][e] - lazy) {  // above the present maximum
                 const float m = x * c2[nt][e];
                 f[nt][e] = th[nt][e] == kNegInf ? 0.f : ex2_approx(-nm[nt][e] - m);
@@ -769,38 +796,52 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
                 l[nt][e] *= f[nt][e];
               }
             }
-          float fv[Q4 ? G : 1];
-          if constexpr (Q4) {
-#pragma unroll
-            for (int q = 0; q < G / 2; ++q) {
-              uint32_t x = vx[q];
-#pragma unroll
-              for (int off = 4; off < 32; off <<= 1) x = __vmaxu2(x, __shfl_xor_sync(0xffffffffu, x, off));
-              uint32_t thr = 0;
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t old = (vthr[q] >> (16 * e)) & 0xFFFFu, now = (x >> (16 * e)) & 0xFFFFu;
-                const int g = 2 * q + e;
-                fv[g] = 1.f;
-                uint32_t lim = old;
-                if (now > old) {
-                  const uint32_t ex = min(now >> 7, 253u);  // biased exponent of the largest step
-                  const float mul = __uint_as_float((254u - ex) << 23);
-                  fv[g] = mul * __fdiv_rn(1.f, vmul[g]);
-                  vmul[g] = mul;
-                  lim = min(((ex + 4) << 7) | 0x7Fu, 0x7FFFu);
-                }
-                thr |= lim << (16 * e);
-              }
-              vthr[q] = thr;
-            }
-          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int k = 0; k < MT; ++k)
+            for (int e = 0; e < 2; ++e) {
+              if constexpr (Q4) {
+                float p4[2 * BPW];  // the weights of this lane's keys
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[nt][k][e] *= Q4 ? f[nt][e & 1] * fv[Q4 ? k / 2 : 0] : f[nt][e & 1];
+                for (int i = 0; i < 2 * BPW; ++i) p4[i] = ex2_approx(fmaf(s[i / 2][nt][e + 2 * (i & 1)], c2[nt][e], nm[nt][e]));
+#pragma unroll
+                for (int q = 0; q < G / 2; ++q) {
+                  float big[2] = {0.f, 0.f};  // the tile's largest p * step of both groups
+#pragma unroll
+                  for (int i = 0; i < 2 * BPW; ++i) {
+                    big[0] = fmaxf(big[0], p4[i] * bf16lo_to_f32(vs[i / 2][i & 1][q]));
+                    big[1] = fmaxf(big[1], p4[i] * bf16hi_to_f32(vs[i / 2][i & 1][q]));
+                  }
+                  uint32_t two = __byte_perm(__float_as_uint(big[0]), __float_as_uint(big[1]), 0x7632);
+#pragma unroll
+                  for (int off = 4; off < 32; off <<= 1) two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, off));
+                  const uint32_t old = mul[nt][e][q];
+                  mul[nt][e][q] = 0;
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    // biased exponents: of mul, and of the largest p * step by the new maximum
+                    const uint32_t was = (old >> (16 * h + 7)) & 0xFFu;
+                    const float seen = f[nt][e] * __uint_as_float((254u + kWeightBits - was) << 23);
+                    const float x = fmaxf(seen, h ? bf16hi_to_f32(two) : bf16lo_to_f32(two));
+                    const uint32_t now = 254u + kWeightBits - min(max(__float_as_uint(x) >> 23, 1u + kWeightBits), 254u);
+                    mul[nt][e][q] |= now << (16 * h + 7);
+                    const int d = min(max(static_cast<int>(now) - static_cast<int>(was), -126), 126);
+                    const float by = f[nt][e] * __uint_as_float((127u + d) << 23);
+                    const int k = 2 * (2 * q + h);
+                    o[nt][k][e] *= by;
+                    o[nt][k][e + 2] *= by;
+                    o[nt][k + 1][e] *= by;
+                    o[nt][k + 1][e + 2] *= by;
+                  }
+                }
+              } else {
+#pragma unroll
+                for (int k = 0; k < MT; ++k) {
+                  o[nt][k][e] *= f[nt][e];
+                  o[nt][k][e + 2] *= f[nt][e];
+                }
+              }
+            }
         }
         // ---- weights ----
 #pragma unroll
@@ -837,12 +878,16 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
               uint32_t a[2][4];
 #pragma unroll
               for (int e = 0; e < 2; ++e) raw_nibbles(vw[e][g], a[0][2 * e], a[0][2 * e + 1], a[1][2 * e], a[1][2 * e + 1]);
-              const float sa = ((g & 1) ? bf16hi_to_f32(vs[u][0][g / 2]) : bf16lo_to_f32(vs[u][0][g / 2])) * vmul[g];
-              const float sb = ((g & 1) ? bf16hi_to_f32(vs[u][1][g / 2]) : bf16lo_to_f32(vs[u][1][g / 2])) * vmul[g];
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                const uint32_t b0 = movm(pack_f16x2(s[u][nt][0] * sa, s[u][nt][1] * sa));
-                const uint32_t b1 = movm(pack_f16x2(s[u][nt][2] * sb, s[u][nt][3] * sb));
+                float x[4];  // p * step * mul
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t two = mul_bf16x2(vs[u][e / 2][g / 2], mul[nt][e & 1][g / 2]);
+                  x[e] = s[u][nt][e] * ((g & 1) ? bf16hi_to_f32(two) : bf16lo_to_f32(two));
+                }
+                const uint32_t b0 = movm(pack_f16x2(x[0], x[1]));
+                const uint32_t b1 = movm(pack_f16x2(x[2], x[3]));
                 mma_f16(o[nt][2 * g], a[0], b0, b1);
                 mma_f16(o[nt][2 * g + 1], a[1], b0, b1);
                 mma_f16(o[nt][2 * g], minus8, b0, b1);
@@ -923,7 +968,8 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
         const float f = th[nt][e] == kNegInf ? 0.f : ex2_approx(-nm[nt][e] - bs);
 #pragma unroll
         for (int k = 0; k < MT; ++k) {
-          const float fk = Q4 ? f * __fdiv_rn(1.f, vmul[Q4 ? k / 2 : 0]) : f;
+          // (mul is a power of two of exponent 1 to 253)
+          const float fk = Q4 ? f * __uint_as_float((254u << 23) - (((mul[nt][e][Q4 ? k / 4 : 0] >> (16 * (k / 2 & 1))) & 0xFFFFu) << 16)) : f;
           o[nt][k][e] *= Q4 ? 0x1p22f : 1.f;
           o[nt][k][e + 2] *= Q4 ? 0x1p18f : 1.f;
           o[nt][k][e] *= fk;
