@@ -42,7 +42,7 @@ struct PagedDev {
   int B, Hkv;
 };
 
-// theta_i / (2 pi) for i < d/2 as the sum of three floats (all of a double): x + y + z.
+// theta^(-2i/d) / (2 pi) for i < d/2 as the sum of three floats (about 72 bits), less whole numbers: x + y + z.
 struct PagedFreqs {
   float4 f[64];
 };

@@ -117,20 +117,47 @@ int check_rope(int* mode, float theta) {
   return ATTNFUSE_OK;
 }
 
-// The frequencies of a theta; a thread keeps those of its last call (64 pow cost as much as a
-// launch).
+// A sum of two doubles, hi the nearest double to it (about 104 bits). Products and sums as in Dekker,
+// "A floating-point technique for extending the available precision", 1971, with fused
+// multiply-adds, which the compiler is not left to form by itself: all machines get the same bits.
+struct Double2 {
+  double hi, lo;
+};
+Double2 sum_of(double a, double b) {  // |a| >= |b| or a = 0
+  const double s = a + b;
+  return {s, b - (s - a)};
+}
+Double2 times(Double2 a, Double2 b) {
+  const double p = a.hi * b.hi, e = std::fma(a.hi, b.hi, -p);
+  return sum_of(p, std::fma(a.hi, b.lo, std::fma(a.lo, b.hi, e)));
+}
+Double2 inverse(double x) {
+  const double q = 1.0 / x;
+  return sum_of(q, std::fma(-q, x, 1.0) * q);
+}
+Double2 root(Double2 a) {
+  const double s = std::sqrt(a.hi);
+  return sum_of(s, (std::fma(-s, s, a.hi) + a.lo) / (2.0 * s));
+}
+
+// The frequencies of a theta; a thread keeps those of its last call (they cost as much as a launch).
+// The kernels multiply them by positions up to 2^24, so a double's 53 bits would leave an angle
+// 2^-29 off. Whole turns per position (theta < 0.16) drop out, positions being whole numbers.
 const PagedFreqs& paged_freqs(int d, float theta) {
   static thread_local PagedFreqs f;
   static thread_local int have_d = 0;
   static thread_local float have_theta = 0.f;
   if (have_d != d || have_theta != theta) {
     memset(&f, 0, sizeof(f));
-    const double two_pi = 6.283185307179586476925286766559;
-    for (int i = 0; i < d / 2; ++i) {
-      double x = std::pow((double)theta, -2.0 * i / d) / two_pi;
-      x -= (f.f[i].x = (float)x);
-      x -= (f.f[i].y = (float)x);
-      f.f[i].z = (float)x;
+    Double2 step = inverse(theta);  // theta^(-2 / d)
+    for (int n = d / 2; n > 1; n /= 2) step = root(step);
+    Double2 turn = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};  // 1 / (2 pi)
+    for (int i = 0; i < d / 2; ++i, turn = times(turn, step)) {
+      const Double2 part = sum_of(turn.hi - std::rint(turn.hi), turn.lo);
+      f.f[i].x = (float)part.hi;
+      const double rest = (part.hi - f.f[i].x) + part.lo;
+      f.f[i].y = (float)rest;
+      f.f[i].z = (float)(rest - f.f[i].y);
     }
     have_d = d;
     have_theta = theta;

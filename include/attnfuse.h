@@ -365,8 +365,8 @@ typedef struct {
 /* Append rows: k, v [B, Hkv, N, d] bf16 (strides as in attnfuse_fwd). Row n < count[b] of
  * sequence b becomes position start[b] + n; rows at and behind count[b] (padding) are not read.
  * count NULL: all N. rope_mode NONE or FUSED (AUTO means FUSED): K is rotated at its position,
- * K' = bf16(fp32(R_p k)), where R_p k is off by at most 2^-34 (|k_i| + |k_{i + d/2}|) at positions up
- * to 2^12. A slot's bits do not depend on the batch it was written in. N = 1 is the decode step's form. */
+ * K' = bf16(fp32(R_p k)), where R_p k is off by at most 2^-34 (|k_i| + |k_{i + d/2}|) at any position
+ * (rope_theta >= 2^-16). A slot's bits do not depend on the batch it was written in. N = 1 is the decode step's form. */
 attnfuse_status attnfuse_paged_append(const attnfuse_paged_cache* cache, const void* k,
                                       const int64_t k_strides[4], const void* v,
                                       const int64_t v_strides[4], const int32_t* start,

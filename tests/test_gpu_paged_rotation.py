@@ -73,3 +73,10 @@ def check(positions, d, theta):
 @pytest.mark.parametrize("d,theta", [(128, 1e4), (64, 5e5), (128, 5e5)])
 def test_keys_next_to_a_border(d, theta):
     check([1, 2, 77, 500, 1023, 2500, 4095, 30000], d, theta)
+
+
+@pytest.mark.parametrize("d,theta", [(128, 1e4), (64, 5e5), (128, 0.5), (64, 2.0 ** -16)])
+def test_keys_next_to_a_border_at_far_positions(d, theta):
+    """Where a rounding of the frequency itself is multiplied by the position."""
+    top = 1 << 24
+    check([top - 1, top - 2, top - 12345, 15_000_001, 12_345_678, 3_000_003, 1_000_000, 131_071], d, theta)
