@@ -623,7 +623,7 @@ def _want(t, name, dtype, shape, device, contiguous=False):
         _need(t, name, (dtype,), shape, device, contiguous)
 
 
-_HERE = contextlib.nullcontext()
+_CURRENT = contextlib.nullcontext()
 
 
 def _on(stream, device):
@@ -632,7 +632,7 @@ def _on(stream, device):
     import torch
 
     if stream is None:
-        return _HERE
+        return _CURRENT
     if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     return torch.cuda.stream(stream)
