@@ -787,7 +787,8 @@ def paged_gather(cache, start, count, N, k=None, v=None, stream=None):
 
 
 def paged_decode_workspace_size(Hq, Hkv, d, cache_format):
-    """Bytes of workspace for paged_decode on the current device (independent of the lengths)."""
+    """Bytes of workspace for paged_decode on the current device (independent of the lengths and of
+    B; the two cache formats need different ones)."""
     n = ctypes.c_size_t()
     _check(load().attnfuse_paged_decode_workspace_size(Hq, Hkv, d, cache_format, ctypes.byref(n)))
     return n.value

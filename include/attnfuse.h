@@ -393,8 +393,9 @@ attnfuse_status attnfuse_paged_gather(const attnfuse_paged_cache* cache, const i
  * page_size at most 2^42. Sequences of any mix of lengths share the GPU evenly: the work is cut
  * into equal runs of tiles of 64 or 128 keys over the whole batch. Results do not vary from run
  * to run. workspace: attnfuse_paged_decode_workspace_size bytes, 16-byte
- * aligned; it depends on the device, d and Hq / Hkv only, not on lengths. Calls that may
- * overlap need workspaces of their own. */
+ * aligned; it depends on the device, the cache's format, d and Hq / Hkv, not on lengths or B (for
+ * caches of both formats take the larger of two queries). Calls that may overlap need workspaces
+ * of their own. */
 attnfuse_status attnfuse_paged_decode_workspace_size(int Hq, int Hkv, int d, int format, size_t* bytes);
 
 attnfuse_status attnfuse_paged_decode(const attnfuse_paged_cache* cache, const void* q,
