@@ -101,6 +101,7 @@ struct PagedDecodeParams : PagedCombineParams {
   int* status;
 };
 constexpr int kPagedMaxCtas = 1024;
+int paged_sm_count();  // SMs of the current device
 cudaError_t launch_paged_append(PagedAppendParams p, int d, int format, bool rope, cudaStream_t stream);
 cudaError_t launch_paged_gather(PagedGatherParams p, int d, int format, cudaStream_t stream);
 size_t paged_decode_workspace(int d, int g, int format);

@@ -27,10 +27,9 @@ __device__ __forceinline__ int seq_of(uint64_t div_n, int64_t row) {
   return static_cast<int>(div_n ? __umul64hi(static_cast<uint64_t>(row), div_n) : row);
 }
 
-// Row of this thread: sequence b, row n of the call, position pos; false if there is none.
+// Where a row lies in the cache.
 struct RowAt {
-  int b, n, page, slot;
-  float pos;
+  int page, slot;
 };
 
 __device__ __forceinline__ void raise_page(int* status) { atomicOr(status, kDevPageRange); }
@@ -51,9 +50,6 @@ __device__ __forceinline__ bool find_row(const PagedDev& c, int b, int n, int fi
     raise_page(status);
     return false;
   }
-  r->b = b;
-  r->n = n;
-  r->pos = static_cast<float>(p);
   r->page = page_at(c, b, static_cast<int>(p), &r->slot);
   if (r->page < 0) raise_page(status);
   return r->page >= 0;
@@ -372,9 +368,9 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
   }
 }
 
-// Heads per thread of the gather: two, unless their threads would not fill the GPU's slots.
+// Heads per thread of the gather: two, unless their threads would be fewer than 1024 per SM.
 int gather_heads(int64_t rows, int tpr, int Hkv) {
-  return Hkv > 1 && rows * tpr * Hkv >= 2 * 152 * 1024 ? kGatherHeads : 1;
+  return Hkv > 1 && rows * tpr * Hkv >= kGatherHeads * 1024 * static_cast<int64_t>(paged_sm_count()) ? kGatherHeads : 1;
 }
 
 // Heads per block of the append: angles (about 2.6 times a row-head's other work, per row) are

@@ -1203,18 +1203,6 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
   }
 }
 
-int sm_count() {
-  static std::atomic<int> known[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
-  int n = known[dev].load(std::memory_order_relaxed);
-  if (n == 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
-    known[dev].store(n, std::memory_order_relaxed);
-  }
-  return n;
-}
-
 // In caches whose sequences cannot be long, items are not cut, and a call is one launch instead of
 // two (eagerly 22 us instead of 25): up to kFewCap keys, or kManyCap where items alone fill a
 // quarter of the CTAs. On the GPU, 32 heads on 8, d = 128, bf16, lengths up to the capacity, uncut
@@ -1224,7 +1212,7 @@ constexpr int kFewCap = 320, kManyCap = 640;
 
 template <int D, int NT, bool Q4, bool PK>
 int cta_count() {
-  return std::min(sm_count() * Cfg<D, NT, Q4, PK>::CTAS, kPagedMaxCtas);
+  return std::min(paged_sm_count() * Cfg<D, NT, Q4, PK>::CTAS, kPagedMaxCtas);
 }
 
 template <int D, int NT, bool Q4, bool PK>
@@ -1268,7 +1256,7 @@ cudaError_t launch(PagedDecodeParams p, cudaStream_t stream) {
   // about two blocks per SM where that many have work
   p.comb_by_run = all_items > p.ctas;
   const int heads = std::min(p.g, C::ROWS);
-  p.comb_heads = p.comb_by_run ? std::min(heads, 4) : (int)std::max<int64_t>(1, std::min<int64_t>(heads, all_items * heads / 304));
+  p.comb_heads = p.comb_by_run ? std::min(heads, 4) : (int)std::max<int64_t>(1, std::min<int64_t>(heads, all_items * heads / (2 * paged_sm_count())));
   cfg.gridDim = dim3((unsigned)std::min<int64_t>(all_items, p.ctas),
                      (heads + p.comb_heads - 1) / p.comb_heads);
   cfg.blockDim = dim3(256);
@@ -1282,6 +1270,18 @@ size_t workspace() {
 }
 
 }  // namespace
+
+int paged_sm_count() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
 
 // Up to 8 query heads per KV head fill one column tile; more take two (16 heads a pass), and
 // groups above 16 read the cache once per 16 heads (through L2). (4-bit, 8 x 32k keys, 16 heads on
