@@ -4,24 +4,28 @@
 //   s_n = scale <R_{L-1} q_h, k_n> + slope_h (n - (L - 1)),  L = lens[b].
 //
 // The cache is read once, from HBM, and that bounds the bf16 kernel (8 sequences of 32768 keys,
-// Hq = 64, Hkv = 8, d = 128: 164 us, 97% of a copy's rate). The matrix instructions are warp-level
+// Hq = 64, Hkv = 8, d = 128: 162 us, 97% of a copy's rate). The matrix instructions are warp-level
 // ones with the KEYS as rows (S^T = K Q^T, O^T = V^T P^T): their operands come straight from
 // registers, which is where 4-bit codes have to be expanded (writing them back to shared memory as
 // 16-bit values for tcgen05 would move 94 of the 128 bytes per cycle that shared memory has, and as
 // much again to read them), and a group of 8 query heads fills the instruction's 8 columns, where
 // a 128-row query tile would be padding.
 //
-// The 4-bit kernel (the same sequences: 86 us, 52% of a copy's rate) is bound by its arithmetic.
-// Measured on GB300, a warp-level product takes a sub-partition 8 cycles and no FMA-pipe
-// instruction runs beside it (packed fp16 takes that pipe 2 cycles), while integer logic (2 cycles
-// each) does. So codes are expanded by logic alone, and what that leaves out, the offset of the
-// codes, is taken out by products of a constant.
+// The 4-bit kernel (the same sequences: 87 us, 51% of a copy's rate) is bound by no single unit: the
+// tensor pipe is busy 36% of the time, integer logic 48%, issue slots 55%, and three consumer warps
+// per scheduler, at 128 registers with a few of them spilled (48 bytes a thread; 372 bytes at 168
+// registers for more than 8 heads on a KV head), leave latencies in the open. Its loads alone,
+// without any arithmetic, take 52 to 63 us. Of what can be cut, products weigh most: measured on
+// GB300, a warp-level product takes a sub-partition 8 cycles and no FMA-pipe instruction runs beside
+// it (packed fp16 takes that pipe 2 cycles), while integer logic (2 cycles each) does. So codes are
+// expanded by logic alone, and what that leaves out, the offset of the codes, is taken out by
+// products of a constant.
 //
 // Work. Sequences are cut into tiles of 64 or 128 keys; the tiles of the whole batch, ordered by
 // (sequence, KV head, chunk of query heads), are dealt to the CTAs in equal runs, from lengths read
 // on the device; an item counts for its tiles and for what its two ends cost (without that, 64
-// sequences of 1 to 8192 keys took 121 us from the 4-bit cache, with it 98). A CTA walks the
-// segments of its run. A segment that is a whole item (all tiles of one (sequence, head chunk)) is
+// sequences of 1 to 8192 keys took 121 us from the 4-bit cache where they took 98 with it). A CTA
+// walks the segments of its run. A segment that is a whole item (all tiles of one (sequence, head chunk)) is
 // finished in place; otherwise its (max, sum, acc) goes to the workspace, at most two per CTA, and
 // the combine kernel joins them in a fixed order. In caches of short sequences every segment is a
 // whole item, and there is no second kernel.
@@ -67,10 +71,10 @@ template <int D, int NT, bool Q4, bool PK>
 struct Cfg {
   // PK (q4, at most 4 heads): columns 0-3 of the column tile take the heads' first parts of q,
   // columns 4-7 the second ones, and the scores of both are added. One product then does for two
-  // (64 sequences of 1 to 8192 keys, 4 heads on each KV head: 90 us, without 97).
+  // (64 sequences of 1 to 8192 keys, 4 heads on each KV head: 88 us, without 96).
   static constexpr int ROWS = PK ? 4 : 8 * NT;                          // query heads per item
   // 16-key blocks of a tile per warp: two hide each other's latencies and share the per-tile
-  // work (q4, 8 x 32k keys, 64 heads: 86 us, with one 105); rows of 256 bytes (bf16, d = 128) keep
+  // work (q4, 8 x 32k keys, 64 heads: 87 us, with one 102); rows of 256 bytes (bf16, d = 128) keep
   // the HBM busy with one.
   static constexpr int BPW = Q4 || D == 64 ? 2 : 1;
   static constexpr int TILE = kWarps * 16 * BPW;                        // keys
@@ -843,7 +847,7 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
               }
             }
         }
-        // ---- weights ----
+        // ---- weights (ex2.approx: within 2 units of fp32's last place, and 16 or 11 bits are kept) ----
 #pragma unroll
         for (int u = 0; u < BPW; ++u)
 #pragma unroll
@@ -1203,7 +1207,8 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
   }
 }
 
-// In caches whose sequences cannot be long, items are not cut, and a call is one launch instead of
+// In caches whose sequences cannot be long, which the host knows by the table's width alone (the
+// lengths are on the device, and a captured call has to serve all of them), items are not cut, and a call is one launch instead of
 // two (eagerly 22 us instead of 25): up to kFewCap keys, or kManyCap where items alone fill a
 // quarter of the CTAs. On the GPU, 32 heads on 8, d = 128, bf16, lengths up to the capacity, uncut
 // against cut: 16 sequences at 512 10.3 and 11.8 us, at 1024 16.5 and 13.8; 64 at 512 19.1 and
@@ -1285,7 +1290,9 @@ int paged_sm_count() {
 
 // Up to 8 query heads per KV head fill one column tile; more take two (16 heads a pass), and
 // groups above 16 read the cache once per 16 heads (through L2). (4-bit, 8 x 32k keys, 16 heads on
-// each KV head, d = 128: 137 us, as two passes of 8 159.) Up to 4 heads, with a 4-bit cache, put
+// each KV head, d = 128: 140 us, as two passes of 8 162.) A last pass of fewer heads costs what a
+// full one does (8 x 16k keys, 4 KV heads, 16, 17, 24 and 32 heads on each: 46, 79, 80, 80 us).
+// Up to 4 heads, with a 4-bit cache, put
 // the two parts of q side by side.
 #define AFX_PAGED_DISPATCH(fn, ...)                                                                                    \
   (format == kPagedQ4                                                                                                  \
