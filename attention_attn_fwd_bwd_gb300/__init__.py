@@ -346,6 +346,8 @@ def _workspace(nbytes, device, workspace=None, reuse_table=False):
     import torch
 
     have = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if have and not workspace.is_contiguous():  # an expanded view has less memory than elements
+        have = min(have, workspace.untyped_storage().nbytes() - workspace.storage_offset() * workspace.element_size())
     if reuse_table and (workspace is None or have < nbytes):
         raise ValueError(f"ROPE_REUSE_TABLE needs the workspace that holds the table "
                          f"({nbytes} bytes); got {'none' if workspace is None else f'{have} bytes'}")
