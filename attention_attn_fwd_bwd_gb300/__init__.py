@@ -850,7 +850,7 @@ def paged_decode(q, cache, lens, scale=None, rope_theta=10000.0, rope_mode=ROPE_
     _launch(load().attnfuse_paged_decode,
             (cache._c, q.data_ptr(), _S3(*_live_strides(q)), _index(lens, "lens", cache), out.data_ptr(), os_,
              None if lse is None else lse.data_ptr(), Hq, d ** -0.5 if scale is None else scale, rope_theta, rope_mode,
-             min(window, 0x7FFFFFFF), alibi_slopes, workspace.data_ptr(), ws_n), dev, stream)
+             max(-1, min(window, 0x7FFFFFFF)), alibi_slopes, workspace.data_ptr(), ws_n), dev, stream)
     return out, lse
 
 
