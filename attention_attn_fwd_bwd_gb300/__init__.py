@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import operator
 import os
 import struct
 import threading
@@ -769,7 +770,7 @@ def paged_gather(cache, start, count, N, k=None, v=None, stream=None):
 
     if not isinstance(cache, PagedCache):
         _need_cache(cache)
-    bf16, dev, N = torch.bfloat16, cache.device, int(N)
+    bf16, dev, N = torch.bfloat16, cache.device, operator.index(N)
     shape = (cache.B, cache.Hkv, N, cache.d)
     dense = N * cache.d
     ks = vs = _S4(cache.Hkv * dense, dense, cache.d, 1)

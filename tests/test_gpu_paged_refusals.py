@@ -35,3 +35,10 @@ def test_negative_windows_of_any_size(window):
     with pytest.raises(af.AttnfuseError) as e:
         af.paged_decode(q, cache, lens, window=window)
     assert e.value.code == 1
+
+
+@pytest.mark.parametrize("N", [2.5, 3.0, "3", None])
+def test_a_gathers_row_count_is_a_whole_number(N):
+    """A fraction is not cut off."""
+    with pytest.raises(TypeError):
+        af.paged_gather(small(), None, None, N)
