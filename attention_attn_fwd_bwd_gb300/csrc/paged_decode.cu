@@ -592,7 +592,8 @@ __device__ __forceinline__ void consume(const PagedDecodeParams& p, uint8_t* sme
     __syncwarp();
     float o[NT][MT][4] = {};
     // q4: O rows r come out 2^-22 and rows r + 8 2^-18 times what they should be. After the products
-    // with 16 keys' n, the same with -8: the sums never carry more than one block's 8 w.
+    // with 16 keys' n, the same with -8: the sums never carry more than one block's 8 w, whose
+    // rounding an element keeps (about 2^-20 of the largest p * |value| in its group).
     const uint32_t minus8[4] = {0x80208020u, 0x82008200u, 0x80208020u, 0x82008200u};
     uint32_t mul[NT][2][Q4 ? G / 2 : 1];  // of this lane's columns, for two groups each as bf16
 #pragma unroll

@@ -386,10 +386,10 @@ attnfuse_status attnfuse_paged_gather(const attnfuse_paged_cache* cache, const i
  * s_n = scale <R q, k_n> [+ alibi_slopes[h] (n - (lens[b] - 1))]; alibi_slopes [Hq] fp32 or NULL.
  * out [B, Hq, d] bf16 (strides as in attnfuse_decode), lse [B, Hq] fp32 or NULL. lens[b] = 0:
  * out 0, lse -inf. rope_mode NONE or FUSED (AUTO means FUSED): q is rotated in fp32 and keeps
- * 22 or more significant bits. Weights keep 16 bits against a BF16 cache, 11 against a Q4 one, and
- * there what lies 2^18 or more below the head's largest weight * |value| of a group of 32 elements
- * keeps fewer: n keys may move an element by n 2^-29 of that largest one. Infinities in q or in
- * visible keys or values may give NaN. Hq: a multiple of Hkv up to 4096, and B * Hq * max_pages *
+ * 22 or more significant bits. Weights keep 16 bits against a BF16 cache, 11 against a Q4 one, where
+ * n keys may move an element by (n + 16) 2^-22 of the head's largest weight * |value| in the element's
+ * group of 32 besides. Infinities in q or in visible keys or values may give NaN, as may |q| >= 2^113
+ * with a Q4 cache. Hq: a multiple of Hkv up to 4096, and B * Hq * max_pages *
  * page_size at most 2^42. Sequences of any mix of lengths share the GPU evenly: the work is cut
  * into equal runs of tiles of 64 or 128 keys over the whole batch. Results do not vary from run
  * to run. workspace: attnfuse_paged_decode_workspace_size bytes, 16-byte
