@@ -132,8 +132,8 @@ Double2 times(Double2 a, Double2 b) {
   return sum_of(p, std::fma(a.hi, b.lo, std::fma(a.lo, b.hi, e)));
 }
 Double2 inverse(double x) {
-  const double q = 1.0 / x;
-  return sum_of(q, std::fma(-q, x, 1.0) * q);
+  const double q = 1.0 / x, e = std::fma(-q, x, 1.0), s = std::fma(e, q, q);
+  return {s, std::fma(e, q, q - s)};
 }
 Double2 root(Double2 a) {
   const double s = std::sqrt(a.hi);
