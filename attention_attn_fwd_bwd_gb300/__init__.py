@@ -6,7 +6,7 @@ PyTorch supplies device memory and streams. There is no CPU fallback: every call
 if ``libattnfuse.so`` is missing or fails to load.
 
 Low-level functions carry the C names (``attnfuse_fwd`` ...) and take raw pointers; the
-torch-level helpers ``fwd``, ``bwd``, ``decode``, ``rope_prerotate`` and, on a ``PagedCache``,
+torch-level helpers ``fwd``, ``bwd``, ``decode``, ``rope_prerotate``, ``rope_axes`` and, on a ``PagedCache``,
 ``paged_append``, ``paged_gather`` and ``paged_decode`` allocate outputs and workspace with torch
 and call them on the current CUDA stream.
 """
@@ -25,7 +25,7 @@ __all__ = [
     "load", "library_path", "fwd", "bwd", "decode", "rope_prerotate", "device_status",
     "fwd_workspace_size", "bwd_workspace_size", "decode_workspace_size",
     "CACHE_BF16", "CACHE_Q4", "PagedCache", "paged_append", "paged_gather", "paged_decode",
-    "paged_decode_workspace_size",
+    "paged_decode_workspace_size", "rope_axes",
 ]
 
 ROPE_NONE, ROPE_FUSED, ROPE_PREROTATE, ROPE_AUTO = 0, 1, 2, 3
@@ -95,6 +95,19 @@ class CPagedCache(ctypes.Structure):
     ]
 
 
+class CRopeAxesMap(ctypes.Structure):
+    """Mirror of the C struct attnfuse_rope_axes_map."""
+    _fields_ = [
+        ("axes", ctypes.c_int32),
+        ("sections", ctypes.c_int32 * 4),
+        ("interleaved", ctypes.c_int32),
+        ("own_spectrum", ctypes.c_int32),
+        ("rope_theta", ctypes.c_float),
+        ("positions", ctypes.c_void_p),
+        ("position_strides", ctypes.c_int64 * 3),
+    ]
+
+
 def library_path() -> str:
     return _LIB_PATH
 
@@ -131,6 +144,7 @@ def load():
             "attnfuse_paged_gather": ([P, P, P, P, P, P, P, I, P], I),
             "attnfuse_paged_decode_workspace_size": ([I, I, I, I, ctypes.POINTER(S)], I),
             "attnfuse_paged_decode": ([P, P, P, P, P, P, P, I, F, F, I, I, P, P, S, P], I),
+            "attnfuse_rope_axes": ([P, P, P, P, I, P, P, P, P, I, I, I, I, P, I, P], I),
             "attnfuse_rope_prerotate": ([P, ST, P, I, I, I, I, F, P, S, P], I),
             "attnfuse_debug_wait_timeout": ([ctypes.c_uint64, P], I),
             "attnfuse_rope_table": ([P, S, I, I, F, P], I),
@@ -853,6 +867,69 @@ def paged_decode(q, cache, lens, scale=None, rope_theta=10000.0, rope_mode=ROPE_
              None if lse is None else lse.data_ptr(), Hq, d ** -0.5 if scale is None else scale, rope_theta, rope_mode,
              max(-1, min(window, 0x7FFFFFFF)), alibi_slopes, workspace.data_ptr(), ws_n), dev, stream)
     return out, lse
+
+
+_AXES_MAP = struct.Struct("@7ifP3q")  # the fields of CRopeAxesMap
+assert _AXES_MAP.size == ctypes.sizeof(CRopeAxesMap)
+
+
+def rope_axes(q, k, positions, sections, rope_theta=10000.0, interleaved=False, own_spectrum=False,
+              inverse=False, q_out=None, k_out=None, stream=None):
+    """Rotate q [B, Hq, N, d] and k [B, Hk, N, d] (or None) bf16 by positions on one to four axes:
+    positions int32 [axes, B, N], or [axes, N] for all sequences alike (a device tensor); sections: pairs of
+    each axis, d/2 in all. interleaved: pairs are dealt to the axes in turn instead of in runs;
+    own_spectrum: the j-th pair of axis a turns at rope_theta^(-j / sections[a]) instead of pair i
+    at rope_theta^(-2i/d). inverse turns back: with dq and dk in place of q and k, the gradients. q_out
+    and k_out may be q and k. Returns (q_out, k_out); attend over them with ROPE_NONE. With a
+    stream, what the call allocates belongs to that stream."""
+    import torch
+
+    bf16 = torch.bfloat16
+    if getattr(q, "dtype", None) is not bf16 or q.dim() != 4 or not q.is_cuda:
+        _need(q, "q", (bf16,), ndim=4, dims="[B, Hq, N, d]")
+    B, Hq, N, d = q.shape
+    dev, Hk = q.device, 0
+    if k is not None:
+        if getattr(k, "dtype", None) is not bf16 or k.dim() != 4:
+            _need(k, "k", (bf16,), ndim=4, dims="[B, Hk, N, d]")
+        Hk = k.shape[1]
+        _want(k, "k", bf16, (B, Hk, N, d), dev)
+        if not Hk:
+            raise ValueError("k: no heads (pass None)")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    sections = [operator.index(n) for n in sections]
+    axes = len(sections)
+    if not 1 <= axes <= 4 or min(sections) < 1 or 2 * sum(sections) != d:
+        raise ValueError(f"sections {sections}: one to four axes of a pair or more, {d // 2} pairs in all")
+    shape = (axes, N) if getattr(positions, "ndim", None) == 2 else (axes, B, N)
+    _want(positions, "positions", torch.int32, shape, dev)
+    st = positions.stride()
+    st = (st[0], 0, st[1]) if len(shape) == 2 else st
+    qs = _S4(Hq * N * d, N * d, d, 1)
+    ks = _S4(Hk * N * d, N * d, d, 1)
+    qos, kos = qs, ks
+    if q_out is not None:
+        _want(q_out, "q_out", bf16, (B, Hq, N, d), dev)
+        qos = _S4(*_live_strides(q_out))
+    if k_out is not None:
+        _want(k_out, "k_out", bf16, (B, Hk, N, d), dev)
+        kos = _S4(*_live_strides(k_out))
+    if not q.is_contiguous():
+        qs = _S4(*_live_strides(q))
+    if k is not None and not k.is_contiguous():
+        ks = _S4(*_live_strides(k))
+    with _on(stream, dev):
+        if q_out is None:
+            q_out = torch.empty((B, Hq, N, d), dtype=bf16, device=dev)
+        if k is not None and k_out is None:
+            k_out = torch.empty((B, Hk, N, d), dtype=bf16, device=dev)
+    m = _AXES_MAP.pack(axes, *sections, *(0,) * (4 - axes), bool(interleaved), bool(own_spectrum), rope_theta,
+                       positions.data_ptr(), *st)
+    _launch(load().attnfuse_rope_axes,
+            (q.data_ptr(), qs, q_out.data_ptr(), qos, Hq, None if k is None else k.data_ptr(), ks,
+             None if k is None else k_out.data_ptr(), kos, Hk, B, N, d, m, bool(inverse)), dev, stream)
+    return q_out, k_out
 
 
 def device_status(clear=True, stream=None, device=None):

@@ -15,7 +15,9 @@ Rules of composition (what one library call can express):
   - masks: at most one of full / causal / sliding_window / block_sparse, except that causal
     may restrict sliding_window or block_sparse;
   - biases: at most one of alibi / additive_bias;
-  - rope: optional (mode "auto" picks fused or pre-rotated by the measured crossover N*);
+  - rope: optional (mode "auto" picks fused or pre-rotated by the measured crossover N*), or
+    rope_axes (positions given per token, on several axes: q and k are rotated by a pass of
+    their own, dq and dk turned back by another);
   - normaliser: softmax (the default). relu_attention is named by the paper but given no
     semantics, so composing it raises NotImplementedError.
 This module only marshals arguments; every step of the computation runs in the library.
@@ -52,6 +54,13 @@ def rope(theta=10000.0, mode="auto"):
     if mode not in _ROPE_MODES:
         raise ValueError(f"rope mode {mode!r}: one of {sorted(_ROPE_MODES)}")
     return Combinator("rope", theta=float(theta), mode=mode)
+
+
+def rope_axes(positions, sections, theta=10000.0, interleaved=False, own_spectrum=False):
+    """Rotary position embedding of q and k by given positions on one to four axes (af.rope_axes):
+    positions int32 [axes, B, N] or [axes, N] device tensor, sections: pairs of each axis."""
+    return Combinator("rope_axes", positions=positions, sections=tuple(sections), theta=float(theta),
+                      interleaved=bool(interleaved), own_spectrum=bool(own_spectrum))
 
 
 def causal():
@@ -122,6 +131,8 @@ class Attention:
             raise ValueError("full and causal contradict each other")
         if "alibi" in by and "additive_bias" in by:
             raise ValueError("one bias combinator per variant (alibi or additive_bias)")
+        if "rope" in by and "rope_axes" in by:
+            raise ValueError("one rotation per variant (rope or rope_axes)")
         self.combinators = combinators
         self.by = by
         self.scale = by["scaled_dot_product"].params["scale"] if "scaled_dot_product" in by else None
@@ -129,6 +140,14 @@ class Attention:
         self.rope_theta = r.params["theta"] if r else 10000.0
         self.rope_mode = _ROPE_MODES[r.params["mode"]] if r else af.ROPE_NONE
         self.bias = by["additive_bias"].params["bias"] if "additive_bias" in by else None
+        self.axes = by["rope_axes"].params if "rope_axes" in by else None
+
+    def rotate(self, q, k, positions, inverse=False):
+        """q and k by the rope_axes stage's positions, or gradients turned back (in place)."""
+        a = self.axes
+        out = {"q_out": q, "k_out": k} if inverse else {}
+        return af.rope_axes(q, k, positions, a["sections"], rope_theta=a["theta"], interleaved=a["interleaved"],
+                            own_spectrum=a["own_spectrum"], inverse=inverse, **out)
 
     def variant(self, Hq, device):
         """The af.Variant (attnfuse_variant) of this composition for Hq query heads."""
@@ -179,6 +198,10 @@ def _autograd_function():
         def forward(ctx, q, k, v, bias, spec):
             scale = spec.scale if spec.scale is not None else 1.0 / math.sqrt(q.shape[-1])
             var = spec.variant(q.shape[1], q.device)
+            positions = None
+            if spec.axes:
+                positions = spec.axes["positions"]
+                q, k = spec.rotate(q, k, positions)
             out, lse = af.fwd(q, k, v, scale=scale, rope_theta=spec.rope_theta,
                               rope_mode=spec.rope_mode, variant=var)
             if lse is None:  # relu_attention: forward only
@@ -186,13 +209,13 @@ def _autograd_function():
                 ctx.relu = True
             else:
                 ctx.relu = False
-            ctx.save_for_backward(q, k, v, out, lse)
+            ctx.save_for_backward(q, k, v, out, lse, positions)
             ctx.spec, ctx.scale, ctx.bias = spec, scale, bias
             return out
 
         @staticmethod
         def backward(ctx, dout):
-            q, k, v, out, lse = ctx.saved_tensors
+            q, k, v, out, lse, positions = ctx.saved_tensors
             if ctx.relu:
                 raise NotImplementedError("relu_attention has no backward in this library")
             spec, bias = ctx.spec, ctx.bias
@@ -207,6 +230,8 @@ def _autograd_function():
                 var.dbias = dbias
             dq, dk, dv = af.bwd(q, k, v, out, lse, dout.contiguous(), scale=ctx.scale,
                                 rope_theta=spec.rope_theta, rope_mode=spec.rope_mode, variant=var)
+            if spec.axes:
+                dq, dk = spec.rotate(dq, dk, positions, inverse=True)
             if dbias is not None and dbias.dtype != bias.dtype:
                 dbias = dbias.to(bias.dtype)
             return dq, dk, dv, dbias, None

@@ -43,6 +43,7 @@ struct PagedDev {
 };
 
 // theta^(-2i/d) / (2 pi) for i < d/2 as the sum of three floats (about 72 bits), less whole numbers: x + y + z.
+// (w: with positions on several axes, the pair's axis, an integer's bits.)
 struct PagedFreqs {
   float4 f[64];
 };
@@ -100,6 +101,22 @@ struct PagedDecodeParams : PagedCombineParams {
   PagedFreqs freqs;
   int* status;
 };
+// Rotation by given positions (rope_axes.cu): q and k [B, H, N, d] bf16, byte strides (b, h, n).
+struct RopeAxesParams {
+  const uint8_t *x[2];              // q, k
+  uint8_t *y[2];
+  int64_t x_sb[2], x_sh[2], x_sn[2], y_sb[2], y_sh[2], y_sn[2];
+  int Hq, H;                        // heads of q, of both
+  int N;
+  int64_t rows;                     // B * N, below 2^31
+  uint64_t div_n;                   // as PagedAppendParams
+  const int32_t* pos;               // [axes, B, N], element strides
+  int64_t pos_sa, pos_sb, pos_sn;
+  int inverse;
+  int rb_log2, passes;              // (log2) rows of a block, heads in turn per thread: set by the launcher
+  PagedFreqs freqs;
+};
+cudaError_t launch_rope_axes(RopeAxesParams p, int d, cudaStream_t stream);
 constexpr int kPagedMaxCtas = 1024;
 int paged_sm_count();  // SMs of the current device
 cudaError_t launch_paged_append(PagedAppendParams p, int d, int format, bool rope, cudaStream_t stream);
@@ -149,15 +166,11 @@ __device__ __forceinline__ float4 freq_at(const PagedFreqs& f, int i) {
   return v;
 }
 
-// (cos, sin) of 2 pi pos (f.x + f.y + f.z), each as hi + lo, hi a multiple of 2^-16 (so that its
-// product with a bf16 is exact in fp32). The angle in turns is reduced exactly,
-// its nearest multiple of 1/256 looked up (table-driven reduction as in Tang, "Table-driven
-// implementation of the exponential function", 1989) and the rest, |d| <= 2 pi / 512, added by
-// the angle-sum formulas with Taylor series to d^5. d is dh + dl, |dl| < 2^-23; of its powers in dl,
-// dl (sine) and dh dl (cosine, up to 2^-29) count. Against 113-bit arithmetic the largest error in
-// 10^6 angles was 2^-35.3.
-__device__ __forceinline__ float4 turn_cossin(float pos, const float4& f) {
-  const float f1 = f.x, f2 = f.y, f3 = f.z;
+// pos (f.x + f.y + f.z) less whole numbers, as r + lo: |pos| <= 2^24 a whole number.
+struct Turns {
+  float r, lo;
+};
+__device__ __forceinline__ Turns turns_of(float pos, float f1, float f2, float f3) {
   const float p1 = __fmul_rn(pos, f1), e1 = __fmaf_rn(pos, f1, -p1);
   const float frac = __fsub_rn(p1, rintf(p1));
   const float p2 = __fmul_rn(pos, f2), e2 = __fmaf_rn(pos, f2, -p2);
@@ -165,7 +178,18 @@ __device__ __forceinline__ float4 turn_cossin(float pos, const float4& f) {
   const float ea = __fadd_rn(__fsub_rn(e1, __fsub_rn(a, ab)), __fsub_rn(p2, ab));
   const float r = __fadd_rn(frac, a), rb = __fsub_rn(r, frac);
   const float er = __fadd_rn(__fsub_rn(frac, __fsub_rn(r, rb)), __fsub_rn(a, rb));
-  const float lo = __fadd_rn(__fadd_rn(er, ea), __fmaf_rn(pos, f3, e2));
+  return {r, __fadd_rn(__fadd_rn(er, ea), __fmaf_rn(pos, f3, e2))};
+}
+
+// (cos, sin) of 2 pi (t.r + t.lo), each as hi + lo, hi a multiple of 2^-16 (so that its
+// product with a bf16 is exact in fp32). The angle's
+// nearest multiple of 1/256 of a turn is looked up (table-driven reduction as in Tang, "Table-driven
+// implementation of the exponential function", 1989) and the rest, |d| <= 2 pi / 512, added by
+// the angle-sum formulas with Taylor series to d^5. d is dh + dl, |dl| < 2^-23; of its powers in dl,
+// dl (sine) and dh dl (cosine, up to 2^-29) count. Against 113-bit arithmetic the largest error in
+// 10^6 angles of positions below 2^24 was 2^-35.3.
+__device__ __forceinline__ float4 cossin_of(const Turns& t) {
+  const float r = t.r, lo = t.lo;
   const float kf = rintf(__fmul_rn(r, 256.0f));
   const float rs = __fmaf_rn(kf, -1.0f / 256.0f, r);  // exact
   const int k = static_cast<int>(kf);
@@ -195,6 +219,25 @@ __device__ __forceinline__ float4 turn_cossin(float pos, const float4& f) {
   const int q = (k >> 6) & 3;
   const float4 w = (q & 1) ? make_float4(-sh, -sl, ch, cl) : make_float4(ch, cl, sh, sl);
   return (q & 2) ? make_float4(-w.x, -w.y, -w.z, -w.w) : w;
+}
+
+__device__ __forceinline__ float4 turn_cossin(float pos, const float4& f) {
+  return cossin_of(turns_of(pos, f.x, f.y, f.z));
+}
+
+// The same for any 32-bit position: from 2^24 on as 2^12 (pos >> 12) + the rest, whose turns are
+// added (2^12 times a frequency's parts are exact, less whole numbers in the first).
+__device__ __forceinline__ float4 turn_cossin_far(int pos, const float4& f) {
+  if (pos <= kPagedMaxPos && pos >= -kPagedMaxPos) return turn_cossin(static_cast<float>(pos), f);
+  const float x = __fmul_rn(4096.0f, f.x);
+  const Turns a = turns_of(static_cast<float>(pos >> 12), __fsub_rn(x, rintf(x)), __fmul_rn(4096.0f, f.y), __fmul_rn(4096.0f, f.z));
+  const Turns b = turns_of(static_cast<float>(pos & 4095), f.x, f.y, f.z);
+  const float ra = __fsub_rn(a.r, rintf(a.r)), rb = __fsub_rn(b.r, rintf(b.r));  // exact
+  const float s = __fadd_rn(ra, rb), bb = __fsub_rn(s, ra);
+  const float es = __fadd_rn(__fsub_rn(ra, __fsub_rn(s, bb)), __fsub_rn(rb, bb));
+  const float sr = __fsub_rn(s, rintf(s)), lo = __fadd_rn(es, __fadd_rn(a.lo, b.lo));
+  const float r = __fadd_rn(sr, lo);
+  return cossin_of({r, __fsub_rn(lo, __fsub_rn(r, sr))});
 }
 
 // x c + y s of two lanes, c and s as hi + lo: h + t, h the rounded sum of the (exact) products

@@ -1,5 +1,5 @@
-// C entry points of the paged cache: argument checks and launches. Declarations and the meaning
-// of every argument are in include/attnfuse.h.
+// C entry points of the paged cache and of the rotation by given positions: argument checks and
+// launches. Declarations and the meaning of every argument are in include/attnfuse.h.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -140,6 +140,20 @@ Double2 root(Double2 a) {
   return sum_of(s, (std::fma(-s, s, a.hi) + a.lo) / (2.0 * s));
 }
 
+constexpr Double2 kTurn = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};  // 1 / (2 pi)
+
+// A frequency in turns, less whole numbers, as three floats.
+float4 parts_of(Double2 turn) {
+  const Double2 part = sum_of(turn.hi - std::rint(turn.hi), turn.lo);
+  float4 f;
+  f.x = (float)part.hi;
+  const double rest = (part.hi - f.x) + part.lo;
+  f.y = (float)rest;
+  f.z = (float)(rest - f.y);
+  f.w = 0.f;
+  return f;
+}
+
 // The frequencies of a theta; a thread keeps those of its last call (they cost as much as a launch).
 // The kernels multiply them by positions up to 2^24, so a double's 53 bits would leave an angle
 // 2^-29 off. Whole turns per position (theta < 0.16) drop out, positions being whole numbers.
@@ -151,17 +165,59 @@ const PagedFreqs& paged_freqs(int d, float theta) {
     memset(&f, 0, sizeof(f));
     Double2 step = inverse(theta);  // theta^(-2 / d)
     for (int n = d / 2; n > 1; n /= 2) step = root(step);
-    Double2 turn = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};  // 1 / (2 pi)
-    for (int i = 0; i < d / 2; ++i, turn = times(turn, step)) {
-      const Double2 part = sum_of(turn.hi - std::rint(turn.hi), turn.lo);
-      f.f[i].x = (float)part.hi;
-      const double rest = (part.hi - f.f[i].x) + part.lo;
-      f.f[i].y = (float)rest;
-      f.f[i].z = (float)(rest - f.f[i].y);
-    }
+    Double2 turn = kTurn;
+    for (int i = 0; i < d / 2; ++i, turn = times(turn, step)) f.f[i] = parts_of(turn);
     have_d = d;
     have_theta = theta;
   }
+  return f;
+}
+
+// theta^(-1 / n): std::pow's value after one step of Newton's method for y^n = theta in pairs of doubles.
+Double2 root_inverse(double theta, int n) {
+  const double y = std::pow(theta, 1.0 / n);
+  Double2 power = {1.0, 0.0};
+  for (int i = 0; i < n; ++i) power = times(power, {y, 0.0});
+  // y^n / theta - 1 = e, small: theta^(1/n) = y (1 - e / n)
+  const double e = ((power.hi - theta) + power.lo) / theta;
+  const Double2 root = sum_of(y, -y * e / n);
+  const Double2 q = inverse(root.hi);
+  return sum_of(q.hi, q.lo - q.hi * q.hi * root.lo);
+}
+
+// Frequencies and axes of the pairs of a map; a thread keeps those of its last call.
+const PagedFreqs& axes_freqs(int d, const attnfuse_rope_axes_map& m) {
+  static thread_local PagedFreqs f;
+  static thread_local attnfuse_rope_axes_map have;
+  static thread_local int have_d = 0;
+  if (have_d == d && have.axes == m.axes && !memcmp(have.sections, m.sections, sizeof(m.sections)) &&
+      !have.interleaved == !m.interleaved && !have.own_spectrum == !m.own_spectrum && have.rope_theta == m.rope_theta)
+    return f;
+  int axis[64], number[64];  // of each pair: its axis, its number within the axis
+  int seen[4] = {0, 0, 0, 0};
+  for (int i = 0, a = 0; i < d / 2; ++i) {
+    while (seen[a] == m.sections[a]) a = (a + 1) % m.axes;
+    axis[i] = a;
+    number[i] = seen[a]++;
+    if (m.interleaved) a = (a + 1) % m.axes;
+  }
+  PagedFreqs g;
+  if (!m.own_spectrum) {
+    g = paged_freqs(d, m.rope_theta);
+  } else {
+    memset(&g, 0, sizeof(g));
+    for (int a = 0; a < m.axes; ++a) {
+      const Double2 step = root_inverse(m.rope_theta, m.sections[a]);
+      Double2 turn = kTurn;
+      for (int j = 0; j < m.sections[a]; ++j, turn = times(turn, step))
+        for (int i = 0; i < d / 2; ++i)
+          if (axis[i] == a && number[i] == j) g.f[i] = parts_of(turn);
+    }
+  }
+  for (int i = 0; i < d / 2; ++i) memcpy(&g.f[i].w, &axis[i], sizeof(float));
+  f = g;
+  have = m;
+  have_d = d;
   return f;
 }
 
@@ -237,6 +293,60 @@ attnfuse_status attnfuse_paged_gather(const attnfuse_paged_cache* cache, const i
   p.rows = (int64_t)cache->B * N;
   p.div_n = N > 1 ? ~0ull / N + 1 : 0;  // ceil(2^64 / N)
   return done(launch_paged_gather(p, cache->d, cache->format, stream), "paged gather launch");
+}
+
+attnfuse_status attnfuse_rope_axes(const void* q, const int64_t q_strides[4], void* q_out,
+                                   const int64_t q_out_strides[4], int Hq, const void* k,
+                                   const int64_t k_strides[4], void* k_out,
+                                   const int64_t k_out_strides[4], int Hk, int B, int N, int d,
+                                   const attnfuse_rope_axes_map* map, int inverse,
+                                   cudaStream_t stream) {
+  RopeAxesParams p;
+  memset(&p, 0, sizeof(p));
+  int rc;
+  if (!map) return fail(ATTNFUSE_ERR_INVALID_ARG, "map is NULL");
+  if (B <= 0 || Hq <= 0 || Hk < 0) return fail(ATTNFUSE_ERR_INVALID_ARG, "bad sizes (B=%d Hq=%d Hk=%d)", B, Hq, Hk);
+  if (Hq > 4096 || Hk > 4096) return fail(ATTNFUSE_ERR_UNSUPPORTED, "Hq=%d Hk=%d (at most 4096)", Hq, Hk);
+  if (d != 64 && d != 128) return fail(ATTNFUSE_ERR_UNSUPPORTED, "head dim %d (need 64 or 128)", d);
+  if ((rc = check_n(B, N))) return rc;
+  if (map->axes < 1 || map->axes > 4) return fail(ATTNFUSE_ERR_INVALID_ARG, "%d axes (need 1 to 4)", map->axes);
+  attnfuse_rope_axes_map m = *map;
+  int64_t pairs = 0;
+  for (int a = 0; a < 4; ++a) {
+    if (a >= m.axes) m.sections[a] = 0;
+    else if (m.sections[a] < 1) return fail(ATTNFUSE_ERR_INVALID_ARG, "axis %d has %d pairs", a, m.sections[a]);
+    pairs += m.sections[a];
+  }
+  if (pairs != d / 2)
+    return fail(ATTNFUSE_ERR_INVALID_ARG, "the axes have %lld pairs, the head dim %d", (long long)pairs, d / 2);
+  if (!(m.rope_theta > 0.f) || !std::isfinite(m.rope_theta))
+    return fail(ATTNFUSE_ERR_INVALID_ARG, "rope_theta must be positive");
+  if ((rc = check_index(m.positions, true, "positions"))) return rc;
+  for (int i = 0; i < 3; ++i)
+    if (m.position_strides[i] < 0) return fail(ATTNFUSE_ERR_INVALID_ARG, "negative positions stride");
+  if ((rc = check_strides(q, q_strides, 4, 8, "q")) || (rc = check_strides(q_out, q_out_strides, 4, 8, "q_out")))
+    return rc;
+  if (Hk && ((rc = check_strides(k, k_strides, 4, 8, "k")) || (rc = check_strides(k_out, k_out_strides, 4, 8, "k_out"))))
+    return rc;
+  const void* x[2] = {q, k};
+  void* y[2] = {q_out, k_out};
+  const int64_t *xs[2] = {q_strides, k_strides}, *ys[2] = {q_out_strides, k_out_strides};
+  for (int i = 0; i < (Hk ? 2 : 1); ++i) {
+    p.x[i] = static_cast<const uint8_t*>(x[i]);
+    p.y[i] = static_cast<uint8_t*>(y[i]);
+    p.x_sb[i] = xs[i][0] * 2, p.x_sh[i] = xs[i][1] * 2, p.x_sn[i] = xs[i][2] * 2;
+    p.y_sb[i] = ys[i][0] * 2, p.y_sh[i] = ys[i][1] * 2, p.y_sn[i] = ys[i][2] * 2;
+  }
+  p.Hq = Hq;
+  p.H = Hq + Hk;
+  p.N = N;
+  p.rows = (int64_t)B * N;
+  p.div_n = N > 1 ? ~0ull / N + 1 : 0;
+  p.pos = m.positions;
+  p.pos_sa = m.position_strides[0], p.pos_sb = m.position_strides[1], p.pos_sn = m.position_strides[2];
+  p.inverse = inverse != 0;
+  p.freqs = axes_freqs(d, m);
+  return done(launch_rope_axes(p, d, stream), "rope axes launch");
 }
 
 attnfuse_status attnfuse_paged_decode_workspace_size(int Hq, int Hkv, int d, int format, size_t* bytes) {

@@ -416,6 +416,41 @@ attnfuse_status attnfuse_rope_prerotate(const void* x, const int64_t x_strides[4
                                         void* workspace, size_t workspace_bytes,
                                         cudaStream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Rotary positions that the caller gives, on one to four axes (images: row and column; video:
+ * time, row and column). (The paper rotates row n at position n only.) Pair i of d/2, (x_i,
+ * x_{i + d/2}), belongs to axis a(i) and is turned by positions[a(i)][b][n] * f_i; inverse != 0
+ * turns back, which is the gradient of the rotation. sections[a] >= 1 pairs belong to axis a, d/2
+ * in all. interleaved = 0: the first sections[0] pairs to axis 0, the next to axis 1, and so on; otherwise
+ * pairs are dealt to the axes in turn, an axis that has all of its pairs being passed over.
+ * own_spectrum = 0: f_i = rope_theta^(-2i/d) as everywhere; otherwise the j-th pair of axis a has
+ * f = rope_theta^(-j / sections[a]). positions: device int32 of any value, element strides (axis, b,
+ * n) >= 0 (0 broadcasts).
+ * q [B, Hq, N, d] and k [B, Hk, N, d] (Hk = 0: none; k, k_out and their strides are ignored)
+ * are rotated by one launch into q_out and k_out, bf16, strides as in attnfuse_fwd. Outputs may be
+ * the inputs themselves (same address, same strides), but may not overlap them otherwise. A value
+ * is (R x), off by at most 2^-34 (|x_i| + |x_{i + d/2}|) for positions up to 2^24 (2^-30 beyond), rounded
+ * to fp32 and then to bf16. With one axis and positions start + n these are the keys that
+ * attnfuse_paged_append stores. Rows to attend over with ATTNFUSE_ROPE_NONE: attnfuse_fwd, attnfuse_bwd
+ * (then turn dq and dk back), attnfuse_paged_append and what reads the cache.
+ * ------------------------------------------------------------------------------------------ */
+typedef struct {
+  int32_t axes;                /* 1 to 4 */
+  int32_t sections[4];         /* pairs of each axis */
+  int32_t interleaved;
+  int32_t own_spectrum;
+  float rope_theta;
+  const int32_t* positions;    /* [axes, B, N] */
+  int64_t position_strides[3]; /* (axis, b, n) in elements */
+} attnfuse_rope_axes_map;
+
+attnfuse_status attnfuse_rope_axes(const void* q, const int64_t q_strides[4], void* q_out,
+                                   const int64_t q_out_strides[4], int Hq, const void* k,
+                                   const int64_t k_strides[4], void* k_out,
+                                   const int64_t k_out_strides[4], int Hk, int B, int N, int d,
+                                   const attnfuse_rope_axes_map* map, int inverse,
+                                   cudaStream_t stream);
+
 /* The mode ATTNFUSE_ROPE_AUTO resolves to for sequence length N and head dim d, for the
  * forward (backward = 0) or the backward (backward = 1). Measured on GB300 with B*N = 16384
  * tokens, causal: fusion wins for head dim 64 below N ~ 1.85k (forward) and N ~ 260
