@@ -7,7 +7,7 @@ if ``libattnfuse.so`` is missing or fails to load.
 
 Low-level functions carry the C names (``attnfuse_fwd`` ...) and take raw pointers; the
 torch-level helpers ``fwd``, ``bwd``, ``decode``, ``rope_prerotate``, ``rope_axes`` and, on a ``PagedCache``,
-``paged_append``, ``paged_gather`` and ``paged_decode`` allocate outputs and workspace with torch
+``paged_append``, ``paged_gather``, ``paged_decode`` and ``paged_attend`` allocate outputs and workspace with torch
 and call them on the current CUDA stream.
 """
 from __future__ import annotations
@@ -26,6 +26,7 @@ __all__ = [
     "fwd_workspace_size", "bwd_workspace_size", "decode_workspace_size",
     "CACHE_BF16", "CACHE_Q4", "PagedCache", "paged_append", "paged_gather", "paged_decode",
     "paged_decode_workspace_size", "rope_axes",
+    "paged_attend", "paged_attend_workspace_size",
 ]
 
 ROPE_NONE, ROPE_FUSED, ROPE_PREROTATE, ROPE_AUTO = 0, 1, 2, 3
@@ -144,6 +145,8 @@ def load():
             "attnfuse_paged_gather": ([P, P, P, P, P, P, P, I, P], I),
             "attnfuse_paged_decode_workspace_size": ([I, I, I, I, ctypes.POINTER(S)], I),
             "attnfuse_paged_decode": ([P, P, P, P, P, P, P, I, F, F, I, I, P, P, S, P], I),
+            "attnfuse_paged_attend_workspace_size": ([I, I, I, I, I, I, I, ctypes.POINTER(S)], I),
+            "attnfuse_paged_attend": ([P, P, P, P, P, P, P, P, I, I, F, F, I, I, P, P, S, P], I),
             "attnfuse_rope_axes": ([P, P, P, P, I, P, P, P, P, I, I, I, I, P, I, P], I),
             "attnfuse_rope_prerotate": ([P, ST, P, I, I, I, I, F, P, S, P], I),
             "attnfuse_debug_wait_timeout": ([ctypes.c_uint64, P], I),
@@ -866,6 +869,60 @@ def paged_decode(q, cache, lens, scale=None, rope_theta=10000.0, rope_mode=ROPE_
             (cache._c, q.data_ptr(), _S3(*_live_strides(q)), _index(lens, "lens", cache), out.data_ptr(), os_,
              None if lse is None else lse.data_ptr(), Hq, d ** -0.5 if scale is None else scale, rope_theta, rope_mode,
              max(-1, min(window, 0x7FFFFFFF)), alibi_slopes, workspace.data_ptr(), ws_n), dev, stream)
+    return out, lse
+
+
+def paged_attend_workspace_size(B, Hq, Hkv, N, d, cache_format, rope_mode=ROPE_FUSED):
+    """Bytes of workspace for paged_attend on the current device."""
+    n = ctypes.c_size_t()
+    _check(load().attnfuse_paged_attend_workspace_size(B, Hq, Hkv, N, d, cache_format, rope_mode, ctypes.byref(n)))
+    return n.value
+
+
+def paged_attend(q, cache, start, count=None, scale=None, rope_theta=10000.0, rope_mode=ROPE_FUSED, window=0,
+                 alibi_slopes=None, out=None, lse=None, with_lse=True, workspace=None, stream=None):
+    """Attention of a chunk of new tokens over a paged cache that holds them already: q [B, Hq, N, d]
+    bf16, row n < count[b] at position start[b] + n (start, count: int32 [B] device tensors; count
+    None: all N), against positions up to its own (window > 0: the last `window` of them) -> (out
+    [B, Hq, N, d], lse [B, Hq, N]). Rows at and behind count[b]: out 0, lse -inf. alibi_slopes: fp32 [Hq], adds
+    slope_h (m - p) to the scores. With a stream, what the call allocates belongs to that stream."""
+    import torch
+
+    if not isinstance(cache, PagedCache):
+        _need_cache(cache)
+    bf16, f32, dev, B, d = torch.bfloat16, torch.float32, cache.device, cache.B, cache.d
+    if getattr(q, "dtype", None) is not bf16 or q.dim() != 4:
+        _need(q, "q", (bf16,), ndim=4, dims="[B, Hq, N, d]")
+    Hq, N = q.shape[1], q.shape[2]
+    shape = (B, Hq, N, d)
+    _want(q, "q", bf16, shape, dev)
+    if start is None:
+        raise TypeError("start: expected an int32 [B] tensor")
+    if alibi_slopes is not None:
+        _want(alibi_slopes, "alibi_slopes", f32, (Hq,), dev, contiguous=True)
+        alibi_slopes = alibi_slopes.data_ptr()
+    os_ = _S4(Hq * N * d, N * d, d, 1)
+    if out is not None:
+        _want(out, "out", bf16, shape, dev)
+        os_ = _S4(*_live_strides(out))
+    if lse is not None:
+        _want(lse, "lse", f32, (B, Hq, N), dev, contiguous=True)
+    with torch.cuda.device(dev) if dev.index != torch._C._cuda_getDevice() else _CURRENT:
+        ws_n = paged_attend_workspace_size(B, Hq, cache.Hkv, N, d, cache.format, rope_mode)
+    with _on(stream, dev):
+        if out is None:
+            out = torch.empty(shape, dtype=bf16, device=dev)
+        if lse is None and with_lse:
+            lse = torch.empty((B, Hq, N), dtype=f32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(ws_n, dtype=torch.uint8, device=dev)
+        else:
+            workspace = _workspace(ws_n, dev, workspace)
+    _launch(load().attnfuse_paged_attend,
+            (cache._c, q.data_ptr(), _S4(*_live_strides(q)), _index(start, "start", cache), _index(count, "count", cache),
+             out.data_ptr(), os_, None if lse is None else lse.data_ptr(), Hq, N, d ** -0.5 if scale is None else scale,
+             rope_theta, rope_mode, max(-1, min(window, 0x7FFFFFFF)), alibi_slopes,
+             None if workspace is None else workspace.data_ptr(), ws_n), dev, stream)
     return out, lse
 
 

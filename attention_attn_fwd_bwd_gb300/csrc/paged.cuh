@@ -101,6 +101,25 @@ struct PagedDecodeParams : PagedCombineParams {
   PagedFreqs freqs;
   int* status;
 };
+struct PagedAttendParams {
+  PagedDev cache;
+  const __nv_bfloat16* q;           // [B, Hq, N, d], element strides
+  int64_t q_sb, q_sh, q_sn;
+  __nv_bfloat16* out;
+  int64_t o_sb, o_sh, o_sn;
+  float* lse;                       // [B, Hq, N] or null
+  const int32_t *first, *count;     // [B]; count may be null: every sequence has N rows
+  const float* slopes;              // [Hq] or null
+  int Hq, g, N;
+  int window;                       // 0: none
+  int rope;
+  float scale;
+  void* workspace;
+  PagedFreqs freqs;
+  int* status;
+};
+size_t paged_attend_workspace(int B, int Hq, int Hkv, int N, int d, int format, bool rope);
+cudaError_t launch_paged_attend(PagedAttendParams p, int d, int format, cudaStream_t stream);
 // Rotation by given positions (rope_axes.cu): q and k [B, H, N, d] bf16, byte strides (b, h, n).
 struct RopeAxesParams {
   const uint8_t *x[2];              // q, k

@@ -414,4 +414,66 @@ attnfuse_status attnfuse_paged_decode(const attnfuse_paged_cache* cache, const v
   return done(launch_paged_decode(p, cache->d, cache->format, stream), "paged decode launch");
 }
 
+attnfuse_status attnfuse_paged_attend_workspace_size(int B, int Hq, int Hkv, int N, int d, int format,
+                                                     attnfuse_rope_mode rope_mode, size_t* bytes) {
+  int rc, mode = rope_mode;
+  if (!bytes) return fail(ATTNFUSE_ERR_INVALID_ARG, "bytes is NULL");
+  if (B <= 0 || Hq <= 0 || Hkv <= 0)
+    return fail(ATTNFUSE_ERR_INVALID_ARG, "sizes must be positive (B=%d Hq=%d Hkv=%d)", B, Hq, Hkv);
+  if ((rc = check_n(B, N))) return rc;
+  if (Hq % Hkv) return fail(ATTNFUSE_ERR_UNSUPPORTED, "Hq=%d not a multiple of Hkv=%d", Hq, Hkv);
+  if (Hq > 4096 || (int64_t)B * Hq > 0x7fffffff)
+    return fail(ATTNFUSE_ERR_UNSUPPORTED, "Hq at most 4096, B * Hq below 2^31");
+  if (d != 64 && d != 128) return fail(ATTNFUSE_ERR_UNSUPPORTED, "head dim %d (need 64 or 128)", d);
+  if (format != ATTNFUSE_CACHE_BF16 && format != ATTNFUSE_CACHE_Q4)
+    return fail(ATTNFUSE_ERR_INVALID_ARG, "cache format %d", format);
+  if ((rc = check_rope(&mode, 1.0f))) return rc;
+  *bytes = paged_attend_workspace(B, Hq, Hkv, N, d, format, mode == ATTNFUSE_ROPE_FUSED);
+  return set_last_error(ATTNFUSE_OK, "");
+}
+
+attnfuse_status attnfuse_paged_attend(const attnfuse_paged_cache* cache, const void* q,
+                                      const int64_t q_strides[4], const int32_t* start,
+                                      const int32_t* count, void* out, const int64_t o_strides[4],
+                                      float* lse, int Hq, int N, float scale, float rope_theta,
+                                      attnfuse_rope_mode rope_mode, int window,
+                                      const float* alibi_slopes, void* workspace,
+                                      size_t workspace_bytes, cudaStream_t stream) {
+  PagedAttendParams p;
+  memset(&p, 0, sizeof(p));
+  int rc, mode = rope_mode;
+  if ((rc = check_cache(cache, &p.cache))) return rc;
+  size_t need = 0;
+  if ((rc = attnfuse_paged_attend_workspace_size(cache->B, Hq, cache->Hkv, N, cache->d, cache->format, rope_mode, &need)))
+    return rc;
+  if ((rc = check_strides(q, q_strides, 4, 8, "q")) || (rc = check_strides(out, o_strides, 4, 8, "out"))) return rc;
+  if ((rc = check_index(start, true, "start")) || (rc = check_index(count, false, "count"))) return rc;
+  if (!aligned(lse, 4)) return fail(ATTNFUSE_ERR_INVALID_ARG, "lse is not 4-byte aligned");
+  if (!aligned(alibi_slopes, 4)) return fail(ATTNFUSE_ERR_INVALID_ARG, "alibi_slopes is not 4-byte aligned");
+  if (!(scale > 0.f) || !std::isfinite(scale))
+    return fail(ATTNFUSE_ERR_INVALID_ARG, "scale must be positive and finite");
+  if (window < 0) return fail(ATTNFUSE_ERR_INVALID_ARG, "window %d < 0", window);
+  if ((rc = check_rope(&mode, rope_theta))) return rc;
+  if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+    return fail(ATTNFUSE_ERR_WORKSPACE_TOO_SMALL, "workspace needs %zu bytes (got %zu)", need, workspace_bytes);
+  if ((rc = current_status_word(&p.status))) return rc;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_sb = q_strides[0], p.q_sh = q_strides[1], p.q_sn = q_strides[2];
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.o_sb = o_strides[0], p.o_sh = o_strides[1], p.o_sn = o_strides[2];
+  p.lse = lse;
+  p.first = start;
+  p.count = count;
+  p.slopes = alibi_slopes;
+  p.Hq = Hq;
+  p.g = Hq / cache->Hkv;
+  p.N = N;
+  p.window = window;
+  p.rope = mode == ATTNFUSE_ROPE_FUSED;
+  p.scale = scale;
+  if (p.rope) p.freqs = paged_freqs(cache->d, rope_theta);
+  p.workspace = workspace;
+  return done(launch_paged_attend(p, cache->d, cache->format, stream), "paged attend launch");
+}
+
 }  // extern "C"

@@ -405,6 +405,32 @@ attnfuse_status attnfuse_paged_decode(const attnfuse_paged_cache* cache, const v
                                       const float* alibi_slopes, void* workspace,
                                       size_t workspace_bytes, cudaStream_t stream);
 
+/* Attend: the rows of a chunk of new tokens, q [B, Hq, N, d] (strides as in attnfuse_fwd), row n < count[b]
+ * at position p = start[b] + n (append the chunk's K and V first), against positions m <= p, with
+ * window > 0 only m > p - window:
+ *   s_m = scale <R_p q, k_m> [+ alibi_slopes[h] (m - p)],  lse = ln sum exp s_m,  out = sum exp(s_m - lse) v_m
+ * out [B, Hq, N, d] bf16, lse [B, Hq, N] fp32 contiguous or NULL. Rows at and behind count[b] (padding) are not
+ * read; their out is 0 and their lse -inf. count NULL: all N. It continues prompts, verifies drafted
+ * tokens and serves batches that mix prompts with single tokens; one token (N = 1) gives what
+ * attnfuse_paged_decode with lens = start + 1 does, at coarser weights. rope_mode NONE or FUSED (AUTO means
+ * FUSED): q is rotated at its position and keeps 16 significant bits against a BF16 cache, 22 against a Q4 one.
+ * Weights are rounded to bf16, and so are the values of a Q4 cache (its keys are not). A value that
+ * is not finite at a visible position may give NaN in all rows of its sequence and KV head, also in those that do
+ * not see it; positions behind start[b] + count[b] - 1, and before the first that some row sees, are not read.
+ * A bad page in a visible place is skipped (status word, above). Hq: a multiple of Hkv up to 4096.
+ * Results do not vary from run to run. workspace: attnfuse_paged_attend_workspace_size bytes on the current device,
+ * 16-byte aligned. Calls that may overlap need workspaces of their own. */
+attnfuse_status attnfuse_paged_attend_workspace_size(int B, int Hq, int Hkv, int N, int d, int format,
+                                                     attnfuse_rope_mode rope_mode, size_t* bytes);
+
+attnfuse_status attnfuse_paged_attend(const attnfuse_paged_cache* cache, const void* q,
+                                      const int64_t q_strides[4], const int32_t* start,
+                                      const int32_t* count, void* out, const int64_t o_strides[4],
+                                      float* lse, int Hq, int N, float scale, float rope_theta,
+                                      attnfuse_rope_mode rope_mode, int window,
+                                      const float* alibi_slopes, void* workspace,
+                                      size_t workspace_bytes, cudaStream_t stream);
+
 /* ------------------------------------------------------------------------------------------
  * Pre-rotation alone (paper Fig. 1a / §5.3 T_pre): x_rot = R_n x for x of shape [B, H, N, d]
  * (row n at position n), written contiguously to `out`. Used by ATTNFUSE_ROPE_PREROTATE and
