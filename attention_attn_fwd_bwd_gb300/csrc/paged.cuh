@@ -101,25 +101,54 @@ struct PagedDecodeParams : PagedCombineParams {
   PagedFreqs freqs;
   int* status;
 };
-struct PagedAttendParams {
+// Attention of a chunk (paged_attend.cu): what the kernel that joins cut work needs, what the one
+// that makes its query operands does, and the main kernel's own.
+struct PagedAttendWork {
   PagedDev cache;
-  const __nv_bfloat16* q;           // [B, Hq, N, d], element strides
-  int64_t q_sb, q_sh, q_sn;
-  __nv_bfloat16* out;
-  int64_t o_sb, o_sh, o_sn;
-  float* lse;                       // [B, Hq, N] or null
   const int32_t *first, *count;     // [B]; count may be null: every sequence has N rows
-  const float* slopes;              // [Hq] or null
   int Hq, g, N;
   int window;                       // 0: none
-  int rope;
-  float scale;
-  void* workspace;
+  __nv_bfloat16* out;               // [B, Hq, N, d], element strides
+  int64_t o_sb, o_sh, o_sn;
+  float* lse;                       // [B, Hq, N] or null
+  int ctas;
+  float* part_acc;                  // [ctas][2][256][d]: partial rows of a run's ends
+  float2* part_ml;                  // (max in log2 units, sum)
+};
+struct PagedQueryParams {
+  const uint8_t* q;                 // bf16 [B, Hq, N, d], byte strides
+  int64_t q_sb, q_sh, q_sn;
+  const int32_t *first, *count;
+  int cap, Hq, N;
+  int64_t rows;                     // B * N
+  uint64_t div_n;
+  uint16_t *hi, *lo;                // 16-bit parts [B, Hq, N, d]; lo null: one part
+  float* factor;                    // [B, Hq, N], 4-bit caches: what the parts of a row are to be multiplied by
+  int rb_log2;
   PagedFreqs freqs;
+};
+struct PagedAttendParams : PagedAttendWork {
+  const __nv_bfloat16* q;           // bf16 rows as they are, or the first parts; element strides
+  int64_t q_sb, q_sh, q_sn;
+  int64_t q_lo;                     // elements from a first part to its second
+  const float* factor;
+  const float* slopes;              // [Hq] or null
+  float scale_log2;
+  CUtensorMap tmK, tmV;             // bf16: pools [num_pages, Hkv, page_size, d], box (64, frag_rows)
+  CUtensorMap tmV16, tmV1;          // and of 16 rows, of one
+  int frag_rows;                    // rows of a page that one copy takes
   int* status;
 };
+// What the C entry point hands over.
+struct PagedAttendCall {
+  PagedAttendParams p;
+  PagedFreqs freqs;
+  int rope;
+  void* workspace;
+};
+constexpr int kAttendTile = 128;    // keys
 size_t paged_attend_workspace(int B, int Hq, int Hkv, int N, int d, int format, bool rope);
-cudaError_t launch_paged_attend(PagedAttendParams p, int d, int format, cudaStream_t stream);
+cudaError_t launch_paged_attend(const PagedAttendCall& c, int d, int format, cudaStream_t stream);
 // Rotation by given positions (rope_axes.cu): q and k [B, H, N, d] bf16, byte strides (b, h, n).
 struct RopeAxesParams {
   const uint8_t *x[2];              // q, k

@@ -6,6 +6,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <numeric>
 
 #include "../../include/attnfuse.h"
 #include "launch.h"
@@ -424,6 +425,8 @@ attnfuse_status attnfuse_paged_attend_workspace_size(int B, int Hq, int Hkv, int
   if (Hq % Hkv) return fail(ATTNFUSE_ERR_UNSUPPORTED, "Hq=%d not a multiple of Hkv=%d", Hq, Hkv);
   if (Hq > 4096 || (int64_t)B * Hq > 0x7fffffff)
     return fail(ATTNFUSE_ERR_UNSUPPORTED, "Hq at most 4096, B * Hq below 2^31");
+  if ((int64_t)N * (Hq / Hkv) > 1 << 30)
+    return fail(ATTNFUSE_ERR_UNSUPPORTED, "N * Hq / Hkv = %lld (at most 2^30)", (long long)N * (Hq / Hkv));
   if (d != 64 && d != 128) return fail(ATTNFUSE_ERR_UNSUPPORTED, "head dim %d (need 64 or 128)", d);
   if (format != ATTNFUSE_CACHE_BF16 && format != ATTNFUSE_CACHE_Q4)
     return fail(ATTNFUSE_ERR_INVALID_ARG, "cache format %d", format);
@@ -439,8 +442,9 @@ attnfuse_status attnfuse_paged_attend(const attnfuse_paged_cache* cache, const v
                                       attnfuse_rope_mode rope_mode, int window,
                                       const float* alibi_slopes, void* workspace,
                                       size_t workspace_bytes, cudaStream_t stream) {
-  PagedAttendParams p;
-  memset(&p, 0, sizeof(p));
+  PagedAttendCall call;
+  memset(&call, 0, sizeof(call));
+  PagedAttendParams& p = call.p;
   int rc, mode = rope_mode;
   if ((rc = check_cache(cache, &p.cache))) return rc;
   size_t need = 0;
@@ -456,6 +460,8 @@ attnfuse_status attnfuse_paged_attend(const attnfuse_paged_cache* cache, const v
   if ((rc = check_rope(&mode, rope_theta))) return rc;
   if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
     return fail(ATTNFUSE_ERR_WORKSPACE_TOO_SMALL, "workspace needs %zu bytes (got %zu)", need, workspace_bytes);
+  if ((double)cache->B * Hq * (N + 256.0) * (p.cache.cap + 1024.0) > 0x1p60)
+    return fail(ATTNFUSE_ERR_UNSUPPORTED, "B * Hq * N * max_pages * page_size too large");
   if ((rc = current_status_word(&p.status))) return rc;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.q_sb = q_strides[0], p.q_sh = q_strides[1], p.q_sn = q_strides[2];
@@ -469,11 +475,22 @@ attnfuse_status attnfuse_paged_attend(const attnfuse_paged_cache* cache, const v
   p.g = Hq / cache->Hkv;
   p.N = N;
   p.window = window;
-  p.rope = mode == ATTNFUSE_ROPE_FUSED;
-  p.scale = scale;
-  if (p.rope) p.freqs = paged_freqs(cache->d, rope_theta);
-  p.workspace = workspace;
-  return done(launch_paged_attend(p, cache->d, cache->format, stream), "paged attend launch");
+  p.scale_log2 = scale * kLog2e;
+  call.rope = mode == ATTNFUSE_ROPE_FUSED;
+  if (call.rope) call.freqs = paged_freqs(cache->d, rope_theta);
+  call.workspace = workspace;
+  if (cache->format == ATTNFUSE_CACHE_BF16) {
+    p.frag_rows = std::gcd(cache->page_size, kAttendTile);
+    auto map = [&](CUtensorMap* m, const void* pool, const int64_t* st, const char* name, int rows) {
+      return encode_map_bhnd(m, pool, st, cache->num_pages, cache->Hkv, cache->page_size, cache->d, name, rows);
+    };
+    if ((rc = map(&p.tmK, cache->k, cache->k_strides, "cache k", p.frag_rows)) ||
+        (rc = map(&p.tmV, cache->v, cache->v_strides, "cache v", p.frag_rows)) ||
+        (rc = map(&p.tmV16, cache->v, cache->v_strides, "cache v", 16)) ||
+        (rc = map(&p.tmV1, cache->v, cache->v_strides, "cache v", 1)))
+      return rc;
+  }
+  return done(launch_paged_attend(call, cache->d, cache->format, stream), "paged attend launch");
 }
 
 }  // extern "C"

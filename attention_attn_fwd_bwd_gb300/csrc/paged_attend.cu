@@ -1,10 +1,31 @@
-// Attention of a chunk of new tokens over a paged cache.
+// Attention of a chunk of new tokens over a paged cache for sm_103a.
 //
 //   O = sum_m p_m v_m,  p = softmax over m in (P - W, P] of  s_m = scale <R_P q, k_m> + slope_h (m - P)
 //
-// for query row n of sequence b at position P = first[b] + n. A warp takes one row of one head and
-// walks its keys one at a time with a running maximum and sum.
+// for query row n of sequence b at position P = first[b] + n.
+//
+// Work. The query heads of a KV head read the same keys, so a row of the products is a (query,
+// head of the group) pair, row n g + j: groups of any size fill 128-row tiles. A unit is up to 256
+// rows, two tiles, of one (sequence, KV head), and walks the tiles of 128 keys that its rows see.
+// The units of the whole batch, ordered by (sequence, KV head, rows), are dealt to the CTAs, one on each SM, in
+// equal runs of keys, from lengths read on the device. A unit that a run's end cuts leaves (max,
+// sum, acc) of its parts in the workspace, at most two per CTA, and a second kernel joins them in a
+// fixed order; it also writes the rows of padding.
+//
+// CTA. tcgen05 products: S_s = Q_s K^T of row tile s = 0, 1 in tensor memory, a softmax warpgroup
+// for each, one row per thread, which writes its weights as bf16 over S_s, and O_s += P_s V with P_s
+// read from tensor memory. The issuing thread goes PV_0(i), S_0(i + 1), PV_1(i), S_1(i + 1): while one
+// tile's softmax runs, the other's products do. K and V tiles come through one ring of shared
+// memory, TMA boxes of a page's rows (bf16) or codes expanded by a warpgroup (4 bits).
+// TMEM (512 columns): S_0 [0, 128), S_1 [128, 256), O_0 [256, 384), O_1 [384, 512); P_s over S_s.
+//
+// Keys of a 4-bit cache are s_g c (8 and 3 bits): exact in fp16 under a power of two of their own
+// key, which multiplies the score; q enters as fp16 under a power of two of its row. A rotated q is two 16-bit parts.
+#include <cuda.h>
 #include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
 
 #include "launch.h"
 #include "paged.cuh"
@@ -13,109 +34,1144 @@ namespace afx {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kTile = kAttendTile;       // keys of a tile
+constexpr int kRows = 256;               // rows of a unit
+constexpr int kEnds = 256;               // keys that a unit's two ends cost: Q's load, O's way out
+constexpr float kLazy = 8.0f;            // the running maximum may lag by 2^8
 
-// Elements C l .. C l + C - 1 (C = D / 32) of a cache row of one head.
-template <int D, bool Q4>
-__device__ __forceinline__ void row_piece(const uint8_t* pool, const uint8_t* steps, int64_t row, int64_t steps_row, int slot,
-                                          int lane, float (&x)[D / 32]) {
-  constexpr int C = D / 32;
-  if constexpr (!Q4) {
-    const uint16_t* at = reinterpret_cast<const uint16_t*>(pool + row) + C * lane;
+template <int D, bool Q4, bool TWO>
+struct Cfg {
+  static constexpr int WARPS = Q4 ? 16 : 12;
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int PANELS = D / 64;
+  static constexpr uint32_t TILE = kTile * D * 2;                  // bytes of a K, V or Q tile
+  static constexpr uint32_t QSLOT = TILE * (TWO ? 2 : 1);
+  static constexpr int STAGES = D == 64 ? 6 : TWO ? 3 : Q4 ? 4 : 5;
+  // key tiles whose notes (factors, bad pages) may be in use at once: of the ring's tiles, those
+  // behind the one whose V is still held by a softmax that reads them
+  static constexpr int NOTES = STAGES == 3 ? 2 : 4;
+  static constexpr uint32_t OFF_KV = 2 * QSLOT;
+  static constexpr uint32_t OFF_CTL = OFF_KV + STAGES * TILE;
+  // registers of the warpgroups: producer, issuer and query loaders; softmax; expanders
+  static constexpr uint32_t LOW = Q4 ? 56 : 88, SM = Q4 ? 184 : 208, EXP = 88;
+  static_assert(LOW + 2 * SM + (Q4 ? EXP : 0) <= (WARPS / 4) * (65536 / THREADS / 8 * 8), "registers of the launch");
+};
+
+// Boundary between two runs: tile t of unit (b, kvh, r).
+struct Pos {
+  int b, kvh, r, t;
+};
+
+template <int NOTES, bool Q4>
+struct Ctl {
+  uint64_t q_full[2], q_empty[2], kv_full[6], kv_empty[6], s_full[2], p_full[2], o_full[2], last;
+  uint32_t tmem_base;
+  int abort_flag;
+  Pos begin, end;
+  int64_t wsum[16];
+  uint64_t bad[NOTES];                   // a byte for each 16 keys: on a page that is none
+  float factor[Q4 ? NOTES : 1][Q4 ? kTile : 1];
+};
+
+template <int D, bool Q4, bool TWO>
+constexpr size_t smem_bytes() {
+  using C = Cfg<D, Q4, TWO>;
+  return 1024 + C::OFF_CTL + sizeof(Ctl<C::NOTES, Q4>);
+}
+
+// ---------------------------------------------------------------------------------------------
+// Work: starts and counts -> units -> this CTA's run
+// ---------------------------------------------------------------------------------------------
+struct Chunk {
+  int first, count;
+  bool bad;
+};
+__device__ __forceinline__ Chunk chunk_of(const int32_t* firsts, const int32_t* counts, int b, int N, int cap) {
+  Chunk c;
+  c.first = __ldg(firsts + b);
+  c.count = counts ? __ldg(counts + b) : N;
+  c.bad = c.count < 0 || c.count > N;
+  c.count = min(max(c.count, 0), N);
+  if (c.count > 0 && (c.first < 0 || c.first > cap - c.count)) {
+    c.bad = true;
+    c.count = c.first < 0 ? 0 : max(0, cap - c.first);
+  }
+  if (c.count == 0) c.first = 0;
+  return c;
+}
+__device__ __forceinline__ Chunk chunk_of(const PagedAttendWork& p, int b) {
+  return chunk_of(p.first, p.count, b, p.N, p.cache.cap);
+}
+
+__device__ __forceinline__ int units_of(const PagedAttendWork& p, const Chunk& c) {
+  return static_cast<int>((static_cast<int64_t>(c.count) * p.g + kRows - 1) / kRows);
+}
+
+// What units before unit r of a (sequence, KV head) cost, in 1/g of a key: unit i reads the keys up
+// to the position of row 256 (i + 1), of which a window leaves W and what its rows spread over.
+__device__ __forceinline__ int64_t cost_before(const PagedAttendWork& p, const Chunk& c, int64_t r) {
+  const int64_t base = static_cast<int64_t>(c.first) * p.g + kRows;
+  int64_t k = r, cap = 0;
+  if (p.window > 0) {
+    cap = (static_cast<int64_t>(p.window) + 1) * p.g + kRows;
+    k = cap > base ? min(r, (cap - base + kRows - 1) / kRows) : 0;
+  }
+  return base * k + kRows / 2 * k * (k - 1) + (r - k) * cap + r * kEnds * p.g;
+}
+
+// Keys [lo, hi) that a unit's rows see, their first tile and number of tiles.
+struct Span {
+  int lo, hi, t0, nt;
+};
+__device__ __forceinline__ Span span_of(const PagedAttendWork& p, const Chunk& c, int r) {
+  const uint32_t g = p.g, row0 = static_cast<uint32_t>(r) * kRows;
+  const uint32_t rows = static_cast<uint32_t>(c.count) * g;
+  Span s;
+  const int p0 = c.first + static_cast<int>(row0 / g);
+  s.hi = c.first + static_cast<int>((min(row0 + kRows, rows) - 1) / g) + 1;
+  s.lo = p.window > 0 ? max(0, p0 - p.window + 1) : 0;
+  s.t0 = s.lo / kTile;
+  s.nt = (s.hi - 1) / kTile - s.t0 + 1;
+  return s;
+}
+
+template <int NTHREADS>
+__device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t* wsum, int64_t* total) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  int64_t x = v;
 #pragma unroll
-    for (int c = 0; c < C; ++c) x[c] = __uint_as_float(static_cast<uint32_t>(at[c]) << 16);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) wsum[warp] = x;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < NTHREADS / 32; ++w) {
+    if (w < warp) before += wsum[w];
+    all += wsum[w];
+  }
+  *total = all;
+  return before + x - v;
+}
+
+// Run i of `ctas` starts at start(i) of T.
+struct Deal {
+  int64_t each, more;
+  __device__ Deal(int64_t T, int ctas) : each(T / ctas), more(T - T / ctas * ctas) {}
+  __device__ int64_t start(int i) const { return i * each + min(static_cast<int64_t>(i), more); }
+};
+
+// The tile at which offset x >= 0 of a unit's cost falls.
+__device__ __forceinline__ int tile_at(const PagedAttendWork& p, int64_t x, int64_t cost, int nt) {
+  const int64_t ends = static_cast<int64_t>(kEnds) * p.g;
+  if (x <= ends) return 0;
+  return static_cast<int>((x - ends) * nt / (cost - ends));
+}
+
+// Offset x of the work that (sequence b, all KV heads) has -> the unit there, and where it begins.
+struct Found {
+  Pos pos;
+  int64_t unit, cost;  // the unit's first offset and its cost
+  int nt;
+};
+__device__ __forceinline__ Found find_in(const PagedAttendWork& p, int b, const Chunk& c, int64_t x) {
+  const int n = units_of(p, c);
+  const int64_t head = cost_before(p, c, n);
+  Found f;
+  f.pos.b = b;
+  f.pos.kvh = static_cast<int>(x / head);
+  const int64_t y = x - f.pos.kvh * head;
+  int a = 0, z = n - 1;
+  while (a < z) {  // the last unit that begins at y or before
+    const int m = (a + z + 1) / 2;
+    if (cost_before(p, c, m) <= y) a = m;
+    else z = m - 1;
+  }
+  f.pos.r = a;
+  const int64_t u = cost_before(p, c, a);
+  f.unit = f.pos.kvh * head + u;
+  f.cost = cost_before(p, c, a + 1) - u;
+  f.nt = span_of(p, c, a).nt;
+  f.pos.t = tile_at(p, y - u, f.cost, f.nt);
+  return f;
+}
+
+// The part of a unit that a run has.
+struct Seg {
+  int b, kvh, row0, rows;    // first row of the unit, rows of the sequence and KV head
+  int first, lo, hi;         // position of query 0; the unit's keys
+  int t, n;                  // first tile of the segment, its tiles
+  int part;                  // -1: the whole unit, else which of the CTA's two partial results it is
+};
+
+struct Walk {
+  const PagedAttendWork& p;
+  Pos at, end;
+  Chunk c;
+  int units;
+  bool done;
+  __device__ Walk(const PagedAttendWork& p_, Pos begin, Pos end_) : p(p_), at(begin), end(end_), c{}, units(0), done(begin.b >= p_.cache.B) {
+    if (!done) enter();
+  }
+  __device__ bool next(Seg& s) {
+    while (!done) {
+      const Span w = span_of(p, c, at.r);
+      const bool stop = at.b == end.b && at.kvh == end.kvh && at.r == end.r;
+      const int t0 = at.t, t1 = stop ? end.t : w.nt;
+      s.b = at.b, s.kvh = at.kvh, s.row0 = at.r * kRows, s.rows = c.count * p.g;
+      s.first = c.first, s.lo = w.lo, s.hi = w.hi;
+      s.t = w.t0 + t0, s.n = t1 - t0;
+      s.part = t0 > 0 ? 0 : t1 < w.nt ? 1 : -1;
+      done = stop;
+      at.t = 0;
+      if (!done && ++at.r == units) {
+        at.r = 0;
+        if (++at.kvh == p.cache.Hkv) {
+          at.kvh = 0;
+          do {
+            if (++at.b >= p.cache.B) {
+              done = true;
+              break;
+            }
+            enter();
+          } while (c.count == 0);
+        }
+      }
+      if (s.n > 0) return true;
+    }
+    return false;
+  }
+
+ private:
+  __device__ void enter() {
+    c = chunk_of(p, at.b);
+    units = units_of(p, c);
+  }
+};
+
+// ---------------------------------------------------------------------------------------------
+// Producer of bf16 tiles (one warp)
+// ---------------------------------------------------------------------------------------------
+template <class C, class T>
+__device__ __forceinline__ void produce(const PagedAttendParams& p, uint8_t* smem, T* ctl, Walk w) {
+  const int lane = threadIdx.x % 32;
+  volatile int* abort_flag = &ctl->abort_flag;
+  const PagedDev& cache = p.cache;
+  const int frag = p.frag_rows, frags = kTile / frag, panel = lane % C::PANELS;
+  const uint32_t ops = frags * C::PANELS;
+  int it = 0, tiles = 0;
+  bool ok = true;
+  // page and slot of a key's fragment; -1: none
+  auto lookup = [&](int b, int key, int* slot) {
+    return page_at(cache, b, key, slot);
+  };
+  Seg s;
+  while (ok && w.next(s)) {
+    for (int i = 0; ok && i < s.n; ++i, ++tiles) {
+      const int k0 = (s.t + i) * kTile;
+      const int key = k0 + lane / C::PANELS * frag;
+      const bool op = lane < ops;
+      const bool seen = op && key < s.hi && key + frag > s.lo;
+      int slot = 0, page = -1;
+      if (seen) page = lookup(s.b, key, &slot);
+      const uint32_t none = __ballot_sync(0xffffffffu, seen && page < 0);
+      if (none && lane == 0) atomicOr(p.status, kDevPageRange);
+      // K: fragments that no row sees stay as they are, their scores are masked
+      int st = it % C::STAGES;
+      ok = __all_sync(0xffffffffu, mbar_wait(&ctl->kv_empty[st], ((it / C::STAGES) & 1) ^ 1, p.status, abort_flag));
+      if (!ok) break;
+      const uint32_t loads = __ballot_sync(0xffffffffu, page >= 0);
+      if (lane == 0) {
+        uint64_t bad = 0;
+        for (uint32_t m = none; m; m &= m - 1) {
+          const int f = (__ffs(m) - 1) / C::PANELS;
+          for (int x = 0; x < frag / 16; ++x) bad |= 0xFFull << (8 * (f * (frag / 16) + x));
+        }
+        ctl->bad[tiles % C::NOTES] = bad;
+        mbar_arrive_expect_tx(&ctl->kv_full[st], __popc(loads) * frag * 128);
+      }
+      __syncwarp();
+      uint8_t* dst = smem + C::OFF_KV + st * C::TILE;
+      if (page >= 0)
+        tma_load_4d(dst + panel * (kTile * 128) + (lane / C::PANELS) * frag * 128, &p.tmK, &ctl->kv_full[st], panel * 64, slot,
+                    s.kvh, page);
+      ++it;
+      // V: what no row sees or has no page is filled with zeros (a box outside the pool)
+      st = it % C::STAGES;
+      ok = __all_sync(0xffffffffu, mbar_wait(&ctl->kv_empty[st], ((it / C::STAGES) & 1) ^ 1, p.status, abort_flag));
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&ctl->kv_full[st], C::TILE);
+      __syncwarp();
+      dst = smem + C::OFF_KV + st * C::TILE;
+      if (k0 >= s.lo && k0 + kTile <= s.hi) {
+        if (op)
+          tma_load_4d(dst + panel * (kTile * 128) + (lane / C::PANELS) * frag * 128, &p.tmV, &ctl->kv_full[st], panel * 64, slot,
+                      s.kvh, page >= 0 ? page : cache.num_pages);
+      } else {
+        // 16 keys at a time, one at a time where only some of them are seen
+        const int grp = lane / C::PANELS, a = k0 + grp * 16;
+        const bool mine = lane < 8 * C::PANELS;
+        const int from = max(a, s.lo), to = min(a + 16, s.hi);
+        page = -1, slot = 0;
+        if (mine && from < to) page = lookup(s.b, a, &slot);
+        const bool some = mine && page >= 0 && to - from < 16;
+        if (mine && !some)
+          tma_load_4d(dst + panel * (kTile * 128) + grp * 2048, &p.tmV16, &ctl->kv_full[st], panel * 64, slot, s.kvh,
+                      page >= 0 ? page : cache.num_pages);
+        for (uint32_t m = __ballot_sync(0xffffffffu, some); m; m &= m - 1) {
+          const int src = __ffs(m) - 1;
+          const int a2 = __shfl_sync(0xffffffffu, a, src), pg = __shfl_sync(0xffffffffu, page, src);
+          const int sl = __shfl_sync(0xffffffffu, slot, src);
+          if (lane < 16) {
+            const int k = a2 + lane;
+            tma_load_4d(dst + (src % C::PANELS) * (kTile * 128) + (a2 - k0 + lane) * 128, &p.tmV1, &ctl->kv_full[st],
+                        (src % C::PANELS) * 64, sl + lane, s.kvh, k >= s.lo && k < s.hi ? pg : cache.num_pages);
+          }
+        }
+      }
+      ++it;
+    }
+  }
+  // no copy may be in flight when the CTA ends
+  for (int i = max(0, it - C::STAGES); i < it; ++i)
+    mbar_wait(&ctl->kv_full[i % C::STAGES], (i / C::STAGES) & 1, p.status, nullptr);
+}
+
+// ---------------------------------------------------------------------------------------------
+// Expanders of 4-bit tiles (four warps): a thread takes a key
+// ---------------------------------------------------------------------------------------------
+// Four codes (the low 16 bits of w) times a step: fp16 (F16) or bf16 pairs.
+template <bool F16>
+__device__ __forceinline__ uint2 expand4(uint32_t w, uint32_t step2) {
+  // 1024 + n in fp16, 128 + n in bf16; less 1024 + 8 and 128 + 8; times the step
+  constexpr uint32_t kMagic = F16 ? 0x64006400u : 0x43004300u, kOff = F16 ? 0x64086408u : 0x43084308u;
+  const uint32_t a = (w & 0xFu) | ((w << 12) & 0xF0000u) | kMagic;
+  const uint32_t b = ((w >> 8) & 0xFu) | ((w << 4) & 0xF0000u) | kMagic;
+  uint2 r;
+  if constexpr (F16) {
+    asm("{\n\t.reg .b32 t;\n\tsub.rn.f16x2 t, %1, %2;\n\tmul.rn.f16x2 %0, t, %3;\n\t}" : "=r"(r.x) : "r"(a), "r"(kOff), "r"(step2));
+    asm("{\n\t.reg .b32 t;\n\tsub.rn.f16x2 t, %1, %2;\n\tmul.rn.f16x2 %0, t, %3;\n\t}" : "=r"(r.y) : "r"(b), "r"(kOff), "r"(step2));
   } else {
-    const int e = C * lane, g = e / 32, r = e % 32 / 4;
-    const uint16_t word = *reinterpret_cast<const uint16_t*>(pool + row + q4_place<D>(r, slot) * (D / 16) + 2 * g);
-    const float step = __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(steps + steps_row + 2 * g)) << 16);
+    asm("{\n\t.reg .b32 t;\n\tsub.rn.bf16x2 t, %1, %2;\n\tmul.rn.bf16x2 %0, t, %3;\n\t}" : "=r"(r.x) : "r"(a), "r"(kOff), "r"(step2));
+    asm("{\n\t.reg .b32 t;\n\tsub.rn.bf16x2 t, %1, %2;\n\tmul.rn.bf16x2 %0, t, %3;\n\t}" : "=r"(r.y) : "r"(b), "r"(kOff), "r"(step2));
+  }
+  return r;
+}
+
+template <int D>
+struct Row4 {
+  uint4 c[D / 32];           // codes, halves swapped back
+  uint32_t s[D / 64];        // steps, two in each
+};
+template <int D>
+__device__ __forceinline__ void load_row4(Row4<D>& r, const uint8_t* codes, const uint8_t* steps, int slot) {
+  const int swap = D == 128 ? slot & 2 : 0;
 #pragma unroll
-    for (int c = 0; c < C; ++c) x[c] = step * (static_cast<float>((word >> (4 * ((e + c) % 4))) & 15) - 8.0f);
+  for (int m = 0; m < D / 32; ++m)
+    r.c[m] = __ldg(reinterpret_cast<const uint4*>(codes + static_cast<int64_t>(slot) * (D / 2)) + (m ^ swap));
+  if constexpr (D == 128) {
+    const uint2 s = __ldg(reinterpret_cast<const uint2*>(steps + static_cast<int64_t>(slot) * 8));
+    r.s[0] = s.x, r.s[1] = s.y;
+  } else {
+    r.s[0] = __ldg(reinterpret_cast<const uint32_t*>(steps + static_cast<int64_t>(slot) * 4));
+  }
+}
+// Expands a row into a tile (128-byte swizzle, panels of 64 elements); steps: the pair of a group.
+template <int D, bool F16>
+__device__ __forceinline__ void store_row4(const Row4<D>& r, const uint32_t (&step2)[D / 32], uint8_t* tile, int row) {
+#pragma unroll
+  for (int m = 0; m < D / 32; ++m)
+#pragma unroll
+    for (int g = 0; g < D / 32; ++g) {
+      // d = 128: 16 bytes are two chunks of four groups' words; d = 64: four chunks of two
+#pragma unroll
+      for (int q = 0; q < (D == 128 ? 1 : 2); ++q) {
+        const uint32_t even = D == 128 ? (g < 2 ? r.c[m].x : r.c[m].y) : (q == 0 ? r.c[m].x : r.c[m].z);
+        const uint32_t odd = D == 128 ? (g < 2 ? r.c[m].z : r.c[m].w) : (q == 0 ? r.c[m].y : r.c[m].w);
+        const uint2 x = expand4<F16>((g & 1) ? even >> 16 : even, step2[g]);
+        const uint2 y = expand4<F16>((g & 1) ? odd >> 16 : odd, step2[g]);
+        const int chunk = 4 * g + (D == 128 ? m : 2 * m + q);
+        *reinterpret_cast<uint4*>(tile + (chunk >> 3) * (kTile * 128) + sw128_offset(row, chunk & 7)) = make_uint4(x.x, x.y, y.x, y.y);
+      }
+    }
+}
+
+template <int D, class C, class T>
+__device__ __forceinline__ void expand(const PagedAttendParams& p, uint8_t* smem, T* ctl, Walk w) {
+  const int row = threadIdx.x % 128, lane = threadIdx.x % 32;
+  volatile int* abort_flag = &ctl->abort_flag;
+  const PagedDev& cache = p.cache;
+  int it = 0, tiles = 0;
+  bool ok = true;
+  Seg s;
+  while (ok && w.next(s)) {
+    const uint8_t* const pool[2] = {cache.k + s.kvh * cache.k_sh, cache.v + s.kvh * cache.v_sh};
+    const uint8_t* const steps[2] = {cache.ks + s.kvh * cache.ks_sh, cache.vs + s.kvh * cache.vs_sh};
+    Row4<D> k, v;
+    int page;
+    bool seen;
+    auto load = [&](int i) {
+      const int key = (s.t + i) * kTile + row;
+      seen = key >= s.lo && key < s.hi;
+      page = -1;
+      int slot = 0;
+      if (seen) page = page_at(cache, s.b, key, &slot);
+#pragma unroll
+      for (int m = 0; m < D / 32; ++m) k.c[m] = v.c[m] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int m = 0; m < D / 64; ++m) k.s[m] = v.s[m] = 0;
+      if (page >= 0) {
+        load_row4<D>(k, pool[0] + page * cache.k_sp, steps[0] + page * cache.ks_sp, slot);
+        load_row4<D>(v, pool[1] + page * cache.v_sp, steps[1] + page * cache.vs_sp, slot);
+      }
+    };
+    load(0);
+    for (int i = 0; i < s.n; ++i, ++tiles) {
+      int st = it % C::STAGES;
+      ok = __all_sync(0xffffffffu, mbar_wait(&ctl->kv_empty[st], ((it / C::STAGES) & 1) ^ 1, p.status, abort_flag));
+      if (!ok) break;
+      const bool none = seen && page < 0;
+      if (__any_sync(0xffffffffu, none) && lane == 0) atomicOr(p.status, kDevPageRange);
+      if (row % 16 == 0) reinterpret_cast<uint8_t*>(&ctl->bad[tiles % C::NOTES])[row / 16] = none ? 0xFF : 0;
+      {
+        // steps under a power of two that takes the key's largest to [2^11, 2^12): products of 11
+        // bits at most, exact in fp16's normal range
+        uint32_t most = 0;
+#pragma unroll
+        for (int m = 0; m < D / 64; ++m) most = max(most, max(k.s[m] & 0x7FFFu, (k.s[m] >> 16) & 0x7FFFu));
+        const uint32_t e = max(most >> 7, 12u);
+        const float up = __uint_as_float((254u + 11u - e) << 23);
+        ctl->factor[tiles % C::NOTES][row] = __uint_as_float((e - 11u) << 23);
+        uint32_t step2[D / 32];
+#pragma unroll
+        for (int g = 0; g < D / 32; ++g) {
+          const float x = (g & 1) ? bf16hi_to_f32(k.s[g / 2]) : bf16lo_to_f32(k.s[g / 2]);
+          const __half2 h = __float2half2_rn(x * up);
+          step2[g] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        store_row4<D, true>(k, step2, smem + C::OFF_KV + st * C::TILE, row);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->kv_full[st]);
+      ++it;
+      st = it % C::STAGES;
+      ok = __all_sync(0xffffffffu, mbar_wait(&ctl->kv_empty[st], ((it / C::STAGES) & 1) ^ 1, p.status, abort_flag));
+      if (!ok) break;
+      {
+        uint32_t step2[D / 32];
+#pragma unroll
+        for (int g = 0; g < D / 32; ++g) step2[g] = __byte_perm(v.s[g / 2], 0, (g & 1) ? 0x3232 : 0x1010);
+        store_row4<D, false>(v, step2, smem + C::OFF_KV + st * C::TILE, row);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->kv_full[st]);
+      ++it;
+      if (i + 1 < s.n) load(i + 1);
+    }
   }
 }
 
-template <int D, bool Q4>
-__global__ void __launch_bounds__(kThreads) attend_rows_kernel(const __grid_constant__ PagedAttendParams p) {
-  constexpr int C = D / 32;
-  const int lane = threadIdx.x % 32;
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / 32;
-  if (w >= static_cast<int64_t>(p.cache.B) * p.Hq * p.N) return;
-  const int n = static_cast<int>(w % p.N), h = static_cast<int>(w / p.N % p.Hq), b = static_cast<int>(w / p.N / p.Hq);
-  int first = __ldg(p.first + b), count = p.count ? __ldg(p.count + b) : p.N;
-  bool bad = count < 0 || count > p.N;
-  count = min(max(count, 0), p.N);
-  if (count > 0 && (first < 0 || static_cast<int64_t>(first) + count > p.cache.cap)) {
-    bad = true;
-    if (first < 0 || first >= p.cache.cap) first = 0, count = 0;
-    else count = p.cache.cap - first;
-  }
-  if (bad && lane == 0) atomicOr(p.status, kDevPageRange);
-  __nv_bfloat16* out = p.out + b * p.o_sb + h * p.o_sh + n * p.o_sn + C * lane;
-  float m = kNegInf, l = 0.f, o[C] = {};
-  if (n < count) {
-    const int pos = first + n;
-    float q[C];
-    const __nv_bfloat16* at = p.q + b * p.q_sb + h * p.q_sh + n * p.q_sn + C * lane;
+// ---------------------------------------------------------------------------------------------
+// Query loaders (two warps)
+// ---------------------------------------------------------------------------------------------
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+template <int D, bool TWO, class C, class T>
+__device__ __forceinline__ void load_queries(const PagedAttendParams& p, uint8_t* smem, T* ctl, Walk w) {
+  constexpr int CH = D / 8;  // 16-byte pieces of a row
+  const int tid = threadIdx.x - 64, lane = threadIdx.x % 32;
+  const int chunk = tid % CH;
+  volatile int* abort_flag = &ctl->abort_flag;
+  int used[2] = {0, 0};
+  bool ok = true;
+  Seg s;
+  while (ok && w.next(s)) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) q[c] = __bfloat162float(at[c]);
-    if (p.rope) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const float other = __shfl_xor_sync(0xffffffffu, q[c], 16);
-        const float4 a = turn_cossin(static_cast<float>(pos), freq_at(p.freqs, (C * lane + c) % (D / 2)));
-        q[c] = q[c] * (a.x + a.y) + (lane < 16 ? -other : other) * (a.z + a.w);
+    for (int slot = 0; slot < 2; ++slot) {
+      const int r0 = s.row0 + 128 * slot;
+      if (r0 >= s.rows) continue;
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(&ctl->q_empty[slot], (used[slot] & 1) ^ 1, p.status, abort_flag));
+      if (!ok) break;
+      ++used[slot];
+      const uint32_t to = smem_u32(smem + slot * C::QSLOT) + (chunk >> 3) * (kTile * 128);
+      const __nv_bfloat16* from = p.q + s.b * p.q_sb + static_cast<int64_t>(s.kvh) * p.g * p.q_sh + chunk * 8;
+      for (int r = tid / CH; r < 128; r += 64 / CH) {
+        const uint32_t dst = to + sw128_offset(r, chunk & 7);
+        const uint32_t row = min(r0 + r, s.rows - 1);  // rows behind the last are not used
+        const uint32_t n = row / static_cast<uint32_t>(p.g), j = row - n * p.g;
+        const __nv_bfloat16* x = from + n * p.q_sn + j * p.q_sh;
+        cp_async16(dst, x);
+        if (TWO) cp_async16(dst + C::TILE, x + p.q_lo);
       }
-    }
-    const float slope = p.slopes ? __ldg(p.slopes + h) : 0.f;
-    const int kvh = h / p.g;
-    for (int i = p.window > 0 ? max(0, pos - p.window + 1) : 0; i <= pos; ++i) {
-      int slot;
-      const int page = page_at(p.cache, b, i, &slot);
-      if (page < 0) {
-        if (lane == 0) atomicOr(p.status, kDevPageRange);
-        continue;
-      }
-      const int64_t st = Q4 ? D / 2 : 0;
-      float k[C], v[C];
-      row_piece<D, Q4>(p.cache.k, p.cache.ks, page * p.cache.k_sp + kvh * p.cache.k_sh + slot * (Q4 ? st : p.cache.k_st),
-                       page * p.cache.ks_sp + kvh * p.cache.ks_sh + slot * (D / 16), slot, lane, k);
-      row_piece<D, Q4>(p.cache.v, p.cache.vs, page * p.cache.v_sp + kvh * p.cache.v_sh + slot * (Q4 ? st : p.cache.v_st),
-                       page * p.cache.vs_sp + kvh * p.cache.vs_sh + slot * (D / 16), slot, lane, v);
-      float s = 0.f;
-#pragma unroll
-      for (int c = 0; c < C; ++c) s = fmaf(q[c], k[c], s);
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-      s = s * p.scale + slope * static_cast<float>(i - pos);
-      if (s > m) {
-        const float a = expf(m - s);
-        m = s;
-        l *= a;
-#pragma unroll
-        for (int c = 0; c < C; ++c) o[c] *= a;
-      }
-      const float e = m == kNegInf ? 0.f : expf(s - m);
-      l += e;
-#pragma unroll
-      for (int c = 0; c < C; ++c) o[c] = fmaf(e, v[c], o[c]);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->q_full[slot]);
     }
   }
-  const bool any = !(l == 0.f);
+}
+
+// ---------------------------------------------------------------------------------------------
+// Issuer of the products (one thread)
+// ---------------------------------------------------------------------------------------------
+template <int D, bool Q4, bool TWO, class C, class T>
+__device__ __forceinline__ void issue(const PagedAttendParams& p, uint8_t* smem, T* ctl, Walk w, uint32_t tmem) {
+  constexpr uint32_t idesc_s = idesc_f32acc(128, 128, 0, 0, Q4), idesc_o = idesc_f32acc(128, D, 0, 1);
+  volatile int* abort_flag = &ctl->abort_flag;
+  int* status = p.status;
+  const uint32_t sQ = smem_u32(smem), sKV = smem_u32(smem + C::OFF_KV);
+  int qu[2] = {0, 0}, pu[2] = {0, 0};
+  bool ok = true;
+  auto wait_tile = [&](int it) {
+    ok = ok && mbar_wait(&ctl->kv_full[it % C::STAGES], (it / C::STAGES) & 1, status, abort_flag);
+  };
+  auto scores = [&](int s, int it, bool first, bool last) {
+    if (first) ok = ok && mbar_wait(&ctl->q_full[s], qu[s]++ & 1, status, abort_flag);
+    if (!ok) return;
+    tc_fence_after();
+    const uint32_t k = sKV + (it % C::STAGES) * C::TILE;
 #pragma unroll
-  for (int c = 0; c < C; ++c) out[c] = __float2bfloat16_rn(any ? o[c] / l : 0.f);
-  if (p.lse && lane == 0) p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.N + n] = any ? m + logf(l) : kNegInf;
+    for (int part = 0; part < (TWO ? 2 : 1); ++part)
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+        mma_ss(tmem + 128 * s, smem_desc_sw128(sQ + s * C::QSLOT + part * C::TILE + off, 16, 1024), smem_desc_sw128(k + off, 16, 1024),
+               idesc_s, part > 0 || kk > 0);
+      }
+    mma_commit(&ctl->s_full[s]);
+    if (last) mma_commit(&ctl->q_empty[s]);
+  };
+  auto values = [&](int s, int it, bool first, bool last) {
+    ok = ok && mbar_wait(&ctl->p_full[s], pu[s]++ & 1, status, abort_flag);
+    if (!ok) return;
+    tc_fence_after();
+    const uint32_t v = sKV + (it % C::STAGES) * C::TILE;
+#pragma unroll
+    for (int kk = 0; kk < kTile / 16; ++kk)
+      mma_ts(tmem + 256 + 128 * s, tmem + 128 * s + kk * 8, smem_desc_sw128(v + kk * 2048, kTile * 128, 1024), idesc_o, !first || kk > 0);
+    if (last) mma_commit(&ctl->o_full[s]);
+  };
+  Seg cur, nxt;
+  bool have = w.next(nxt);
+  int ci = 0, ni = 0, it = 0;  // tile of the segment, ring index of the tile's K
+  bool act[2] = {true, false}, nact[2] = {true, false};
+  if (have) {
+    nact[1] = nxt.row0 + 128 < nxt.rows;
+    wait_tile(0);
+    for (int s = 0; s < 2; ++s)
+      if (nact[s]) scores(s, 0, true, nxt.n == 1);
+    if (ok) mma_commit(&ctl->kv_empty[0]);
+  }
+  while (ok && have) {
+    cur = nxt, ci = ni;
+    act[1] = nact[1];
+    const bool first = ci == 0, last = ci == cur.n - 1;
+    if (last) {
+      have = w.next(nxt);
+      ni = 0;
+      if (have) nact[1] = nxt.row0 + 128 < nxt.rows;
+    } else {
+      ++ni;
+    }
+    const int vt = it + 1, kt = it + 2;
+    wait_tile(vt);
+    for (int s = 0; s < 2 && ok; ++s) {
+      if (act[s]) values(s, vt, first, last);
+      if (s == 1 || !act[1]) {
+        if (ok && (s == 0 || act[1])) mma_commit(&ctl->kv_empty[vt % C::STAGES]);
+      }
+      if (have && s == 0) wait_tile(kt);
+      if (have && nact[s] && ok) scores(s, kt, ni == 0, ni == nxt.n - 1);
+    }
+    if (ok && have) mma_commit(&ctl->kv_empty[kt % C::STAGES]);
+    it = kt;
+  }
+  // all products have ended before tensor memory is given back
+  mma_commit(&ctl->last);
+  mbar_wait(&ctl->last, 0, status, nullptr);
+}
+
+// ---------------------------------------------------------------------------------------------
+// Softmax of row tile s (four warps, one row per thread)
+// ---------------------------------------------------------------------------------------------
+template <int D, bool Q4, class C, class T>
+__device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk w, uint32_t tmem, int slot) {
+  const int lane = threadIdx.x % 32, quarter = (threadIdx.x / 32) % 4, r = quarter * 32 + lane;
+  volatile int* abort_flag = &ctl->abort_flag;
+  int* status = p.status;
+  const uint32_t tS = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 128 * slot;
+  const uint32_t tO = tS - 128 * slot + 256 + 128 * slot;
+  int sc = 0, oc = 0, tiles = 0;
+  bool ok = true;
+  Seg s;
+  while (ok && w.next(s)) {
+    if (s.row0 + 128 * slot >= s.rows) {
+      tiles += s.n;
+      continue;
+    }
+    const int row = s.row0 + 128 * slot + r;
+    const bool live = row < s.rows;
+    const uint32_t n = static_cast<uint32_t>(min(row, s.rows - 1)) / static_cast<uint32_t>(p.g);
+    const int h = s.kvh * p.g + (min(row, s.rows - 1) - static_cast<int>(n) * p.g);
+    const int pos = live ? s.first + static_cast<int>(n) : -1;   // a row behind the last sees nothing
+    const int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+    float mul = p.scale_log2;
+    if (Q4) mul *= __ldg(p.factor + (static_cast<int64_t>(s.b) * p.Hq + h) * p.N + n);
+    const float slope = p.slopes ? __ldg(p.slopes + h) * kLog2e : 0.f;
+    float m_run = kNegInf, l_run = 0.f;
+    for (int i = 0; i < s.n; ++i, ++tiles) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&ctl->s_full[slot], sc & 1, status, abort_flag));
+      if (!ok) break;
+      ++sc;
+      tc_fence_after();
+      uint32_t xr[128];
+      tmem_ld32<0>(tS, xr);
+      tmem_ld32<32>(tS + 32, xr);
+      tmem_ld32<64>(tS + 64, xr);
+      tmem_ld32<96>(tS + 96, xr);
+      const uint64_t bad = *reinterpret_cast<volatile uint64_t*>(&ctl->bad[tiles % C::NOTES]);
+      tmem_wait_ld();
+      float x[128];
+#pragma unroll
+      for (int c = 0; c < 128; ++c) x[c] = __uint_as_float(xr[c]);
+      if constexpr (Q4) {
+        const float4* f = reinterpret_cast<const float4*>(ctl->factor[tiles % C::NOTES]);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float4 y = f[c];
+          const uint64_t a = mul2(f2_pack(x[4 * c], x[4 * c + 1]), f2_pack(y.x, y.y));
+          const uint64_t b = mul2(f2_pack(x[4 * c + 2], x[4 * c + 3]), f2_pack(y.z, y.w));
+          x[4 * c] = f2_lo(a), x[4 * c + 1] = f2_hi(a), x[4 * c + 2] = f2_lo(b), x[4 * c + 3] = f2_hi(b);
+        }
+      }
+      const int k0 = (s.t + i) * kTile;
+      float unit = mul;
+      if (p.slopes) {
+        const float base = slope * static_cast<float>(k0 - pos);
+#pragma unroll
+        for (int c = 0; c < 128; ++c) x[c] = __fmaf_rn(slope, static_cast<float>(c), __fmaf_rn(x[c], mul, base));
+        unit = 1.f;
+      }
+      if (__builtin_expect(k0 + kTile - 1 > pos || k0 < lo, 0)) {
+        const int c0 = lo - k0, c1 = pos - k0;
+#pragma unroll
+        for (int c = 0; c < 128; ++c) x[c] = c >= c0 && c <= c1 ? x[c] : kNegInf;
+      }
+      if (__builtin_expect(bad != 0, 0)) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c) x[c] = (bad >> (8 * (c / 16))) & 1 ? kNegInf : x[c];
+      }
+      float mp[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mp[k] = fmaxf(x[2 * k], x[2 * k + 1]);
+#pragma unroll
+      for (int j = 1; j < 8; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mp[k] = max3f(mp[k], x[16 * j + 2 * k], x[16 * j + 2 * k + 1]);
+      const float mx = max3f(max3f(mp[0], mp[1], mp[2]), max3f(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7])) * unit;
+      // O keeps its scale unless this tile exceeds it by more than 2^kLazy
+      const float m_new = mx > m_run + kLazy ? mx : m_run;
+      const bool grow = m_new > m_run && m_run != kNegInf;
+      if (__any_sync(0xffffffffu, grow)) {
+        // (the products of the tile before are complete: S of this one was issued behind them)
+        const float alpha = grow ? ex2_approx(m_run - m_new) : 1.f;
+        l_run *= alpha;
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t o[32];
+          tmem_ld32(tO + ch * 32, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
+          tmem_st32(tO + ch * 32, o);
+        }
+      }
+      m_run = m_new;
+      const float nb = m_new == kNegInf ? 0.f : -m_new;
+      const uint64_t u2 = f2_pack(unit, unit), nb2 = f2_pack(nb, nb);
+      uint64_t acc2[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const int e = 32 * ch + 2 * c;
+          const uint64_t a = fma2(f2_pack(x[e], x[e + 1]), u2, nb2);
+          const float p0 = ex2_approx(f2_lo(a)), p1 = ex2_approx(f2_hi(a));
+          acc2[c & 3] = add2(acc2[c & 3], f2_pack(p0, p1));
+          pk[c] = pack_bf16x2(p0, p1);
+        }
+        tmem_st16(tS + 16 * ch, pk);
+      }
+      const uint64_t acc = add2(add2(acc2[0], acc2[1]), add2(acc2[2], acc2[3]));
+      l_run += f2_lo(acc) + f2_hi(acc);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->p_full[slot]);
+    }
+    if (!ok) break;
+    ok = __all_sync(0xffffffffu, mbar_wait(&ctl->o_full[slot], oc & 1, status, abort_flag));
+    if (!ok) break;
+    ++oc;
+    tc_fence_after();
+    const bool any = !(l_run == 0.f);  // a NaN goes to the output
+    if (s.part < 0) {
+      const float inv = any ? 1.f / l_run : 0.f;
+      __nv_bfloat16* out = p.out + s.b * p.o_sb + h * p.o_sh + n * p.o_sn;
+#pragma unroll 1
+      for (int ch = 0; ch < D / 32; ++ch) {
+        uint32_t o[32];
+        tmem_ld32(tO + ch * 32, o);
+        tmem_wait_ld();
+        if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(out + ch * 32);
+#pragma unroll
+          for (int v4 = 0; v4 < 4; ++v4) {
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int q = v4 * 8 + 2 * e;
+              y[e] = any ? pack_bf16x2(__uint_as_float(o[q]) * inv, __uint_as_float(o[q + 1]) * inv) : 0u;
+            }
+            __stcs(dst + v4, make_uint4(y[0], y[1], y[2], y[3]));
+          }
+        }
+      }
+      if (p.lse && live)
+        p.lse[(static_cast<int64_t>(s.b) * p.Hq + h) * p.N + n] = any ? (m_run + log2f(l_run)) * kLn2 : kNegInf;
+    } else {
+      const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + s.part) * kRows + 128 * slot + r;
+#pragma unroll 1
+      for (int ch = 0; ch < D / 32; ++ch) {
+        uint32_t o[32];
+        tmem_ld32(tO + ch * 32, o);
+        tmem_wait_ld();
+        if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(p.part_acc + at * D + ch * 32);
+#pragma unroll
+          for (int v4 = 0; v4 < 8; ++v4) dst[v4] = make_uint4(o[4 * v4], o[4 * v4 + 1], o[4 * v4 + 2], o[4 * v4 + 3]);
+        }
+      }
+      if (live) p.part_ml[at] = make_float2(m_run, l_run);
+    }
+  }
+}
+
+template <int D, bool Q4, bool TWO>
+__global__ void __launch_bounds__(Cfg<D, Q4, TWO>::THREADS, 1) attend_kernel(const __grid_constant__ PagedAttendParams p) {
+  using C = Cfg<D, Q4, TWO>;
+  using T = Ctl<C::NOTES, Q4>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  T* ctl = reinterpret_cast<T*>(smem + C::OFF_CTL);
+  const int tid = threadIdx.x, warp = tid / 32;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->q_full[i], 2);
+      mbar_init(&ctl->q_empty[i], 1);
+      mbar_init(&ctl->s_full[i], 1);
+      mbar_init(&ctl->p_full[i], 4);
+      mbar_init(&ctl->o_full[i], 1);
+    }
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&ctl->kv_full[i], Q4 ? 4 : 1);
+      mbar_init(&ctl->kv_empty[i], 1);
+    }
+    mbar_init(&ctl->last, 1);
+    ctl->abort_flag = 0;
+    ctl->begin = ctl->end = Pos{p.cache.B, 0, 0, 0};
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl->tmem_base, 512);
+    tmem_relinquish();
+  }
+  // Launched as a programmatic dependent: global memory is touched only from here on.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // thread j sums the work of its share of the sequences
+  const int B = p.cache.B, share = (B + C::THREADS - 1) / C::THREADS;
+  int64_t mine = 0;
+  for (int b = tid * share; b < min(B, (tid + 1) * share); ++b) {
+    const Chunk c = chunk_of(p, b);
+    if (blockIdx.x == 0 && c.bad) atomicOr(p.status, kDevPageRange);
+    mine += cost_before(p, c, units_of(p, c)) * p.cache.Hkv;
+  }
+  int64_t total;
+  const int64_t before = block_prefix<C::THREADS>(mine, ctl->wsum, &total);
+  const Deal deal(total, p.ctas);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int64_t x = deal.start(blockIdx.x + e);
+    if (mine > 0 && x >= before && x < before + mine) {
+      int64_t y = x - before;
+      for (int b = tid * share;; ++b) {
+        const Chunk c = chunk_of(p, b);
+        const int64_t all = cost_before(p, c, units_of(p, c)) * p.cache.Hkv;
+        if (y < all) {
+          (e ? ctl->end : ctl->begin) = find_in(p, b, c, y).pos;
+          break;
+        }
+        y -= all;
+      }
+    }
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  const Walk w(p, ctl->begin, ctl->end);
+  if (warp < 4) {
+    setmaxnreg_dec<C::LOW>();
+    if (warp == 0) {
+      if constexpr (!Q4) produce<C>(p, smem, ctl, w);
+    } else if (warp == 1) {
+      if (tid % 32 == 0) issue<D, Q4, TWO, C>(p, smem, ctl, w, tmem);
+    } else {
+      load_queries<D, TWO, C>(p, smem, ctl, w);
+    }
+  } else if (warp < 12) {
+    setmaxnreg_inc<C::SM>();
+    softmax<D, Q4, C>(p, ctl, w, tmem, (warp - 4) / 4);
+  } else if constexpr (Q4) {
+    setmaxnreg_dec<C::EXP>();
+    expand<D, C>(p, smem, ctl, w);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------------------------
+// Joining cut units, and rows of padding
+// ---------------------------------------------------------------------------------------------
+// Block (x, y): if run x + 1 begins within a unit whose first tiles run x has, rows 32 y .. of that unit.
+constexpr int kJoinRows = 32;
+
+template <int D>
+__global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ PagedAttendWork p) {
+  __shared__ int64_t wsum[8];
+  __shared__ Found found;
+  __shared__ int64_t found_before;
+  __shared__ int16_t order[kPagedMaxCtas];
+  __shared__ int order_n;
+  // the stream's next kernel may come in and wait
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x;
+  const int B = p.cache.B, share = (B + 255) / 256;
+  if (tid == 0) found.pos.t = 0;
+  int64_t mine = 0;
+  for (int b = tid * share; b < min(B, (tid + 1) * share); ++b) {
+    const Chunk c = chunk_of(p, b);
+    mine += cost_before(p, c, units_of(p, c)) * p.cache.Hkv;
+  }
+  int64_t total;
+  const int64_t before = block_prefix<256>(mine, wsum, &total);
+  const Deal deal(total, p.ctas);
+  const int run = blockIdx.x + 1;
+  const int64_t x = run < p.ctas ? deal.start(run) : total;
+  if (mine > 0 && x >= before && x < before + mine) {
+    int64_t y = x - before;
+    for (int b = tid * share;; ++b) {
+      const Chunk c = chunk_of(p, b);
+      const int64_t all = cost_before(p, c, units_of(p, c)) * p.cache.Hkv;
+      if (y < all) {
+        found = find_in(p, b, c, y);
+        found_before = x - y;
+        break;
+      }
+      y -= all;
+    }
+  }
+  __syncthreads();
+  const Found f = found;
+  // Partial results of the unit, in the order of its tiles: run - 1's last segment, then the first ones
+  // of the runs that begin within it. (A run of less than a tile may have none.)
+  int parts = 0;
+  if (f.pos.t > 0) {
+    const int64_t unit = found_before + f.unit;
+    auto tile_of = [&](int k) {  // where boundary k cuts the unit
+      const int64_t z = k < p.ctas ? deal.start(k) : total;
+      return z <= unit ? 0 : z >= unit + f.cost ? f.nt : tile_at(p, z - unit, f.cost, f.nt);
+    };
+    if (tile_of(run - 1) == 0) {
+      for (int k = run - 1 + tid; k < p.ctas; k += 256) {
+        const int t0 = tile_of(k), t1 = tile_of(k + 1);
+        order[k - run + 1] = t0 == f.nt ? -1 : t0 < t1 ? 1 : 0;
+      }
+      __syncthreads();
+      if (tid == 0) {
+        int n = 0;
+        for (int k = 0; k < p.ctas - run + 1 && order[k] >= 0; ++k)
+          if (order[k]) order[n++] = static_cast<int16_t>(k);
+        order_n = n;
+      }
+      __syncthreads();
+      parts = order_n;
+    }
+  }
+  // partial rows, and the order of writes to out and lse against earlier kernels, from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // padding: rows [count, N) of every head
+  const int blocks = gridDim.x * gridDim.y, block = blockIdx.y * gridDim.x + blockIdx.x;
+  const int groups = min(B, blocks);  // blocks of one number modulo this share sequences
+  for (int b = block % groups; b < B; b += groups) {
+    const int count = chunk_of(p, b).count;
+    const int64_t pieces = static_cast<int64_t>(p.N - count) * p.Hq * (D / 8);
+    const int64_t step = static_cast<int64_t>((blocks - block % groups + groups - 1) / groups) * 256;
+    for (int64_t i = static_cast<int64_t>(block / groups) * 256 + tid; i < pieces; i += step) {
+      const int64_t row = i / (D / 8);
+      const int h = static_cast<int>(row / (p.N - count)), n = count + static_cast<int>(row % (p.N - count));
+      *reinterpret_cast<uint4*>(p.out + b * p.o_sb + h * p.o_sh + n * p.o_sn + i % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
+      if (p.lse && i % (D / 8) == 0) p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.N + n] = kNegInf;
+    }
+  }
+  if (parts == 0) return;
+  const Chunk c = chunk_of(p, f.pos.b);
+  constexpr int L = D / 4;  // threads of a row
+  const int col = tid % L * 4;
+  for (int i = tid / L; i < kJoinRows; i += 256 / L) {
+    const int r = blockIdx.y * kJoinRows + i, row = f.pos.r * kRows + r;
+    if (row >= c.count * p.g) break;
+    auto at = [&](int i) {
+      const int k = order[i];
+      return (static_cast<int64_t>(run - 1 + k) * 2 + (k == 0 ? 1 : 0)) * kRows + r;
+    };
+    float mx = kNegInf;
+    for (int k = 0; k < parts; ++k) mx = fmaxf(mx, p.part_ml[at(k)].x);
+    const float base = mx == kNegInf ? 0.f : mx;
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < parts; ++k) {
+      const float2 ml = p.part_ml[at(k)];
+      const float4 o = *reinterpret_cast<const float4*>(p.part_acc + at(k) * D + col);
+      const float wgt = ex2_approx(ml.x - base);
+      sum += wgt * ml.y;
+      acc.x += wgt * o.x, acc.y += wgt * o.y, acc.z += wgt * o.z, acc.w += wgt * o.w;
+    }
+    const bool any = !(sum == 0.f);
+    const float inv = any ? 1.f / sum : 0.f;
+    const int n = row / p.g, h = f.pos.kvh * p.g + row % p.g;
+    *reinterpret_cast<uint2*>(p.out + f.pos.b * p.o_sb + h * p.o_sh + n * p.o_sn + col) =
+        any ? make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv)) : make_uint2(0, 0);
+    if (p.lse && col == 0) p.lse[(static_cast<int64_t>(f.pos.b) * p.Hq + h) * p.N + n] = any ? (mx + log2f(sum)) * kLn2 : kNegInf;
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Query operands: rotated rows in two parts; for 4-bit caches in fp16 under a power of two
+// ---------------------------------------------------------------------------------------------
+constexpr int kQueryThreads = 128;
+
+template <int D, bool Q4, bool ROPE>
+__global__ void __launch_bounds__(kQueryThreads) attend_query_kernel(const __grid_constant__ PagedQueryParams p) {
+  constexpr int CP = D / 16, H2 = D / 2;
+  extern __shared__ float4 ang[];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) << p.rb_log2;
+  const int t = threadIdx.x % CP, k = threadIdx.x / CP, rr = k & ((1 << p.rb_log2) - 1);
+  const int step = (kQueryThreads / CP) >> p.rb_log2;
+  auto where = [&](int64_t row, int* n) {
+    const int b = static_cast<int>(p.div_n ? __umul64hi(static_cast<uint64_t>(row), p.div_n) : row);
+    *n = static_cast<int>(row - static_cast<int64_t>(b) * p.N);
+    return b;
+  };
+  const int64_t row = row0 + rr;
+  int n = 0, b = 0;
+  bool live = row < p.rows;
+  if (live) {
+    b = where(row, &n);
+    live = n < chunk_of(p.first, p.count, b, p.N, p.cap).count;
+  }
+  if (ROPE) {
+    for (int i = threadIdx.x; i < H2 << p.rb_log2; i += kQueryThreads) {
+      const int64_t r = row0 + i / H2;
+      if (r >= p.rows) break;
+      int rn;
+      const int rb = where(r, &rn);
+      const Chunk c = chunk_of(p.first, p.count, rb, p.N, p.cap);
+      if (rn >= c.count) continue;
+      const int j = i % H2, q = j / CP, u = j % CP;
+      const float4 a = turn_cossin(static_cast<float>(c.first + rn), freq_at(p.freqs, 8 * u + q));
+      ang[(i / H2) * H2 + q * CP + u] = a;
+    }
+    __syncthreads();
+  }
+  for (int h0 = 0; h0 < p.Hq; h0 += step) {  // (all threads alike: the warp exchanges maxima)
+    const int h = h0 + (k >> p.rb_log2);
+    const bool on = live && h < p.Hq;
+    float x[16];
+    if (on) {
+      const uint8_t* from = p.q + b * p.q_sb + n * p.q_sn + h * p.q_sh + t * 16;
+      const uint4 lo = __ldg(reinterpret_cast<const uint4*>(from)), hi = __ldg(reinterpret_cast<const uint4*>(from + D));
+      const uint32_t L[4] = {lo.x, lo.y, lo.z, lo.w}, G[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float xl = (q & 1) ? bf16hi_to_f32(L[q / 2]) : bf16lo_to_f32(L[q / 2]);
+        const float xh = (q & 1) ? bf16hi_to_f32(G[q / 2]) : bf16lo_to_f32(G[q / 2]);
+        x[q] = xl, x[8 + q] = xh;
+        if (ROPE) {
+          const float4 a = ang[rr * H2 + q * CP + t];
+          const float c = a.x + a.y, s = a.z + a.w;
+          x[q] = __fmaf_rn(xl, c, -xh * s);
+          x[8 + q] = __fmaf_rn(xh, c, xl * s);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 16; ++q) x[q] = 0.f;
+    }
+    float f = 1.f;
+    if (Q4) {
+      float most = 0.f;
+#pragma unroll
+      for (int q = 0; q < 16; ++q) most = fmaxf(most, fabsf(x[q]));
+#pragma unroll
+      for (int o = CP / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+      // to [2^14, 2^15), by 2^100 at most
+      const uint32_t e = max(__float_as_uint(most) >> 23, 41u);
+      const float up = __uint_as_float((254u + 14u - e) << 23);
+      f = __uint_as_float((e - 14u) << 23);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) x[q] *= up;
+    }
+    if (!on) continue;
+    const int64_t to = (static_cast<int64_t>(b) * p.Hq + h) * p.N + n;
+    if (Q4 && t == 0) p.factor[to] = f;
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      const float a = x[2 * w], c = x[2 * w + 1];
+      if (Q4) {
+        const __half2 y = __floats2half2_rn(a, c);
+        hi[w] = *reinterpret_cast<const uint32_t*>(&y);
+        const float2 back = __half22float2(y);
+        const __half2 z = __floats2half2_rn(a - back.x, c - back.y);
+        lo[w] = *reinterpret_cast<const uint32_t*>(&z);
+      } else {
+        hi[w] = pack_bf16x2(a, c);
+        lo[w] = pack_bf16x2(a - bf16lo_to_f32(hi[w]), c - bf16hi_to_f32(hi[w]));
+      }
+    }
+    uint4* dst = reinterpret_cast<uint4*>(p.hi + to * D + t * 8);
+    dst[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    dst[D / 16] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+    if (ROPE) {
+      dst = reinterpret_cast<uint4*>(p.lo + to * D + t * 8);
+      dst[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      dst[D / 16] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+    }
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <class... P>
+cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const P&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int D, bool Q4, bool TWO>
+cudaError_t launch(const PagedAttendParams& p, cudaStream_t stream) {
+  using C = Cfg<D, Q4, TWO>;
+  constexpr size_t bytes = smem_bytes<D, Q4, TWO>();
+  static_assert(bytes <= 232448, "shared memory");
+  auto kern = attend_kernel<D, Q4, TWO>;
+  static std::atomic<uint64_t> ready;  // devices that the kernel's shared memory was allowed on
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready.load(std::memory_order_acquire) & bit) || dev > 63) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
+  e = launch_pdl<PagedAttendParams>(kern, dim3(p.ctas), C::THREADS, bytes, stream, p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl<PagedAttendWork>(attend_join_kernel<D>, dim3(p.ctas, kRows / kJoinRows), 256, 0, stream, p);
+}
+
+size_t part_bytes(int d) {
+  return (size_t)std::min(paged_sm_count(), kPagedMaxCtas) * 2 * kRows * (d * sizeof(float) + sizeof(float2));
 }
 
 }  // namespace
 
-size_t paged_attend_workspace(int, int, int, int, int, int, bool) { return 16; }
+// Partial rows of each CTA; where q is rotated or the cache has 4 bits, its parts and their factors.
+size_t paged_attend_workspace(int B, int Hq, int Hkv, int N, int d, int format, bool rope) {
+  (void)Hkv;
+  const size_t rows = (size_t)B * Hq * N;
+  size_t n = part_bytes(d);
+  if (rope || format == kPagedQ4) n += rows * d * 2 * (rope ? 2 : 1);
+  if (format == kPagedQ4) n += rows * sizeof(float);
+  return n;
+}
 
-cudaError_t launch_paged_attend(PagedAttendParams p, int d, int format, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(p.cache.B) * p.Hq * p.N;
-  void (*kern)(PagedAttendParams);
-  if (format == kPagedQ4) kern = d == 128 ? attend_rows_kernel<128, true> : attend_rows_kernel<64, true>;
-  else kern = d == 128 ? attend_rows_kernel<128, false> : attend_rows_kernel<64, false>;
-  kern<<<static_cast<unsigned>((rows + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_paged_attend(const PagedAttendCall& c, int d, int format, cudaStream_t stream) {
+  PagedAttendParams p = c.p;
+  const bool q4 = format == kPagedQ4, two = c.rope;
+  p.ctas = std::min(paged_sm_count(), kPagedMaxCtas);
+  p.part_acc = static_cast<float*>(c.workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part_acc + (int64_t)p.ctas * 2 * kRows * d);
+  if (two || q4) {
+    PagedQueryParams q;
+    q.q = reinterpret_cast<const uint8_t*>(p.q);
+    q.q_sb = p.q_sb * 2, q.q_sh = p.q_sh * 2, q.q_sn = p.q_sn * 2;
+    q.first = p.first;
+    q.count = p.count;
+    q.cap = p.cache.cap;
+    q.Hq = p.Hq;
+    q.N = p.N;
+    q.rows = (int64_t)p.cache.B * p.N;
+    q.div_n = p.N > 1 ? ~0ull / p.N + 1 : 0;
+    const int64_t plane = q.rows * p.Hq * d;
+    q.hi = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(c.workspace) + part_bytes(d));
+    q.lo = two ? q.hi + plane : nullptr;
+    q.factor = reinterpret_cast<float*>(q.hi + plane * (two ? 2 : 1));
+    q.freqs = c.freqs;
+    const int places = kQueryThreads / (d / 16);
+    q.rb_log2 = 0;
+    while ((places >> q.rb_log2) > p.Hq) ++q.rb_log2;
+    void (*kern)(PagedQueryParams);
+    if (q4)
+      kern = d == 128 ? (two ? attend_query_kernel<128, true, true> : attend_query_kernel<128, true, false>)
+                      : (two ? attend_query_kernel<64, true, true> : attend_query_kernel<64, true, false>);
+    else
+      kern = d == 128 ? attend_query_kernel<128, false, true> : attend_query_kernel<64, false, true>;
+    const cudaError_t e = launch_pdl<PagedQueryParams>(
+        kern, dim3(static_cast<unsigned>((q.rows + (1 << q.rb_log2) - 1) >> q.rb_log2)), kQueryThreads,
+        two ? (d / 2 * sizeof(float4)) << q.rb_log2 : 0, stream, q);
+    if (e != cudaSuccess) return e;
+    p.q = reinterpret_cast<const __nv_bfloat16*>(q.hi);
+    p.q_sn = d, p.q_sh = (int64_t)p.N * d, p.q_sb = (int64_t)p.Hq * p.N * d;
+    p.q_lo = plane;
+    p.factor = q.factor;
+  }
+  if (q4) {
+    if (d == 128) return two ? launch<128, true, true>(p, stream) : launch<128, true, false>(p, stream);
+    return two ? launch<64, true, true>(p, stream) : launch<64, true, false>(p, stream);
+  }
+  if (d == 128) return two ? launch<128, false, true>(p, stream) : launch<128, false, false>(p, stream);
+  return two ? launch<64, false, true>(p, stream) : launch<64, false, false>(p, stream);
 }
 
 }  // namespace afx
