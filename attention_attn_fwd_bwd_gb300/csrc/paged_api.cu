@@ -479,8 +479,8 @@ attnfuse_status attnfuse_paged_attend(const attnfuse_paged_cache* cache, const v
   call.rope = mode == ATTNFUSE_ROPE_FUSED;
   if (call.rope) call.freqs = paged_freqs(cache->d, rope_theta);
   call.workspace = workspace;
+  p.frag_rows = std::gcd(cache->page_size, kAttendTile);
   if (cache->format == ATTNFUSE_CACHE_BF16) {
-    p.frag_rows = std::gcd(cache->page_size, kAttendTile);
     auto map = [&](CUtensorMap* m, const void* pool, const int64_t* st, const char* name, int rows) {
       return encode_map_bhnd(m, pool, st, cache->num_pages, cache->Hkv, cache->page_size, cache->d, name, rows);
     };

@@ -10,7 +10,7 @@
 // The units of the whole batch, ordered by (sequence, KV head, rows), are dealt to the CTAs, one on each SM, in
 // equal runs of keys, from lengths read on the device. A unit that a run's end cuts leaves (max,
 // sum, acc) of its parts in the workspace, at most two per CTA, and a second kernel joins them in a
-// fixed order; it also writes the rows of padding.
+// fixed order.
 //
 // CTA. tcgen05 products: S_s = Q_s K^T of row tile s = 0, 1 in tensor memory, a softmax warpgroup
 // for each, one row per thread, which writes its weights as bf16 over S_s, and O_s += P_s V with P_s
@@ -19,8 +19,9 @@
 // memory, TMA boxes of a page's rows (bf16) or codes expanded by a warpgroup (4 bits).
 // TMEM (512 columns): S_0 [0, 128), S_1 [128, 256), O_0 [256, 384), O_1 [384, 512); P_s over S_s.
 //
-// Keys of a 4-bit cache are s_g c (8 and 3 bits): exact in fp16 under a power of two of their own
-// key, which multiplies the score; q enters as fp16 under a power of two of its row. A rotated q is two 16-bit parts.
+// Keys of a 4-bit cache are s_g c (8 and 3 bits): exact in fp16 under a power of two of the tile's
+// largest step, for steps down to 2^-28 of it (and off by at most 2^-36 of it below); q enters as fp16
+// under a power of two of its row. A rotated q is two 16-bit parts.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -46,14 +47,18 @@ struct Cfg {
   static constexpr int PANELS = D / 64;
   static constexpr uint32_t TILE = kTile * D * 2;                  // bytes of a K, V or Q tile
   static constexpr uint32_t QSLOT = TILE * (TWO ? 2 : 1);
-  static constexpr int STAGES = D == 64 ? 6 : TWO ? 3 : Q4 ? 4 : 5;
+  static constexpr int STAGES = D == 64 ? 6 : TWO ? (Q4 ? 2 : 3) : Q4 ? 4 : 5;
   // key tiles whose notes (factors, bad pages) may be in use at once: of the ring's tiles, those
   // behind the one whose V is still held by a softmax that reads them
-  static constexpr int NOTES = STAGES == 3 ? 2 : 4;
+  static constexpr int NOTES = STAGES <= 3 ? 2 : 4;
+  // 4 bits: K or V of a tile as the cache has it, codes and then steps
+  static constexpr uint32_t CODES = kTile * (D / 2), RAW = CODES + kTile * (D / 16);
+  static constexpr int RAWS = !Q4 ? 0 : D == 64 ? 6 : 3;
   static constexpr uint32_t OFF_KV = 2 * QSLOT;
-  static constexpr uint32_t OFF_CTL = OFF_KV + STAGES * TILE;
+  static constexpr uint32_t OFF_RAW = OFF_KV + STAGES * TILE;
+  static constexpr uint32_t OFF_CTL = OFF_RAW + RAWS * RAW;
   // registers of the warpgroups: producer, issuer and query loaders; softmax; expanders
-  static constexpr uint32_t LOW = Q4 ? 56 : 88, SM = Q4 ? 184 : 208, EXP = 88;
+  static constexpr uint32_t LOW = Q4 ? 80 : 104, SM = Q4 ? 168 : 200, EXP = 96;
   static_assert(LOW + 2 * SM + (Q4 ? EXP : 0) <= (WARPS / 4) * (65536 / THREADS / 8 * 8), "registers of the launch");
 };
 
@@ -61,23 +66,6 @@ struct Cfg {
 struct Pos {
   int b, kvh, r, t;
 };
-
-template <int NOTES, bool Q4>
-struct Ctl {
-  uint64_t q_full[2], q_empty[2], kv_full[6], kv_empty[6], s_full[2], p_full[2], o_full[2], last;
-  uint32_t tmem_base;
-  int abort_flag;
-  Pos begin, end;
-  int64_t wsum[16];
-  uint64_t bad[NOTES];                   // a byte for each 16 keys: on a page that is none
-  float factor[Q4 ? NOTES : 1][Q4 ? kTile : 1];
-};
-
-template <int D, bool Q4, bool TWO>
-constexpr size_t smem_bytes() {
-  using C = Cfg<D, Q4, TWO>;
-  return 1024 + C::OFF_CTL + sizeof(Ctl<C::NOTES, Q4>);
-}
 
 // ---------------------------------------------------------------------------------------------
 // Work: starts and counts -> units -> this CTA's run
@@ -206,50 +194,89 @@ struct Seg {
   int part;                  // -1: the whole unit, else which of the CTA's two partial results it is
 };
 
+// Steps through a run's segments; a converged warp calls it. The state and the segment lie in shared
+// memory, a copy for each warp, for the softmax has no registers to spare.
+struct WalkState {
+  Pos at;
+  int first, count, units, done;
+  Seg seg;
+};
 struct Walk {
   const PagedAttendWork& p;
-  Pos at, end;
-  Chunk c;
-  int units;
-  bool done;
-  __device__ Walk(const PagedAttendWork& p_, Pos begin, Pos end_) : p(p_), at(begin), end(end_), c{}, units(0), done(begin.b >= p_.cache.B) {
-    if (!done) enter();
-  }
-  __device__ bool next(Seg& s) {
-    while (!done) {
-      const Span w = span_of(p, c, at.r);
-      const bool stop = at.b == end.b && at.kvh == end.kvh && at.r == end.r;
-      const int t0 = at.t, t1 = stop ? end.t : w.nt;
-      s.b = at.b, s.kvh = at.kvh, s.row0 = at.r * kRows, s.rows = c.count * p.g;
-      s.first = c.first, s.lo = w.lo, s.hi = w.hi;
-      s.t = w.t0 + t0, s.n = t1 - t0;
-      s.part = t0 > 0 ? 0 : t1 < w.nt ? 1 : -1;
-      done = stop;
-      at.t = 0;
-      if (!done && ++at.r == units) {
-        at.r = 0;
-        if (++at.kvh == p.cache.Hkv) {
-          at.kvh = 0;
-          do {
-            if (++at.b >= p.cache.B) {
-              done = true;
-              break;
-            }
-            enter();
-          } while (c.count == 0);
-        }
-      }
-      if (s.n > 0) return true;
+  const Pos& end;
+  WalkState* st;
+  __device__ Walk(const PagedAttendWork& p_, const Pos& begin, const Pos& end_, WalkState* st_) : p(p_), end(end_), st(st_) {
+    if (threadIdx.x % 32 == 0) {
+      st->at = begin;
+      st->done = begin.b >= p.cache.B;
+      if (!st->done) enter(chunk_of(p, begin.b));
     }
-    return false;
+    __syncwarp();
+  }
+  // The next segment, or null. It stays until the next call.
+  __device__ __forceinline__ const Seg* next() {
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) step();
+    __syncwarp();
+    return st->seg.n > 0 ? &st->seg : nullptr;
   }
 
  private:
-  __device__ void enter() {
-    c = chunk_of(p, at.b);
-    units = units_of(p, c);
+  __device__ __forceinline__ void enter(const Chunk& c) {
+    st->first = c.first, st->count = c.count;
+    st->units = units_of(p, c);
+  }
+  __device__ __forceinline__ void step() {
+    Seg& s = st->seg;
+    s.n = 0;
+    while (!st->done) {
+      const Pos at = st->at;
+      const Chunk c = {st->first, st->count, false};
+      const Span w = span_of(p, c, at.r);
+      const bool stop = at.b == end.b && at.kvh == end.kvh && at.r == end.r;
+      const int t1 = stop ? end.t : w.nt;
+      s.b = at.b, s.kvh = at.kvh, s.row0 = at.r * kRows, s.rows = c.count * p.g;
+      s.first = c.first, s.lo = w.lo, s.hi = w.hi;
+      s.t = w.t0 + at.t, s.n = max(0, t1 - at.t);
+      s.part = at.t > 0 ? 0 : t1 < w.nt ? 1 : -1;
+      st->done = stop;
+      st->at.t = 0;
+      if (!stop && (st->at.r = at.r + 1) == st->units) {
+        st->at.r = 0;
+        if ((st->at.kvh = at.kvh + 1) == p.cache.Hkv) {
+          st->at.kvh = 0;
+          int b = at.b + 1;
+          Chunk next = {};
+          while (b < p.cache.B && (next = chunk_of(p, b)).count == 0) ++b;
+          st->at.b = b;
+          if (b < p.cache.B) enter(next);
+          else st->done = 1;
+        }
+      }
+      if (s.n > 0) return;
+    }
   }
 };
+
+template <int NOTES, bool Q4>
+struct Ctl {
+  uint64_t q_full[2], q_empty[2], kv_full[6], kv_empty[6], s_full[2], p_full[2], o_full[2], last;
+  uint64_t raw_full[Q4 ? 6 : 1], raw_empty[Q4 ? 6 : 1], raw_bad[Q4 ? 6 : 1];
+  uint32_t tmem_base;
+  int abort_flag;
+  Pos begin, end;
+  WalkState walk[Q4 ? 16 : 12];
+  int64_t wsum[16];
+  uint64_t bad[NOTES];                   // a byte for each 16 keys: on a page that is none
+  float factor[NOTES];                   // 4 bits: what the tile's scores are to be multiplied by
+  uint32_t most[2][4];                   // its largest step, by expanding warp
+};
+
+template <int D, bool Q4, bool TWO>
+constexpr size_t smem_bytes() {
+  using C = Cfg<D, Q4, TWO>;
+  return 1024 + C::OFF_CTL + sizeof(Ctl<C::NOTES, Q4>);
+}
 
 // ---------------------------------------------------------------------------------------------
 // Producer of bf16 tiles (one warp)
@@ -267,8 +294,9 @@ __device__ __forceinline__ void produce(const PagedAttendParams& p, uint8_t* sme
   auto lookup = [&](int b, int key, int* slot) {
     return page_at(cache, b, key, slot);
   };
-  Seg s;
-  while (ok && w.next(s)) {
+  const Seg* seg;
+  while (ok && (seg = w.next())) {
+    const Seg& s = *seg;
     for (int i = 0; ok && i < s.n; ++i, ++tiles) {
       const int k0 = (s.t + i) * kTile;
       const int key = k0 + lane / C::PANELS * frag;
@@ -340,137 +368,189 @@ __device__ __forceinline__ void produce(const PagedAttendParams& p, uint8_t* sme
 }
 
 // ---------------------------------------------------------------------------------------------
-// Expanders of 4-bit tiles (four warps): a thread takes a key
+// 4-bit tiles: a producer (one warp) copies codes and steps to shared memory, expanders (four warps,
+// a thread takes a key) write them to the ring as 16-bit values
 // ---------------------------------------------------------------------------------------------
-// Four codes (the low 16 bits of w) times a step: fp16 (F16) or bf16 pairs.
-template <bool F16>
-__device__ __forceinline__ uint2 expand4(uint32_t w, uint32_t step2) {
-  // 1024 + n in fp16, 128 + n in bf16; less 1024 + 8 and 128 + 8; times the step
-  constexpr uint32_t kMagic = F16 ? 0x64006400u : 0x43004300u, kOff = F16 ? 0x64086408u : 0x43084308u;
-  const uint32_t a = (w & 0xFu) | ((w << 12) & 0xF0000u) | kMagic;
-  const uint32_t b = ((w >> 8) & 0xFu) | ((w << 4) & 0xF0000u) | kMagic;
-  uint2 r;
-  if constexpr (F16) {
-    asm("{\n\t.reg .b32 t;\n\tsub.rn.f16x2 t, %1, %2;\n\tmul.rn.f16x2 %0, t, %3;\n\t}" : "=r"(r.x) : "r"(a), "r"(kOff), "r"(step2));
-    asm("{\n\t.reg .b32 t;\n\tsub.rn.f16x2 t, %1, %2;\n\tmul.rn.f16x2 %0, t, %3;\n\t}" : "=r"(r.y) : "r"(b), "r"(kOff), "r"(step2));
-  } else {
-    asm("{\n\t.reg .b32 t;\n\tsub.rn.bf16x2 t, %1, %2;\n\tmul.rn.bf16x2 %0, t, %3;\n\t}" : "=r"(r.x) : "r"(a), "r"(kOff), "r"(step2));
-    asm("{\n\t.reg .b32 t;\n\tsub.rn.bf16x2 t, %1, %2;\n\tmul.rn.bf16x2 %0, t, %3;\n\t}" : "=r"(r.y) : "r"(b), "r"(kOff), "r"(step2));
-  }
-  return r;
+__device__ __forceinline__ void bulk_load(uint8_t* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 
-template <int D>
-struct Row4 {
-  uint4 c[D / 32];           // codes, halves swapped back
-  uint32_t s[D / 64];        // steps, two in each
-};
-template <int D>
-__device__ __forceinline__ void load_row4(Row4<D>& r, const uint8_t* codes, const uint8_t* steps, int slot) {
-  const int swap = D == 128 ? slot & 2 : 0;
+template <int D, class C, class T>
+__device__ __forceinline__ void produce4(const PagedAttendParams& p, uint8_t* smem, T* ctl, Walk w) {
+  const int lane = threadIdx.x % 32;
+  volatile int* abort_flag = &ctl->abort_flag;
+  const PagedDev& cache = p.cache;
+  const int frag = p.frag_rows, frags = kTile / frag;
+  int it = 0;
+  bool ok = true;
+  const Seg* seg;
+  while (ok && (seg = w.next())) {
+    const Seg& s = *seg;
+    for (int i = 0; ok && i < s.n; ++i) {
+      const int key = (s.t + i) * kTile + lane * frag;
+      const bool seen = lane < frags && key < s.hi && key + frag > s.lo;
+      int slot = 0, page = -1;
+      if (seen) page = page_at(cache, s.b, key, &slot);
+      const uint32_t none = __ballot_sync(0xffffffffu, seen && page < 0), loads = __ballot_sync(0xffffffffu, page >= 0);
+      if (none && lane == 0) atomicOr(p.status, kDevPageRange);
 #pragma unroll
-  for (int m = 0; m < D / 32; ++m)
-    r.c[m] = __ldg(reinterpret_cast<const uint4*>(codes + static_cast<int64_t>(slot) * (D / 2)) + (m ^ swap));
-  if constexpr (D == 128) {
-    const uint2 s = __ldg(reinterpret_cast<const uint2*>(steps + static_cast<int64_t>(slot) * 8));
-    r.s[0] = s.x, r.s[1] = s.y;
-  } else {
-    r.s[0] = __ldg(reinterpret_cast<const uint32_t*>(steps + static_cast<int64_t>(slot) * 4));
-  }
-}
-// Expands a row into a tile (128-byte swizzle, panels of 64 elements); steps: the pair of a group.
-template <int D, bool F16>
-__device__ __forceinline__ void store_row4(const Row4<D>& r, const uint32_t (&step2)[D / 32], uint8_t* tile, int row) {
-#pragma unroll
-  for (int m = 0; m < D / 32; ++m)
-#pragma unroll
-    for (int g = 0; g < D / 32; ++g) {
-      // d = 128: 16 bytes are two chunks of four groups' words; d = 64: four chunks of two
-#pragma unroll
-      for (int q = 0; q < (D == 128 ? 1 : 2); ++q) {
-        const uint32_t even = D == 128 ? (g < 2 ? r.c[m].x : r.c[m].y) : (q == 0 ? r.c[m].x : r.c[m].z);
-        const uint32_t odd = D == 128 ? (g < 2 ? r.c[m].z : r.c[m].w) : (q == 0 ? r.c[m].y : r.c[m].w);
-        const uint2 x = expand4<F16>((g & 1) ? even >> 16 : even, step2[g]);
-        const uint2 y = expand4<F16>((g & 1) ? odd >> 16 : odd, step2[g]);
-        const int chunk = 4 * g + (D == 128 ? m : 2 * m + q);
-        *reinterpret_cast<uint4*>(tile + (chunk >> 3) * (kTile * 128) + sw128_offset(row, chunk & 7)) = make_uint4(x.x, x.y, y.x, y.y);
+      for (int v = 0; v < 2; ++v, ++it) {
+        const int st = it % C::RAWS;
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&ctl->raw_empty[st], ((it / C::RAWS) & 1) ^ 1, p.status, abort_flag));
+        if (!ok) break;
+        if (lane == 0) {
+          uint64_t bad = 0;
+          for (uint32_t m = none; m; m &= m - 1)
+            for (int x = 0; x < frag / 16; ++x) bad |= 0xFFull << (8 * ((__ffs(m) - 1) * (frag / 16) + x));
+          ctl->raw_bad[st] = bad;
+          mbar_arrive_expect_tx(&ctl->raw_full[st], __popc(loads) * frag * (D / 2 + D / 16));
+        }
+        __syncwarp();
+        if (page >= 0) {
+          uint8_t* dst = smem + C::OFF_RAW + st * C::RAW;
+          const uint8_t* codes = v ? cache.v + page * cache.v_sp + s.kvh * cache.v_sh : cache.k + page * cache.k_sp + s.kvh * cache.k_sh;
+          const uint8_t* steps = v ? cache.vs + page * cache.vs_sp + s.kvh * cache.vs_sh : cache.ks + page * cache.ks_sp + s.kvh * cache.ks_sh;
+          bulk_load(dst + lane * frag * (D / 2), codes + static_cast<int64_t>(slot) * (D / 2), frag * (D / 2), &ctl->raw_full[st]);
+          bulk_load(dst + C::CODES + lane * frag * (D / 16), steps + static_cast<int64_t>(slot) * (D / 16), frag * (D / 16),
+                    &ctl->raw_full[st]);
+        }
       }
     }
+  }
+  // no copy may be in flight when the CTA ends
+  for (int i = max(0, it - C::RAWS); i < it; ++i) mbar_wait(&ctl->raw_full[i % C::RAWS], (i / C::RAWS) & 1, p.status, nullptr);
+}
+
+// Eight elements of each of two groups, from a word of four codes of both for the first four and one
+// for the last: fp16 (F16) or bf16 pairs, times the groups' steps (a pair). Codes of the two groups are
+// handled in pairs, as they lie, and sorted at the end.
+template <bool F16>
+__device__ __forceinline__ void expand8(uint32_t first, uint32_t last, uint32_t step2, uint4& g0, uint4& g1) {
+  uint32_t y[2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w = i ? last : first;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t c;
+      if constexpr (F16) {
+        // 1024 + n, or 1024 + 16 n times 1/16, less what makes it n - 8: all exact
+        const uint32_t u = e < 2 ? w : w >> 8;
+        if (e & 1) {
+          const uint32_t x = (u & 0x00F000F0u) | 0x64006400u;
+          asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(c) : "r"(x), "r"(0x2C002C00u), "r"(0xD480D480u));
+        } else {
+          const uint32_t x = (u & 0x000F000Fu) | 0x64006400u;
+          asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(c) : "r"(x), "r"(0x64086408u));
+        }
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[i][e]) : "r"(c), "r"(step2));
+      } else {
+        const uint32_t x = ((w >> (4 * e)) & 0x000F000Fu) | 0x43004300u;  // 128 + n
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(x), "r"(0x43084308u));
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y[i][e]) : "r"(c), "r"(step2));
+      }
+    }
+  }
+  g0 = make_uint4(__byte_perm(y[0][0], y[0][1], 0x5410), __byte_perm(y[0][2], y[0][3], 0x5410),
+                  __byte_perm(y[1][0], y[1][1], 0x5410), __byte_perm(y[1][2], y[1][3], 0x5410));
+  g1 = make_uint4(__byte_perm(y[0][0], y[0][1], 0x7632), __byte_perm(y[0][2], y[0][3], 0x7632),
+                  __byte_perm(y[1][0], y[1][1], 0x7632), __byte_perm(y[1][2], y[1][3], 0x7632));
+}
+
+// Expands row `row` of a copied tile into a tile of the ring (128-byte swizzle, panels of 64
+// elements). Rows take their 16-byte pieces in different orders, so that neither the loads nor
+// the stores of eight rows meet in a bank.
+template <int D, bool F16>
+__device__ __forceinline__ void expand_row(const uint8_t* raw, const uint32_t (&step2)[D / 64], uint8_t* tile, int row) {
+  const int turn = D == 128 ? (row & 2) | ((row >> 2) & 1) : (row >> 2) & 1;
+#pragma unroll 2
+  for (int j = 0; j < D / 32; ++j) {
+    const int at = j ^ turn;
+    const uint4 c = *reinterpret_cast<const uint4*>(raw + row * (D / 2) + at * 16);
+    uint4 g0, g1;
+    auto put = [&](int chunk, const uint4& x) {
+      *reinterpret_cast<uint4*>(tile + (chunk >> 3) * (kTile * 128) + sw128_offset(row, chunk & 7)) = x;
+    };
+    if constexpr (D == 128) {
+      // two chunks of four groups; slots (as rows: pages are multiples of 16) with bit 1 have their halves swapped
+      const int m = at ^ (row & 2);
+      expand8<F16>(c.x, c.z, step2[0], g0, g1);
+      put(m, g0), put(4 + m, g1);
+      expand8<F16>(c.y, c.w, step2[1], g0, g1);
+      put(8 + m, g0), put(12 + m, g1);
+    } else {
+      // four chunks of two groups
+      expand8<F16>(c.x, c.y, step2[0], g0, g1);
+      put(2 * at, g0), put(4 + 2 * at, g1);
+      expand8<F16>(c.z, c.w, step2[0], g0, g1);
+      put(2 * at + 1, g0), put(5 + 2 * at, g1);
+    }
+  }
 }
 
 template <int D, class C, class T>
 __device__ __forceinline__ void expand(const PagedAttendParams& p, uint8_t* smem, T* ctl, Walk w) {
   const int row = threadIdx.x % 128, lane = threadIdx.x % 32;
   volatile int* abort_flag = &ctl->abort_flag;
-  const PagedDev& cache = p.cache;
   int it = 0, tiles = 0;
   bool ok = true;
-  Seg s;
-  while (ok && w.next(s)) {
-    const uint8_t* const pool[2] = {cache.k + s.kvh * cache.k_sh, cache.v + s.kvh * cache.v_sh};
-    const uint8_t* const steps[2] = {cache.ks + s.kvh * cache.ks_sh, cache.vs + s.kvh * cache.vs_sh};
-    Row4<D> k, v;
-    int page;
-    bool seen;
-    auto load = [&](int i) {
+  const Seg* seg;
+  while (ok && (seg = w.next())) {
+    const Seg& s = *seg;
+    for (int i = 0; ok && i < s.n; ++i, ++tiles) {
       const int key = (s.t + i) * kTile + row;
-      seen = key >= s.lo && key < s.hi;
-      page = -1;
-      int slot = 0;
-      if (seen) page = page_at(cache, s.b, key, &slot);
 #pragma unroll
-      for (int m = 0; m < D / 32; ++m) k.c[m] = v.c[m] = make_uint4(0, 0, 0, 0);
+      for (int v = 0; v < 2; ++v, ++it) {
+        const int rs = it % C::RAWS, st = it % C::STAGES;
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&ctl->raw_full[rs], (it / C::RAWS) & 1, p.status, abort_flag) &&
+                                               mbar_wait(&ctl->kv_empty[st], ((it / C::STAGES) & 1) ^ 1, p.status, abort_flag));
+        if (!ok) break;
+        const uint8_t* raw = smem + C::OFF_RAW + rs * C::RAW;
+        uint8_t* tile = smem + C::OFF_KV + st * C::TILE;
+        const uint64_t bad = *reinterpret_cast<volatile uint64_t*>(&ctl->raw_bad[rs]);
+        // keys that no row sees, or without a page, are zeros (steps of 0, whatever lies there)
+        const bool seen = key >= s.lo && key < s.hi && !((bad >> (8 * (row / 16))) & 1);
+        uint32_t step2[D / 64];
 #pragma unroll
-      for (int m = 0; m < D / 64; ++m) k.s[m] = v.s[m] = 0;
-      if (page >= 0) {
-        load_row4<D>(k, pool[0] + page * cache.k_sp, steps[0] + page * cache.ks_sp, slot);
-        load_row4<D>(v, pool[1] + page * cache.v_sp, steps[1] + page * cache.vs_sp, slot);
-      }
-    };
-    load(0);
-    for (int i = 0; i < s.n; ++i, ++tiles) {
-      int st = it % C::STAGES;
-      ok = __all_sync(0xffffffffu, mbar_wait(&ctl->kv_empty[st], ((it / C::STAGES) & 1) ^ 1, p.status, abort_flag));
-      if (!ok) break;
-      const bool none = seen && page < 0;
-      if (__any_sync(0xffffffffu, none) && lane == 0) atomicOr(p.status, kDevPageRange);
-      if (row % 16 == 0) reinterpret_cast<uint8_t*>(&ctl->bad[tiles % C::NOTES])[row / 16] = none ? 0xFF : 0;
-      {
-        // steps under a power of two that takes the key's largest to [2^11, 2^12): products of 11
-        // bits at most, exact in fp16's normal range
-        uint32_t most = 0;
+        for (int g = 0; g < D / 64; ++g)
+          step2[g] = seen ? *reinterpret_cast<const uint32_t*>(raw + C::CODES + row * (D / 16) + g * 4) : 0u;
+        if (v == 0) {
+          // steps under a power of two that takes the tile's largest (finite) one to [2^11, 2^12):
+          // products of 11 bits at most, exact in fp16's normal range
+          uint32_t most = 0;
 #pragma unroll
-        for (int m = 0; m < D / 64; ++m) most = max(most, max(k.s[m] & 0x7FFFu, (k.s[m] >> 16) & 0x7FFFu));
-        const uint32_t e = max(most >> 7, 12u);
-        const float up = __uint_as_float((254u + 11u - e) << 23);
-        ctl->factor[tiles % C::NOTES][row] = __uint_as_float((e - 11u) << 23);
-        uint32_t step2[D / 32];
+          for (int g = 0; g < D / 64; ++g) {
+            const uint32_t a = step2[g] & 0x7FFFu, b = (step2[g] >> 16) & 0x7FFFu;
+            most = max(most, max(a < 0x7F80u ? a : 0u, b < 0x7F80u ? b : 0u));
+          }
+          most = __reduce_max_sync(0xffffffffu, most);
+          uint32_t(&all)[4] = ctl->most[tiles & 1];
+          if (lane == 0) all[row / 32] = most;
+          named_bar_sync(1, 128);
+          const uint32_t e = max(max(max(all[0], all[1]), max(all[2], all[3])) >> 7, 12u);
+          const float up = __uint_as_float((254u + 11u - e) << 23);
+          if (row == 0) {
+            ctl->factor[tiles % C::NOTES] = __uint_as_float((e - 11u) << 23);
+            ctl->bad[tiles % C::NOTES] = bad;
+          }
 #pragma unroll
-        for (int g = 0; g < D / 32; ++g) {
-          const float x = (g & 1) ? bf16hi_to_f32(k.s[g / 2]) : bf16lo_to_f32(k.s[g / 2]);
-          const __half2 h = __float2half2_rn(x * up);
-          step2[g] = *reinterpret_cast<const uint32_t*>(&h);
+          for (int g = 0; g < D / 64; ++g) {
+            const __half2 h = __floats2half2_rn(bf16lo_to_f32(step2[g]) * up, bf16hi_to_f32(step2[g]) * up);
+            step2[g] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          expand_row<D, true>(raw, step2, tile, row);
+        } else {
+          expand_row<D, false>(raw, step2, tile, row);
         }
-        store_row4<D, true>(k, step2, smem + C::OFF_KV + st * C::TILE, row);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&ctl->kv_full[st]);
+          mbar_arrive(&ctl->raw_empty[rs]);
+        }
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->kv_full[st]);
-      ++it;
-      st = it % C::STAGES;
-      ok = __all_sync(0xffffffffu, mbar_wait(&ctl->kv_empty[st], ((it / C::STAGES) & 1) ^ 1, p.status, abort_flag));
-      if (!ok) break;
-      {
-        uint32_t step2[D / 32];
-#pragma unroll
-        for (int g = 0; g < D / 32; ++g) step2[g] = __byte_perm(v.s[g / 2], 0, (g & 1) ? 0x3232 : 0x1010);
-        store_row4<D, false>(v, step2, smem + C::OFF_KV + st * C::TILE, row);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->kv_full[st]);
-      ++it;
-      if (i + 1 < s.n) load(i + 1);
     }
   }
 }
@@ -490,8 +570,9 @@ __device__ __forceinline__ void load_queries(const PagedAttendParams& p, uint8_t
   volatile int* abort_flag = &ctl->abort_flag;
   int used[2] = {0, 0};
   bool ok = true;
-  Seg s;
-  while (ok && w.next(s)) {
+  const Seg* seg;
+  while (ok && (seg = w.next())) {
+    const Seg& s = *seg;
 #pragma unroll
     for (int slot = 0; slot < 2; ++slot) {
       const int r0 = s.row0 + 128 * slot;
@@ -501,13 +582,17 @@ __device__ __forceinline__ void load_queries(const PagedAttendParams& p, uint8_t
       ++used[slot];
       const uint32_t to = smem_u32(smem + slot * C::QSLOT) + (chunk >> 3) * (kTile * 128);
       const __nv_bfloat16* from = p.q + s.b * p.q_sb + static_cast<int64_t>(s.kvh) * p.g * p.q_sh + chunk * 8;
-      for (int r = tid / CH; r < 128; r += 64 / CH) {
+      constexpr int STEP = 64 / CH;
+      const int g = p.g, dn = STEP / g, dj = STEP - dn * g, last = s.rows - r0;  // rows behind the last are not used
+      int n = (r0 + tid / CH) / g, j = r0 + tid / CH - n * g;
+#pragma unroll 4
+      for (int r = tid / CH; r < min(128, last); r += STEP) {
         const uint32_t dst = to + sw128_offset(r, chunk & 7);
-        const uint32_t row = min(r0 + r, s.rows - 1);  // rows behind the last are not used
-        const uint32_t n = row / static_cast<uint32_t>(p.g), j = row - n * p.g;
         const __nv_bfloat16* x = from + n * p.q_sn + j * p.q_sh;
         cp_async16(dst, x);
         if (TWO) cp_async16(dst + C::TILE, x + p.q_lo);
+        n += dn, j += dj;
+        if (j >= g) j -= g, ++n;
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
@@ -515,85 +600,103 @@ __device__ __forceinline__ void load_queries(const PagedAttendParams& p, uint8_t
       if (lane == 0) mbar_arrive(&ctl->q_full[slot]);
     }
   }
+  // then, while the last products run, padding: rows [count, N) of every head. CTAs of one number
+  // modulo `groups` share sequences.
+  const int B = p.cache.B, groups = min(B, p.ctas), cta = blockIdx.x;
+  for (int b = cta % groups; b < B; b += groups) {
+    const int count = chunk_of(p, b).count, rows = p.N - count;
+    const int64_t pieces = static_cast<int64_t>(rows) * p.Hq * CH;
+    const int64_t step = static_cast<int64_t>((p.ctas - cta % groups + groups - 1) / groups) * 64;
+    for (int64_t i = static_cast<int64_t>(cta / groups) * 64 + tid; i < pieces; i += step) {
+      const uint32_t row = static_cast<uint32_t>(i / CH);  // below N Hq
+      const uint32_t h = row / static_cast<uint32_t>(rows), n = count + (row - h * rows);
+      __stcs(reinterpret_cast<uint4*>(p.out + b * p.o_sb + h * p.o_sh + n * p.o_sn + i % CH * 8), make_uint4(0, 0, 0, 0));
+      if (p.lse && i % CH == 0) p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.N + n] = kNegInf;
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------------------------
-// Issuer of the products (one thread)
+// Issuer of the products (one warp, converged, so that descriptors stay in uniform registers: one
+// thread alone took 100 cycles to issue a product of 64)
 // ---------------------------------------------------------------------------------------------
 template <int D, bool Q4, bool TWO, class C, class T>
 __device__ __forceinline__ void issue(const PagedAttendParams& p, uint8_t* smem, T* ctl, Walk w, uint32_t tmem) {
   constexpr uint32_t idesc_s = idesc_f32acc(128, 128, 0, 0, Q4), idesc_o = idesc_f32acc(128, D, 0, 1);
   volatile int* abort_flag = &ctl->abort_flag;
   int* status = p.status;
-  const uint32_t sQ = smem_u32(smem), sKV = smem_u32(smem + C::OFF_KV);
-  int qu[2] = {0, 0}, pu[2] = {0, 0};
+  // descriptors as a low word, to which a product's place in the tile adds a constant, and one high word
+  static_assert(smem_bytes<D, Q4, TWO>() < (1u << 18), "descriptor address field");
+  constexpr uint32_t dhi = desc_sw128_hi(1024);
+  const uint32_t dQ = desc_sw128_lo(smem_u32(smem), 16), dK = desc_sw128_lo(smem_u32(smem + C::OFF_KV), 16);
+  const uint32_t dV = desc_sw128_lo(smem_u32(smem + C::OFF_KV), kTile * 128);
+  uint32_t phases = 0;  // bit s: of q_full[s], bit 2 + s: of p_full[s]
   bool ok = true;
-  auto wait_tile = [&](int it) {
-    ok = ok && mbar_wait(&ctl->kv_full[it % C::STAGES], (it / C::STAGES) & 1, status, abort_flag);
+  auto wait = [&](uint64_t* bar, int parity) {
+    ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, status, abort_flag));
   };
+  auto wait_tile = [&](int it) { wait(&ctl->kv_full[it % C::STAGES], (it / C::STAGES) & 1); };
   auto scores = [&](int s, int it, bool first, bool last) {
-    if (first) ok = ok && mbar_wait(&ctl->q_full[s], qu[s]++ & 1, status, abort_flag);
+    if (first) {
+      wait(&ctl->q_full[s], (phases >> s) & 1);
+      phases ^= 1u << s;
+    }
     if (!ok) return;
     tc_fence_after();
-    const uint32_t k = sKV + (it % C::STAGES) * C::TILE;
+    const uint32_t q = dQ + s * (C::QSLOT >> 4), k = dK + (it % C::STAGES) * (C::TILE >> 4);
+    mma_ss_warp<0>(tmem + 128 * s, q, k, dhi, idesc_s);
 #pragma unroll
-    for (int part = 0; part < (TWO ? 2 : 1); ++part)
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
-        mma_ss(tmem + 128 * s, smem_desc_sw128(sQ + s * C::QSLOT + part * C::TILE + off, 16, 1024), smem_desc_sw128(k + off, 16, 1024),
-               idesc_s, part > 0 || kk > 0);
-      }
-    mma_commit(&ctl->s_full[s]);
-    if (last) mma_commit(&ctl->q_empty[s]);
+    for (int kk = 1; kk < (TWO ? 2 : 1) * (D / 16); ++kk) {
+      const uint32_t off = ((kk % (D / 16)) >> 2) * (kTile * 128) + (kk & 3) * 32;
+      mma_ss_warp<1>(tmem + 128 * s, q + (((kk / (D / 16)) * C::TILE + off) >> 4), k + (off >> 4), dhi, idesc_s);
+    }
+    mma_commit_warp(&ctl->s_full[s]);
+    if (last) mma_commit_warp(&ctl->q_empty[s]);
   };
   auto values = [&](int s, int it, bool first, bool last) {
-    ok = ok && mbar_wait(&ctl->p_full[s], pu[s]++ & 1, status, abort_flag);
+    wait(&ctl->p_full[s], (phases >> (2 + s)) & 1);
+    phases ^= 4u << s;
     if (!ok) return;
     tc_fence_after();
-    const uint32_t v = sKV + (it % C::STAGES) * C::TILE;
+    const uint32_t v = dV + (it % C::STAGES) * (C::TILE >> 4), o = tmem + 256 + 128 * s, w = tmem + 128 * s;
+    if (first) mma_ts_warp<0>(o, w, v, dhi, idesc_o);
+    else mma_ts_warp<1>(o, w, v, dhi, idesc_o);
 #pragma unroll
-    for (int kk = 0; kk < kTile / 16; ++kk)
-      mma_ts(tmem + 256 + 128 * s, tmem + 128 * s + kk * 8, smem_desc_sw128(v + kk * 2048, kTile * 128, 1024), idesc_o, !first || kk > 0);
-    if (last) mma_commit(&ctl->o_full[s]);
+    for (int kk = 1; kk < kTile / 16; ++kk) mma_ts_warp<1>(o, w + kk * 8, v + kk * (2048 >> 4), dhi, idesc_o);
+    if (last) mma_commit_warp(&ctl->o_full[s]);
   };
-  Seg cur, nxt;
-  bool have = w.next(nxt);
-  int ci = 0, ni = 0, it = 0;  // tile of the segment, ring index of the tile's K
-  bool act[2] = {true, false}, nact[2] = {true, false};
-  if (have) {
-    nact[1] = nxt.row0 + 128 < nxt.rows;
-    wait_tile(0);
-    for (int s = 0; s < 2; ++s)
-      if (nact[s]) scores(s, 0, true, nxt.n == 1);
-    if (ok) mma_commit(&ctl->kv_empty[0]);
-  }
-  while (ok && have) {
-    cur = nxt, ci = ni;
-    act[1] = nact[1];
-    const bool first = ci == 0, last = ci == cur.n - 1;
-    if (last) {
-      have = w.next(nxt);
-      ni = 0;
-      if (have) nact[1] = nxt.row0 + 128 < nxt.rows;
-    } else {
-      ++ni;
-    }
-    const int vt = it + 1, kt = it + 2;
-    wait_tile(vt);
-    for (int s = 0; s < 2 && ok; ++s) {
-      if (act[s]) values(s, vt, first, last);
-      if (s == 1 || !act[1]) {
-        if (ok && (s == 0 || act[1])) mma_commit(&ctl->kv_empty[vt % C::STAGES]);
-      }
+  // the next segment's tiles and whether it has a second row tile; false: there is none
+  auto next = [&](int* n, bool* two) {
+    const Seg* s = w.next();
+    *n = __shfl_sync(0xffffffffu, s ? s->n : 0, 0);
+    *two = __any_sync(0xffffffffu, s && s->row0 + 128 < s->rows);
+    return __any_sync(0xffffffffu, s != nullptr) != 0;
+  };
+  // Step: the values' products of a tile and the scores' of the next one, row tile by row tile.
+  int cn = 0, nn = 0, ci = 0, ni = 0, vt = -1;  // tiles of their segments, the tiles' numbers, ring index of V
+  bool act1 = false, nact1 = false, cur = false;
+  bool have = next(&nn, &nact1);
+  while (ok && (cur || have)) {
+    const bool first = ci == 0, last = ci == cn - 1, nfirst = ni == 0, nlast = ni == nn - 1;
+    const int kt = vt + 1;
+    if (cur) wait_tile(vt);
+#pragma unroll 1
+    for (int s = 0; s < 2; ++s) {
+      if (cur && (s == 0 || act1)) values(s, vt, first, last);
+      if (cur && s == act1 && ok) mma_commit_warp(&ctl->kv_empty[vt % C::STAGES]);
       if (have && s == 0) wait_tile(kt);
-      if (have && nact[s] && ok) scores(s, kt, ni == 0, ni == nxt.n - 1);
+      if (have && (s == 0 || nact1)) scores(s, kt, nfirst, nlast);
     }
-    if (ok && have) mma_commit(&ctl->kv_empty[kt % C::STAGES]);
-    it = kt;
+    if (have && ok) mma_commit_warp(&ctl->kv_empty[kt % C::STAGES]);
+    cur = have, cn = nn, ci = ni, act1 = nact1;
+    vt += 2;
+    if (have && ++ni == nn) {
+      have = next(&nn, &nact1);
+      ni = 0;
+    }
   }
   // all products have ended before tensor memory is given back
-  mma_commit(&ctl->last);
+  mma_commit_warp(&ctl->last);
   mbar_wait(&ctl->last, 0, status, nullptr);
 }
 
@@ -609,8 +712,9 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
   const uint32_t tO = tS - 128 * slot + 256 + 128 * slot;
   int sc = 0, oc = 0, tiles = 0;
   bool ok = true;
-  Seg s;
-  while (ok && w.next(s)) {
+  const Seg* seg;
+  while (ok && (seg = w.next())) {
+    const Seg& s = *seg;
     if (s.row0 + 128 * slot >= s.rows) {
       tiles += s.n;
       continue;
@@ -630,55 +734,52 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
       if (!ok) break;
       ++sc;
       tc_fence_after();
-      uint32_t xr[128];
-      tmem_ld32<0>(tS, xr);
-      tmem_ld32<32>(tS + 32, xr);
-      tmem_ld32<64>(tS + 64, xr);
-      tmem_ld32<96>(tS + 96, xr);
       const uint64_t bad = *reinterpret_cast<volatile uint64_t*>(&ctl->bad[tiles % C::NOTES]);
-      tmem_wait_ld();
-      float x[128];
-#pragma unroll
-      for (int c = 0; c < 128; ++c) x[c] = __uint_as_float(xr[c]);
-      if constexpr (Q4) {
-        const float4* f = reinterpret_cast<const float4*>(ctl->factor[tiles % C::NOTES]);
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float4 y = f[c];
-          const uint64_t a = mul2(f2_pack(x[4 * c], x[4 * c + 1]), f2_pack(y.x, y.y));
-          const uint64_t b = mul2(f2_pack(x[4 * c + 2], x[4 * c + 3]), f2_pack(y.z, y.w));
-          x[4 * c] = f2_lo(a), x[4 * c + 1] = f2_hi(a), x[4 * c + 2] = f2_lo(b), x[4 * c + 3] = f2_hi(b);
-        }
-      }
+      float part = 1.f;  // of the scores: a power of two
+      if constexpr (Q4) part = *reinterpret_cast<volatile float*>(&ctl->factor[tiles % C::NOTES]);
       const int k0 = (s.t + i) * kTile;
-      float unit = mul;
-      if (p.slopes) {
-        const float base = slope * static_cast<float>(k0 - pos);
+      const float unit = p.slopes ? 1.f : mul * part;
+      const bool edge = k0 + kTile - 1 > pos || k0 < lo || bad != 0;
+      // Scores of columns 64 half .. of the row, masked, in units of 1 / unit. (Both passes over the tile
+      // read them again from tensor memory, in loops: all 128 at once, unrolled, take registers and
+      // instruction cache that the warps of five roles do not have.)
+      auto load = [&](int half, float (&x)[64]) {
+        uint32_t xr[64];
+        tmem_ld32<0>(tS + 64 * half, xr);
+        tmem_ld32<32>(tS + 64 * half + 32, xr);
+        tmem_wait_ld_dep(xr);
 #pragma unroll
-        for (int c = 0; c < 128; ++c) x[c] = __fmaf_rn(slope, static_cast<float>(c), __fmaf_rn(x[c], mul, base));
-        unit = 1.f;
+        for (int c = 0; c < 64; ++c) x[c] = __uint_as_float(xr[c]);
+        if (p.slopes) {
+          const float base = slope * static_cast<float>(k0 + 64 * half - pos);
+#pragma unroll
+          for (int c = 0; c < 64; ++c) x[c] = __fmaf_rn(slope, static_cast<float>(c), __fmaf_rn(x[c], mul * part, base));
+        }
+        if (__builtin_expect(edge, 0)) {
+          const int c0 = lo - k0 - 64 * half, c1 = pos - k0 - 64 * half;
+          const uint32_t gone = static_cast<uint32_t>(bad >> (32 * half));
+#pragma unroll
+          for (int c = 0; c < 64; ++c) x[c] = c >= c0 && c <= c1 && !((gone >> (8 * (c / 16))) & 1) ? x[c] : kNegInf;
+        }
+      };
+      float mx = kNegInf;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        float x[64], m[8];
+        load(half, x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m[k] = fmaxf(x[2 * k], x[2 * k + 1]);
+#pragma unroll
+        for (int j = 1; j < 4; ++j)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) m[k] = max3f(m[k], x[16 * j + 2 * k], x[16 * j + 2 * k + 1]);
+        mx = max3f(mx, max3f(m[0], m[1], m[2]), max3f(max3f(m[3], m[4], m[5]), m[6], m[7]));
       }
-      if (__builtin_expect(k0 + kTile - 1 > pos || k0 < lo, 0)) {
-        const int c0 = lo - k0, c1 = pos - k0;
-#pragma unroll
-        for (int c = 0; c < 128; ++c) x[c] = c >= c0 && c <= c1 ? x[c] : kNegInf;
-      }
-      if (__builtin_expect(bad != 0, 0)) {
-#pragma unroll
-        for (int c = 0; c < 128; ++c) x[c] = (bad >> (8 * (c / 16))) & 1 ? kNegInf : x[c];
-      }
-      float mp[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) mp[k] = fmaxf(x[2 * k], x[2 * k + 1]);
-#pragma unroll
-      for (int j = 1; j < 8; ++j)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mp[k] = max3f(mp[k], x[16 * j + 2 * k], x[16 * j + 2 * k + 1]);
-      const float mx = max3f(max3f(mp[0], mp[1], mp[2]), max3f(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7])) * unit;
+      mx *= unit;
       // O keeps its scale unless this tile exceeds it by more than 2^kLazy
       const float m_new = mx > m_run + kLazy ? mx : m_run;
       const bool grow = m_new > m_run && m_run != kNegInf;
-      if (__any_sync(0xffffffffu, grow)) {
+      if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
         // (the products of the tile before are complete: S of this one was issued behind them)
         const float alpha = grow ? ex2_approx(m_run - m_new) : 1.f;
         l_run *= alpha;
@@ -686,7 +787,7 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
         for (int ch = 0; ch < D / 32; ++ch) {
           uint32_t o[32];
           tmem_ld32(tO + ch * 32, o);
-          tmem_wait_ld();
+          tmem_wait_ld_dep(o);
 #pragma unroll
           for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
           tmem_st32(tO + ch * 32, o);
@@ -695,22 +796,23 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
       m_run = m_new;
       const float nb = m_new == kNegInf ? 0.f : -m_new;
       const uint64_t u2 = f2_pack(unit, unit), nb2 = f2_pack(nb, nb);
-      uint64_t acc2[4] = {0, 0, 0, 0};
+      uint64_t acc[2] = {0, 0};
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        float x[64];
+        load(half, x);
+        uint32_t pk[32];
 #pragma unroll
-      for (int ch = 0; ch < 4; ++ch) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const int e = 32 * ch + 2 * c;
-          const uint64_t a = fma2(f2_pack(x[e], x[e + 1]), u2, nb2);
+        for (int c = 0; c < 32; ++c) {
+          const uint64_t a = fma2(f2_pack(x[2 * c], x[2 * c + 1]), u2, nb2);
           const float p0 = ex2_approx(f2_lo(a)), p1 = ex2_approx(f2_hi(a));
-          acc2[c & 3] = add2(acc2[c & 3], f2_pack(p0, p1));
+          acc[c & 1] = add2(acc[c & 1], f2_pack(p0, p1));
           pk[c] = pack_bf16x2(p0, p1);
         }
-        tmem_st16(tS + 16 * ch, pk);
+        tmem_st32(tS + 32 * half, pk);  // over scores that are weighed already
       }
-      const uint64_t acc = add2(add2(acc2[0], acc2[1]), add2(acc2[2], acc2[3]));
-      l_run += f2_lo(acc) + f2_hi(acc);
+      const uint64_t both = add2(acc[0], acc[1]);
+      l_run += f2_lo(both) + f2_hi(both);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -771,7 +873,7 @@ __global__ void __launch_bounds__(Cfg<D, Q4, TWO>::THREADS, 1) attend_kernel(con
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   T* ctl = reinterpret_cast<T*>(smem + C::OFF_CTL);
-  const int tid = threadIdx.x, warp = tid / 32;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid / 32, 0);
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->q_full[i], 2);
@@ -783,6 +885,10 @@ __global__ void __launch_bounds__(Cfg<D, Q4, TWO>::THREADS, 1) attend_kernel(con
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(&ctl->kv_full[i], Q4 ? 4 : 1);
       mbar_init(&ctl->kv_empty[i], 1);
+    }
+    for (int i = 0; i < C::RAWS; ++i) {
+      mbar_init(&ctl->raw_full[i], 1);
+      mbar_init(&ctl->raw_empty[i], 4);
     }
     mbar_init(&ctl->last, 1);
     ctl->abort_flag = 0;
@@ -827,13 +933,14 @@ __global__ void __launch_bounds__(Cfg<D, Q4, TWO>::THREADS, 1) attend_kernel(con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
-  const Walk w(p, ctl->begin, ctl->end);
+  const Walk w(p, ctl->begin, ctl->end, &ctl->walk[warp]);
   if (warp < 4) {
     setmaxnreg_dec<C::LOW>();
     if (warp == 0) {
-      if constexpr (!Q4) produce<C>(p, smem, ctl, w);
+      if constexpr (Q4) produce4<D, C>(p, smem, ctl, w);
+      else produce<C>(p, smem, ctl, w);
     } else if (warp == 1) {
-      if (tid % 32 == 0) issue<D, Q4, TWO, C>(p, smem, ctl, w, tmem);
+      issue<D, Q4, TWO, C>(p, smem, ctl, w, tmem);
     } else {
       load_queries<D, TWO, C>(p, smem, ctl, w);
     }
@@ -852,7 +959,7 @@ __global__ void __launch_bounds__(Cfg<D, Q4, TWO>::THREADS, 1) attend_kernel(con
 }
 
 // ---------------------------------------------------------------------------------------------
-// Joining cut units, and rows of padding
+// Joining cut units
 // ---------------------------------------------------------------------------------------------
 // Block (x, y): if run x + 1 begins within a unit whose first tiles run x has, rows 32 y .. of that unit.
 constexpr int kJoinRows = 32;
@@ -921,20 +1028,6 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   }
   // partial rows, and the order of writes to out and lse against earlier kernels, from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // padding: rows [count, N) of every head
-  const int blocks = gridDim.x * gridDim.y, block = blockIdx.y * gridDim.x + blockIdx.x;
-  const int groups = min(B, blocks);  // blocks of one number modulo this share sequences
-  for (int b = block % groups; b < B; b += groups) {
-    const int count = chunk_of(p, b).count;
-    const int64_t pieces = static_cast<int64_t>(p.N - count) * p.Hq * (D / 8);
-    const int64_t step = static_cast<int64_t>((blocks - block % groups + groups - 1) / groups) * 256;
-    for (int64_t i = static_cast<int64_t>(block / groups) * 256 + tid; i < pieces; i += step) {
-      const int64_t row = i / (D / 8);
-      const int h = static_cast<int>(row / (p.N - count)), n = count + static_cast<int>(row % (p.N - count));
-      *reinterpret_cast<uint4*>(p.out + b * p.o_sb + h * p.o_sh + n * p.o_sn + i % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
-      if (p.lse && i % (D / 8) == 0) p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.N + n] = kNegInf;
-    }
-  }
   if (parts == 0) return;
   const Chunk c = chunk_of(p, f.pos.b);
   constexpr int L = D / 4;  // threads of a row
