@@ -27,6 +27,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <climits>
 
 #include "launch.h"
 #include "paged.cuh"
@@ -50,7 +51,7 @@ struct Cfg {
   static constexpr int STAGES = D == 64 ? 6 : TWO ? (Q4 ? 2 : 3) : Q4 ? 4 : 5;
   // key tiles whose notes (factors, bad pages) may be in use at once: of the ring's tiles, those
   // behind the one whose V is still held by a softmax that reads them
-  static constexpr int NOTES = STAGES <= 3 ? 2 : 4;
+  static constexpr int NOTES = STAGES <= 3 ? 2 : STAGES <= 5 ? 3 : 4;
   // 4 bits: K or V of a tile as the cache has it, codes and then steps
   static constexpr uint32_t CODES = kTile * (D / 2), RAW = CODES + kTile * (D / 16);
   static constexpr int RAWS = !Q4 ? 0 : D == 64 ? 6 : 3;
@@ -186,19 +187,24 @@ __device__ __forceinline__ Found find_in(const PagedAttendWork& p, int b, const 
   return f;
 }
 
+// How a segment's tiles go to the two row tiles' accumulators ("slots"): units of up to 128 rows have
+// one row tile, whose key tiles alternate between both, joined at the segment's end, so that one's
+// softmax runs beside the other's products.
+constexpr int kOne = 0, kTwo = 1, kSplit = 2;
+
 // The part of a unit that a run has.
 struct Seg {
   int b, kvh, row0, rows;    // first row of the unit, rows of the sequence and KV head
   int first, lo, hi;         // position of query 0; the unit's keys
   int t, n;                  // first tile of the segment, its tiles
-  int part;                  // -1: the whole unit, else which of the CTA's two partial results it is
+  int8_t part;               // -1: the whole unit, else which of the CTA's two partial results it is
+  int8_t kind;
 };
 
 // Steps through a run's segments; a converged warp calls it. The state and the segment lie in shared
 // memory, a copy for each warp, for the softmax has no registers to spare.
 struct WalkState {
   Pos at;
-  int first, count, units, done;
   Seg seg;
 };
 struct Walk {
@@ -206,11 +212,7 @@ struct Walk {
   const Pos& end;
   WalkState* st;
   __device__ Walk(const PagedAttendWork& p_, const Pos& begin, const Pos& end_, WalkState* st_) : p(p_), end(end_), st(st_) {
-    if (threadIdx.x % 32 == 0) {
-      st->at = begin;
-      st->done = begin.b >= p.cache.B;
-      if (!st->done) enter(chunk_of(p, begin.b));
-    }
+    if (threadIdx.x % 32 == 0) st->at = begin;
     __syncwarp();
   }
   // The next segment, or null. It stays until the next call.
@@ -222,16 +224,12 @@ struct Walk {
   }
 
  private:
-  __device__ __forceinline__ void enter(const Chunk& c) {
-    st->first = c.first, st->count = c.count;
-    st->units = units_of(p, c);
-  }
   __device__ __forceinline__ void step() {
     Seg& s = st->seg;
+    Pos at = st->at;
     s.n = 0;
-    while (!st->done) {
-      const Pos at = st->at;
-      const Chunk c = {st->first, st->count, false};
+    while (at.b < p.cache.B) {
+      const Chunk c = chunk_of(p, at.b);
       const Span w = span_of(p, c, at.r);
       const bool stop = at.b == end.b && at.kvh == end.kvh && at.r == end.r;
       const int t1 = stop ? end.t : w.nt;
@@ -239,37 +237,43 @@ struct Walk {
       s.first = c.first, s.lo = w.lo, s.hi = w.hi;
       s.t = w.t0 + at.t, s.n = max(0, t1 - at.t);
       s.part = at.t > 0 ? 0 : t1 < w.nt ? 1 : -1;
-      st->done = stop;
-      st->at.t = 0;
-      if (!stop && (st->at.r = at.r + 1) == st->units) {
-        st->at.r = 0;
-        if ((st->at.kvh = at.kvh + 1) == p.cache.Hkv) {
-          st->at.kvh = 0;
-          int b = at.b + 1;
-          Chunk next = {};
-          while (b < p.cache.B && (next = chunk_of(p, b)).count == 0) ++b;
-          st->at.b = b;
-          if (b < p.cache.B) enter(next);
-          else st->done = 1;
+      s.kind = s.rows - s.row0 > 128 ? kTwo : s.n > 1 ? kSplit : kOne;
+      at.t = 0;
+      if (stop) {
+        at.b = p.cache.B;
+      } else if (++at.r == units_of(p, c)) {
+        at.r = 0;
+        if (++at.kvh == p.cache.Hkv) {
+          at.kvh = 0;
+          do ++at.b;
+          while (at.b < p.cache.B && chunk_of(p, at.b).count == 0);
         }
       }
-      if (s.n > 0) return;
+      if (s.n > 0) break;
     }
+    st->at = at;
   }
 };
 
 template <int NOTES, bool Q4>
 struct Ctl {
   uint64_t q_full[2], q_empty[2], kv_full[6], kv_empty[6], s_full[2], p_full[2], o_full[2], last;
-  uint64_t raw_full[Q4 ? 6 : 1], raw_empty[Q4 ? 6 : 1], raw_bad[Q4 ? 6 : 1];
+  uint64_t joint_full, joint_empty;      // split segments: slot 1's result is complete, is taken
+  uint64_t raw_full[Q4 ? 6 : 0], raw_empty[Q4 ? 6 : 0], raw_bad[Q4 ? 6 : 0], most_full[Q4 ? 2 : 0];
+  uint64_t bad[NOTES];                   // a byte for each 16 keys: on a page that is none
+  float factor[Q4 ? NOTES : 0];          // what the tile's scores are to be multiplied by
+  uint32_t most[Q4 ? 2 : 0][4];          // its largest step, by expanding warp
   uint32_t tmem_base;
   int abort_flag;
-  Pos begin, end;
+  Pos end;
   WalkState walk[Q4 ? 16 : 12];
-  int64_t wsum[16];
-  uint64_t bad[NOTES];                   // a byte for each 16 keys: on a page that is none
-  float factor[NOTES];                   // 4 bits: what the tile's scores are to be multiplied by
-  uint32_t most[2][4];                   // its largest step, by expanding warp
+  union {
+    struct {
+      Pos begin;
+      int64_t wsum[16];
+    };
+    float2 joint[128];                   // slot 1's (max, sum)
+  };
 };
 
 template <int D, bool Q4, bool TWO>
@@ -527,8 +531,12 @@ __device__ __forceinline__ void expand(const PagedAttendParams& p, uint8_t* smem
           }
           most = __reduce_max_sync(0xffffffffu, most);
           uint32_t(&all)[4] = ctl->most[tiles & 1];
-          if (lane == 0) all[row / 32] = most;
-          named_bar_sync(1, 128);
+          if (lane == 0) {
+            all[row / 32] = most;
+            mbar_arrive(&ctl->most_full[tiles & 1]);
+          }
+          ok = __all_sync(0xffffffffu, mbar_wait(&ctl->most_full[tiles & 1], (tiles >> 1) & 1, p.status, abort_flag));
+          if (!ok) break;
           const uint32_t e = max(max(max(all[0], all[1]), max(all[2], all[3])) >> 7, 12u);
           const float up = __uint_as_float((254u + 11u - e) << 23);
           if (row == 0) {
@@ -576,7 +584,7 @@ __device__ __forceinline__ void load_queries(const PagedAttendParams& p, uint8_t
 #pragma unroll
     for (int slot = 0; slot < 2; ++slot) {
       const int r0 = s.row0 + 128 * slot;
-      if (r0 >= s.rows) continue;
+      if (slot > 0 && s.kind != kTwo) continue;
       ok = ok && __all_sync(0xffffffffu, mbar_wait(&ctl->q_empty[slot], (used[slot] & 1) ^ 1, p.status, abort_flag));
       if (!ok) break;
       ++used[slot];
@@ -636,14 +644,15 @@ __device__ __forceinline__ void issue(const PagedAttendParams& p, uint8_t* smem,
     ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, status, abort_flag));
   };
   auto wait_tile = [&](int it) { wait(&ctl->kv_full[it % C::STAGES], (it / C::STAGES) & 1); };
-  auto scores = [&](int s, int it, bool first, bool last) {
+  // S of slot s from row tile `qs`
+  auto scores = [&](int s, int qs, int it, bool first, bool last) {
     if (first) {
-      wait(&ctl->q_full[s], (phases >> s) & 1);
-      phases ^= 1u << s;
+      wait(&ctl->q_full[qs], (phases >> qs) & 1);
+      phases ^= 1u << qs;
     }
     if (!ok) return;
     tc_fence_after();
-    const uint32_t q = dQ + s * (C::QSLOT >> 4), k = dK + (it % C::STAGES) * (C::TILE >> 4);
+    const uint32_t q = dQ + qs * (C::QSLOT >> 4), k = dK + (it % C::STAGES) * (C::TILE >> 4);
     mma_ss_warp<0>(tmem + 128 * s, q, k, dhi, idesc_s);
 #pragma unroll
     for (int kk = 1; kk < (TWO ? 2 : 1) * (D / 16); ++kk) {
@@ -651,48 +660,77 @@ __device__ __forceinline__ void issue(const PagedAttendParams& p, uint8_t* smem,
       mma_ss_warp<1>(tmem + 128 * s, q + (((kk / (D / 16)) * C::TILE + off) >> 4), k + (off >> 4), dhi, idesc_s);
     }
     mma_commit_warp(&ctl->s_full[s]);
-    if (last) mma_commit_warp(&ctl->q_empty[s]);
+    if (last) mma_commit_warp(&ctl->q_empty[qs]);
   };
   auto values = [&](int s, int it, bool first, bool last) {
+    const uint32_t v = dV + (it % C::STAGES) * (C::TILE >> 4), o = tmem + 256 + 128 * s, w = tmem + 128 * s;
     wait(&ctl->p_full[s], (phases >> (2 + s)) & 1);
     phases ^= 4u << s;
     if (!ok) return;
     tc_fence_after();
-    const uint32_t v = dV + (it % C::STAGES) * (C::TILE >> 4), o = tmem + 256 + 128 * s, w = tmem + 128 * s;
     if (first) mma_ts_warp<0>(o, w, v, dhi, idesc_o);
     else mma_ts_warp<1>(o, w, v, dhi, idesc_o);
 #pragma unroll
-    for (int kk = 1; kk < kTile / 16; ++kk) mma_ts_warp<1>(o, w + kk * 8, v + kk * (2048 >> 4), dhi, idesc_o);
+    for (int kk = 1; kk < 8; ++kk) mma_ts_warp<1>(o, w + kk * 8, v + kk * (2048 >> 4), dhi, idesc_o);
     if (last) mma_commit_warp(&ctl->o_full[s]);
   };
-  // the next segment's tiles and whether it has a second row tile; false: there is none
-  auto next = [&](int* n, bool* two) {
+  // the next segment's tiles and kind (as votes, so that branches on them are known to be the warp's)
+  int nn = 0;
+  bool have = false, two = false, split = false;
+  auto next = [&]() {
     const Seg* s = w.next();
-    *n = __shfl_sync(0xffffffffu, s ? s->n : 0, 0);
-    *two = __any_sync(0xffffffffu, s && s->row0 + 128 < s->rows);
-    return __any_sync(0xffffffffu, s != nullptr) != 0;
+    nn = __shfl_sync(0xffffffffu, s ? s->n : 0, 0);
+    have = __any_sync(0xffffffffu, s != nullptr);
+    two = __any_sync(0xffffffffu, s && s->kind == kTwo);
+    split = __any_sync(0xffffffffu, s && s->kind == kSplit);
   };
-  // Step: the values' products of a tile and the scores' of the next one, row tile by row tile.
-  int cn = 0, nn = 0, ci = 0, ni = 0, vt = -1;  // tiles of their segments, the tiles' numbers, ring index of V
-  bool act1 = false, nact1 = false, cur = false;
-  bool have = next(&nn, &nact1);
-  while (ok && (cur || have)) {
-    const bool first = ci == 0, last = ci == cn - 1, nfirst = ni == 0, nlast = ni == nn - 1;
-    const int kt = vt + 1;
-    if (cur) wait_tile(vt);
+  next();
+  int vt = -1;  // ring index of the V before the next K
+  while (ok && have) {
+    if (split) {
+      // the next tile's scores, in the other slot, go before a tile's values
+      int kt = vt + 1;
+      wait_tile(kt);
+      scores(0, 0, kt, true, false);
+      if (ok) mma_commit_warp(&ctl->kv_empty[kt % C::STAGES]);
 #pragma unroll 1
-    for (int s = 0; s < 2; ++s) {
-      if (cur && (s == 0 || act1)) values(s, vt, first, last);
-      if (cur && s == act1 && ok) mma_commit_warp(&ctl->kv_empty[vt % C::STAGES]);
-      if (have && s == 0) wait_tile(kt);
-      if (have && (s == 0 || nact1)) scores(s, kt, nfirst, nlast);
+      for (int i = 0; i < nn && ok; ++i, kt += 2) {
+        if (i + 1 < nn) {
+          wait_tile(kt + 2);
+          scores(~i & 1, 0, kt + 2, false, i + 2 == nn);
+          if (ok) mma_commit_warp(&ctl->kv_empty[(kt + 2) % C::STAGES]);
+        }
+        wait_tile(kt + 1);
+        values(i & 1, kt + 1, i < 2, i >= nn - 2);
+        if (ok) mma_commit_warp(&ctl->kv_empty[(kt + 1) % C::STAGES]);
+      }
+      vt += 2 * nn;
+      next();
+      continue;
     }
-    if (have && ok) mma_commit_warp(&ctl->kv_empty[kt % C::STAGES]);
-    cur = have, cn = nn, ci = ni, act1 = nact1;
-    vt += 2;
-    if (have && ++ni == nn) {
-      have = next(&nn, &nact1);
-      ni = 0;
+    // a step: the values' products of a tile and the scores' of the next one, row tile by row tile
+    int cn = 0, ci = 0, ni = 0;  // tiles of the segment, the tiles' numbers
+    bool act1 = false, cur = false;
+    while (ok && (cur || (have && !split))) {
+      const bool more = have && !split, first = ci == 0, last = ci == cn - 1, nfirst = ni == 0, nlast = ni == nn - 1;
+      const int kt = vt + 1;
+      if (cur) wait_tile(vt);
+#pragma unroll 1
+      for (int s = 0; s < 2; ++s) {
+        if (cur && (s == 0 || act1)) values(s, vt, first, last);
+        if (cur && s == act1 && ok) mma_commit_warp(&ctl->kv_empty[vt % C::STAGES]);
+        if (more && s == 0) wait_tile(kt);
+        if (more && (s == 0 || two)) scores(s, s, kt, nfirst, nlast);
+      }
+      if (more && ok) mma_commit_warp(&ctl->kv_empty[kt % C::STAGES]);
+      cur = more, cn = nn, ci = ni, act1 = two;
+      if (more) {
+        vt += 2;
+        if (++ni == nn) {
+          next();
+          ni = 0;
+        }
+      }
     }
   }
   // all products have ended before tensor memory is given back
@@ -710,33 +748,39 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
   int* status = p.status;
   const uint32_t tS = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 128 * slot;
   const uint32_t tO = tS - 128 * slot + 256 + 128 * slot;
-  int sc = 0, oc = 0, tiles = 0;
+  int sc = 0, oc = 0, jc = 0, tiles = 0;
   bool ok = true;
   const Seg* seg;
   while (ok && (seg = w.next())) {
     const Seg& s = *seg;
-    if (s.row0 + 128 * slot >= s.rows) {
+    const bool split = s.kind == kSplit;
+    if (slot == 1 && s.kind == kOne) {
       tiles += s.n;
       continue;
     }
-    const int row = s.row0 + 128 * slot + r;
+    const int row = s.row0 + (split ? 0 : 128 * slot) + r;
     const bool live = row < s.rows;
     const uint32_t n = static_cast<uint32_t>(min(row, s.rows - 1)) / static_cast<uint32_t>(p.g);
     const int h = s.kvh * p.g + (min(row, s.rows - 1) - static_cast<int>(n) * p.g);
-    const int pos = live ? s.first + static_cast<int>(n) : -1;   // a row behind the last sees nothing
-    const int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+    const int pos = live ? s.first + static_cast<int>(n) : INT_MAX;  // a row behind the last needs no mask
+    const bool some = __any_sync(0xffffffffu, live);
+    const int lo = p.window > 0 && live ? max(0, pos - p.window + 1) : 0;
     float mul = p.scale_log2;
     if (Q4) mul *= __ldg(p.factor + (static_cast<int64_t>(s.b) * p.Hq + h) * p.N + n);
     const float slope = p.slopes ? __ldg(p.slopes + h) * kLog2e : 0.f;
     float m_run = kNegInf, l_run = 0.f;
-    for (int i = 0; i < s.n; ++i, ++tiles) {
+    for (int i = split ? slot : 0; i < s.n; i += split ? 2 : 1) {
       ok = __all_sync(0xffffffffu, mbar_wait(&ctl->s_full[slot], sc & 1, status, abort_flag));
       if (!ok) break;
       ++sc;
+      if (!some) {  // none of the warp's rows is one: the weights stay as they are
+        if (lane == 0) mbar_arrive(&ctl->p_full[slot]);
+        continue;
+      }
       tc_fence_after();
-      const uint64_t bad = *reinterpret_cast<volatile uint64_t*>(&ctl->bad[tiles % C::NOTES]);
+      const uint64_t bad = *reinterpret_cast<volatile uint64_t*>(&ctl->bad[(tiles + i) % C::NOTES]);
       float part = 1.f;  // of the scores: a power of two
-      if constexpr (Q4) part = *reinterpret_cast<volatile float*>(&ctl->factor[tiles % C::NOTES]);
+      if constexpr (Q4) part = *reinterpret_cast<volatile float*>(&ctl->factor[(tiles + i) % C::NOTES]);
       const int k0 = (s.t + i) * kTile;
       const float unit = p.slopes ? 1.f : mul * part;
       const bool edge = k0 + kTile - 1 > pos || k0 < lo || bad != 0;
@@ -756,10 +800,17 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
           for (int c = 0; c < 64; ++c) x[c] = __fmaf_rn(slope, static_cast<float>(c), __fmaf_rn(x[c], mul * part, base));
         }
         if (__builtin_expect(edge, 0)) {
-          const int c0 = lo - k0 - 64 * half, c1 = pos - k0 - 64 * half;
+          // a bit for each column that the row sees
           const uint32_t gone = static_cast<uint32_t>(bad >> (32 * half));
 #pragma unroll
-          for (int c = 0; c < 64; ++c) x[c] = c >= c0 && c <= c1 && !((gone >> (8 * (c / 16))) & 1) ? x[c] : kNegInf;
+          for (int w = 0; w < 2; ++w) {
+            const int c0 = min(max(lo - k0 - 64 * half - 32 * w, 0), 32), c1 = min(max(pos - k0 - 64 * half - 32 * w + 1, 0), 32);
+            uint32_t see = static_cast<uint32_t>(((1ull << c1) - 1) & ~((1ull << c0) - 1));
+            if ((gone >> (16 * w)) & 1) see &= 0xFFFF0000u;
+            if ((gone >> (16 * w)) & 0x100) see &= 0x0000FFFFu;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) x[32 * w + c] = (see >> c) & 1 ? x[32 * w + c] : kNegInf;
+          }
         }
       };
       float mx = kNegInf;
@@ -778,7 +829,7 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
       mx *= unit;
       // O keeps its scale unless this tile exceeds it by more than 2^kLazy
       const float m_new = mx > m_run + kLazy ? mx : m_run;
-      const bool grow = m_new > m_run && m_run != kNegInf;
+      const bool grow = m_new > m_run && m_run != kNegInf && live;
       if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
         // (the products of the tile before are complete: S of this one was issued behind them)
         const float alpha = grow ? ex2_approx(m_run - m_new) : 1.f;
@@ -818,11 +869,47 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->p_full[slot]);
     }
+    tiles += s.n;
     if (!ok) break;
     ok = __all_sync(0xffffffffu, mbar_wait(&ctl->o_full[slot], oc & 1, status, abort_flag));
     if (!ok) break;
     ++oc;
     tc_fence_after();
+    float w0 = 1.f, w1 = 0.f;  // the slots' weights
+    if (split) {
+      if (slot == 1) {
+        // O_1 stays as it is until slot 0 has taken it
+        ctl->joint[r] = make_float2(m_run, l_run);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->joint_full);
+        ok = __all_sync(0xffffffffu, mbar_wait(&ctl->joint_empty, jc & 1, status, abort_flag));
+        ++jc;
+        continue;
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(&ctl->joint_full, jc & 1, status, abort_flag));
+      if (!ok) break;
+      ++jc;
+      tc_fence_after();
+      const float2 ml = ctl->joint[r];
+      const float m = fmaxf(m_run, ml.x), base = m == kNegInf ? 0.f : m;
+      w0 = ex2_approx(m_run - base), w1 = ex2_approx(ml.x - base);
+      l_run = w0 * l_run + w1 * ml.y;
+      m_run = m;
+    }
+    // columns 32 ch .. of the row's accumulator
+    auto result = [&](int ch, uint32_t (&o)[32]) {
+      tmem_ld32(tO + ch * 32, o);
+      tmem_wait_ld_dep(o);
+      if (split) {
+        uint32_t o1[32];
+        tmem_ld32(tO + 128 + ch * 32, o1);
+        tmem_wait_ld_dep(o1);
+#pragma unroll
+        for (int q = 0; q < 32; ++q)
+          o[q] = __float_as_uint(__fmaf_rn(__uint_as_float(o1[q]), w1, __uint_as_float(o[q]) * w0));
+      }
+    };
     const bool any = !(l_run == 0.f);  // a NaN goes to the output
     if (s.part < 0) {
       const float inv = any ? 1.f / l_run : 0.f;
@@ -830,8 +917,7 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
 #pragma unroll 1
       for (int ch = 0; ch < D / 32; ++ch) {
         uint32_t o[32];
-        tmem_ld32(tO + ch * 32, o);
-        tmem_wait_ld();
+        result(ch, o);
         if (live) {
           uint4* dst = reinterpret_cast<uint4*>(out + ch * 32);
 #pragma unroll
@@ -853,8 +939,7 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
 #pragma unroll 1
       for (int ch = 0; ch < D / 32; ++ch) {
         uint32_t o[32];
-        tmem_ld32(tO + ch * 32, o);
-        tmem_wait_ld();
+        result(ch, o);
         if (live) {
           uint4* dst = reinterpret_cast<uint4*>(p.part_acc + at * D + ch * 32);
 #pragma unroll
@@ -862,6 +947,11 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
         }
       }
       if (live) p.part_ml[at] = make_float2(m_run, l_run);
+    }
+    if (split) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->joint_empty);
     }
   }
 }
@@ -890,6 +980,12 @@ __global__ void __launch_bounds__(Cfg<D, Q4, TWO>::THREADS, 1) attend_kernel(con
       mbar_init(&ctl->raw_full[i], 1);
       mbar_init(&ctl->raw_empty[i], 4);
     }
+    if constexpr (Q4) {
+      mbar_init(&ctl->most_full[0], 4);
+      mbar_init(&ctl->most_full[1], 4);
+    }
+    mbar_init(&ctl->joint_full, 4);
+    mbar_init(&ctl->joint_empty, 4);
     mbar_init(&ctl->last, 1);
     ctl->abort_flag = 0;
     ctl->begin = ctl->end = Pos{p.cache.B, 0, 0, 0};
@@ -933,7 +1029,8 @@ __global__ void __launch_bounds__(Cfg<D, Q4, TWO>::THREADS, 1) attend_kernel(con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
-  const Walk w(p, ctl->begin, ctl->end, &ctl->walk[warp]);
+  Walk w(p, ctl->begin, ctl->end, &ctl->walk[warp]);
+  __syncthreads();  // (the begin's place is used for other things from here on)
   if (warp < 4) {
     setmaxnreg_dec<C::LOW>();
     if (warp == 0) {

@@ -130,6 +130,25 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* s
   }
 }
 
+// The same, but the clock is first read after 256 polls: reading it takes longer than most waits
+// are still to last when the first poll has failed.
+__device__ __forceinline__ bool mbar_wait_poll(uint64_t* bar, uint32_t parity, int* status, volatile int* abort_flag) {
+  const uint32_t a = smem_u32(bar);
+  uint64_t t0 = 0;
+  for (uint32_t polls = 1; !mbar_try_wait(a, parity); ++polls) {
+    if (polls & 255u) continue;
+    if (abort_flag && *abort_flag) return false;
+    const uint64_t t = globaltimer_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > ATTNFUSE_WAIT_LIMIT_NS) {
+      if (status) atomicOr(status, kDevTimeout);
+      if (abort_flag) *abort_flag = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
 // Bounded wait until a global flag that another CTA releases reads `want`; then this thread's
 // later TMA copies see what was written before the release. Same failure contract as mbar_wait.
 __device__ __forceinline__ bool flag_wait(const uint32_t* flag, uint32_t want, int* status,
