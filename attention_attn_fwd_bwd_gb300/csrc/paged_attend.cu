@@ -28,6 +28,7 @@
 #include <algorithm>
 #include <atomic>
 #include <climits>
+#include <type_traits>
 
 #include "launch.h"
 #include "paged.cuh"
@@ -469,7 +470,7 @@ __device__ __forceinline__ void expand8(uint32_t first, uint32_t last, uint32_t 
 template <int D, bool F16>
 __device__ __forceinline__ void expand_row(const uint8_t* raw, const uint32_t (&step2)[D / 64], uint8_t* tile, int row) {
   const int turn = D == 128 ? (row & 2) | ((row >> 2) & 1) : (row >> 2) & 1;
-#pragma unroll 2
+#pragma unroll 1
   for (int j = 0; j < D / 32; ++j) {
     const int at = j ^ turn;
     const uint4 c = *reinterpret_cast<const uint4*>(raw + row * (D / 2) + at * 16);
@@ -743,6 +744,7 @@ __device__ __forceinline__ void issue(const PagedAttendParams& p, uint8_t* smem,
 // ---------------------------------------------------------------------------------------------
 template <int D, bool Q4, class C, class T>
 __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk w, uint32_t tmem, int slot) {
+  constexpr int CW = 32;  // columns of the scores that a thread takes at once
   const int lane = threadIdx.x % 32, quarter = (threadIdx.x / 32) % 4, r = quarter * 32 + lane;
   volatile int* abort_flag = &ctl->abort_flag;
   int* status = p.status;
@@ -784,86 +786,89 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
       const int k0 = (s.t + i) * kTile;
       const float unit = p.slopes ? 1.f : mul * part;
       const bool edge = k0 + kTile - 1 > pos || k0 < lo || bad != 0;
-      // Scores of columns 64 half .. of the row, masked, in units of 1 / unit. (Both passes over the tile
-      // read them again from tensor memory, in loops: all 128 at once, unrolled, take registers and
-      // instruction cache that the warps of five roles do not have.)
-      auto load = [&](int half, float (&x)[64]) {
-        uint32_t xr[64];
-        tmem_ld32<0>(tS + 64 * half, xr);
-        tmem_ld32<32>(tS + 64 * half + 32, xr);
-        tmem_wait_ld_dep(xr);
+      // Both passes over the tile read its scores from tensor memory, CW columns at a time, in loops:
+      // all 128 at once, unrolled, take registers and instruction cache that the warps of five
+      // roles do not have. For the same reason tiles that need masks or a bias have code of their own.
+      auto tile = [&](auto general) {
+        constexpr bool GENERAL = decltype(general)::value;
+        // scores of columns CW ch .. of the row, in units of 1 / unit
+        auto load = [&](int ch, float (&x)[CW]) {
+          uint32_t xr[CW];
+          tmem_ld32(tS + CW * ch, xr);
+          tmem_wait_ld_dep(xr);
 #pragma unroll
-        for (int c = 0; c < 64; ++c) x[c] = __uint_as_float(xr[c]);
-        if (p.slopes) {
-          const float base = slope * static_cast<float>(k0 + 64 * half - pos);
+          for (int c = 0; c < CW; ++c) x[c] = __uint_as_float(xr[c]);
+          if constexpr (GENERAL) {
+            if (p.slopes) {
+              const float base = slope * static_cast<float>(k0 + CW * ch - pos);
 #pragma unroll
-          for (int c = 0; c < 64; ++c) x[c] = __fmaf_rn(slope, static_cast<float>(c), __fmaf_rn(x[c], mul * part, base));
-        }
-        if (__builtin_expect(edge, 0)) {
-          // a bit for each column that the row sees
-          const uint32_t gone = static_cast<uint32_t>(bad >> (32 * half));
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const int c0 = min(max(lo - k0 - 64 * half - 32 * w, 0), 32), c1 = min(max(pos - k0 - 64 * half - 32 * w + 1, 0), 32);
+              for (int c = 0; c < CW; ++c) x[c] = __fmaf_rn(slope, static_cast<float>(c), __fmaf_rn(x[c], mul * part, base));
+            }
+            // a bit for each column that the row sees
+            const uint32_t gone = static_cast<uint32_t>(bad >> (CW / 2 * ch));
+            const int at = k0 + CW * ch, c0 = min(max(lo - at, 0), 32), c1 = min(max(pos - at, -1), 31) + 1;
             uint32_t see = static_cast<uint32_t>(((1ull << c1) - 1) & ~((1ull << c0) - 1));
-            if ((gone >> (16 * w)) & 1) see &= 0xFFFF0000u;
-            if ((gone >> (16 * w)) & 0x100) see &= 0x0000FFFFu;
+            if (gone & 1) see &= 0xFFFF0000u;
+            if (gone & 0x100) see &= 0x0000FFFFu;
 #pragma unroll
-            for (int c = 0; c < 32; ++c) x[32 * w + c] = (see >> c) & 1 ? x[32 * w + c] : kNegInf;
+            for (int c = 0; c < CW; ++c) x[c] = (see >> c) & 1 ? x[c] : kNegInf;
+          }
+        };
+        float mx = kNegInf;
+#pragma unroll 1
+        for (int ch = 0; ch < kTile / CW; ++ch) {
+          float x[CW], m[CW / 8];
+          load(ch, x);
+#pragma unroll
+          for (int k = 0; k < CW / 8; ++k) m[k] = fmaxf(x[2 * k], x[2 * k + 1]);
+#pragma unroll
+          for (int j = 1; j < 4; ++j)
+#pragma unroll
+            for (int k = 0; k < CW / 8; ++k) m[k] = max3f(m[k], x[CW / 4 * j + 2 * k], x[CW / 4 * j + 2 * k + 1]);
+#pragma unroll
+          for (int k = 0; k < CW / 8; k += 2) mx = max3f(mx, m[k], m[k + 1]);
+        }
+        mx *= unit;
+        // O keeps its scale unless this tile exceeds it by more than 2^kLazy
+        const float m_new = mx > m_run + kLazy ? mx : m_run;
+        const bool grow = m_new > m_run && m_run != kNegInf && live;
+        if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
+          // (the products of the tile before are complete: S of this one was issued behind them)
+          const float alpha = grow ? ex2_approx(m_run - m_new) : 1.f;
+          l_run *= alpha;
+#pragma unroll 1
+          for (int ch = 0; ch < D / 32; ++ch) {
+            uint32_t o[32];
+            tmem_ld32(tO + ch * 32, o);
+            tmem_wait_ld_dep(o);
+#pragma unroll
+            for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
+            tmem_st32(tO + ch * 32, o);
           }
         }
+        m_run = m_new;
+        const float nb = m_new == kNegInf ? 0.f : -m_new;
+        const uint64_t u2 = f2_pack(unit, unit), nb2 = f2_pack(nb, nb);
+        uint64_t acc[2] = {0, 0};
+#pragma unroll 1
+        for (int ch = 0; ch < kTile / CW; ++ch) {
+          float x[CW];
+          load(ch, x);
+          uint32_t pk[CW / 2];
+#pragma unroll
+          for (int c = 0; c < CW / 2; ++c) {
+            const uint64_t a = fma2(f2_pack(x[2 * c], x[2 * c + 1]), u2, nb2);
+            const float p0 = ex2_approx(f2_lo(a)), p1 = ex2_approx(f2_hi(a));
+            acc[c & 1] = add2(acc[c & 1], f2_pack(p0, p1));
+            pk[c] = pack_bf16x2(p0, p1);
+          }
+          tmem_st16(tS + CW / 2 * ch, pk);  // over scores that are weighed already
+        }
+        const uint64_t both = add2(acc[0], acc[1]);
+        l_run += f2_lo(both) + f2_hi(both);
       };
-      float mx = kNegInf;
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        float x[64], m[8];
-        load(half, x);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) m[k] = fmaxf(x[2 * k], x[2 * k + 1]);
-#pragma unroll
-        for (int j = 1; j < 4; ++j)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) m[k] = max3f(m[k], x[16 * j + 2 * k], x[16 * j + 2 * k + 1]);
-        mx = max3f(mx, max3f(m[0], m[1], m[2]), max3f(max3f(m[3], m[4], m[5]), m[6], m[7]));
-      }
-      mx *= unit;
-      // O keeps its scale unless this tile exceeds it by more than 2^kLazy
-      const float m_new = mx > m_run + kLazy ? mx : m_run;
-      const bool grow = m_new > m_run && m_run != kNegInf && live;
-      if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
-        // (the products of the tile before are complete: S of this one was issued behind them)
-        const float alpha = grow ? ex2_approx(m_run - m_new) : 1.f;
-        l_run *= alpha;
-#pragma unroll 1
-        for (int ch = 0; ch < D / 32; ++ch) {
-          uint32_t o[32];
-          tmem_ld32(tO + ch * 32, o);
-          tmem_wait_ld_dep(o);
-#pragma unroll
-          for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
-          tmem_st32(tO + ch * 32, o);
-        }
-      }
-      m_run = m_new;
-      const float nb = m_new == kNegInf ? 0.f : -m_new;
-      const uint64_t u2 = f2_pack(unit, unit), nb2 = f2_pack(nb, nb);
-      uint64_t acc[2] = {0, 0};
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        float x[64];
-        load(half, x);
-        uint32_t pk[32];
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const uint64_t a = fma2(f2_pack(x[2 * c], x[2 * c + 1]), u2, nb2);
-          const float p0 = ex2_approx(f2_lo(a)), p1 = ex2_approx(f2_hi(a));
-          acc[c & 1] = add2(acc[c & 1], f2_pack(p0, p1));
-          pk[c] = pack_bf16x2(p0, p1);
-        }
-        tmem_st32(tS + 32 * half, pk);  // over scores that are weighed already
-      }
-      const uint64_t both = add2(acc[0], acc[1]);
-      l_run += f2_lo(both) + f2_hi(both);
+      if (p.slopes || __any_sync(0xffffffffu, edge)) tile(std::true_type());
+      else tile(std::false_type());
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();

@@ -130,25 +130,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* s
   }
 }
 
-// The same, but the clock is first read after 256 polls: reading it takes longer than most waits
-// are still to last when the first poll has failed.
-__device__ __forceinline__ bool mbar_wait_poll(uint64_t* bar, uint32_t parity, int* status, volatile int* abort_flag) {
-  const uint32_t a = smem_u32(bar);
-  uint64_t t0 = 0;
-  for (uint32_t polls = 1; !mbar_try_wait(a, parity); ++polls) {
-    if (polls & 255u) continue;
-    if (abort_flag && *abort_flag) return false;
-    const uint64_t t = globaltimer_ns();
-    if (t0 == 0) t0 = t;
-    if (t - t0 > ATTNFUSE_WAIT_LIMIT_NS) {
-      if (status) atomicOr(status, kDevTimeout);
-      if (abort_flag) *abort_flag = 1;
-      return false;
-    }
-  }
-  return true;
-}
-
 // Bounded wait until a global flag that another CTA releases reads `want`; then this thread's
 // later TMA copies see what was written before the release. Same failure contract as mbar_wait.
 __device__ __forceinline__ bool flag_wait(const uint32_t* flag, uint32_t want, int* status,
@@ -611,16 +592,6 @@ __device__ __forceinline__ void tmem_wait_ld_dep(uint32_t (&r)[32]) {
                  "+r"(r[31])
                :
                : "memory");
-}
-// The same for 64 registers.
-__device__ __forceinline__ void tmem_wait_ld_dep(uint32_t (&r)[64]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 64; i += 16)
-    asm volatile(""
-                 : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
-                   "+r"(r[i + 6]), "+r"(r[i + 7]), "+r"(r[i + 8]), "+r"(r[i + 9]), "+r"(r[i + 10]), "+r"(r[i + 11]),
-                   "+r"(r[i + 12]), "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15]));
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
