@@ -16,7 +16,7 @@
 // for each, one row per thread, which writes its weights as bf16 over S_s, and O_s += P_s V with P_s
 // read from tensor memory. The issuing thread goes PV_0(i), S_0(i + 1), PV_1(i), S_1(i + 1): while one
 // tile's softmax runs, the other's products do. K and V tiles come through one ring of shared
-// memory, TMA boxes of a page's rows (bf16) or codes expanded by a warpgroup (4 bits).
+// memory, TMA boxes of a page's rows (bf16) or codes expanded by two warpgroups (4 bits).
 // TMEM (512 columns): S_0 [0, 128), S_1 [128, 256), O_0 [256, 384), O_1 [384, 512); P_s over S_s.
 //
 // Keys of a 4-bit cache are s_g c (8 and 3 bits): exact in fp16 under a power of two of the tile's
@@ -44,15 +44,17 @@ constexpr float kLazy = 8.0f;            // the running maximum may lag by 2^8
 
 template <int D, bool Q4, bool TWO>
 struct Cfg {
-  static constexpr int WARPS = Q4 ? 16 : 12;
+  static constexpr int WARPS = Q4 ? 20 : 12;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int PANELS = D / 64;
   static constexpr uint32_t TILE = kTile * D * 2;                  // bytes of a K, V or Q tile
   static constexpr uint32_t QSLOT = TILE * (TWO ? 2 : 1);
   static constexpr int STAGES = D == 64 ? 6 : TWO ? (Q4 ? 2 : 3) : Q4 ? 4 : 5;
-  // key tiles whose notes (factors, bad pages) may be in use at once: of the ring's tiles, those
-  // behind the one whose V is still held by a softmax that reads them
-  static constexpr int NOTES = STAGES <= 3 ? 2 : STAGES <= 5 ? 3 : 4;
+  // Key tiles whose notes (factors, bad pages) may be in use at once, with tile t the first that a
+  // softmax still reads. bf16: the ring's producer is at most STAGES ahead of V(t), which is held until
+  // then. 4 bits: K(u) is written once the scores of tile u - STAGES / 2 are complete, and those of
+  // tile t + 2 (t + 1, where slots do not alternate) follow t's weights.
+  static constexpr int NOTES = Q4 ? STAGES / 2 + 2 : STAGES <= 3 ? 2 : STAGES <= 5 ? 3 : 4;
   // 4 bits: K or V of a tile as the cache has it, codes and then steps
   static constexpr uint32_t CODES = kTile * (D / 2), RAW = CODES + kTile * (D / 16);
   static constexpr int RAWS = !Q4 ? 0 : D == 64 ? 6 : 3;
@@ -60,8 +62,8 @@ struct Cfg {
   static constexpr uint32_t OFF_RAW = OFF_KV + STAGES * TILE;
   static constexpr uint32_t OFF_CTL = OFF_RAW + RAWS * RAW;
   // registers of the warpgroups: producer, issuer and query loaders; softmax; expanders
-  static constexpr uint32_t LOW = Q4 ? 80 : 104, SM = Q4 ? 168 : 200, EXP = 96;
-  static_assert(LOW + 2 * SM + (Q4 ? EXP : 0) <= (WARPS / 4) * (65536 / THREADS / 8 * 8), "registers of the launch");
+  static constexpr uint32_t LOW = Q4 ? 64 : 104, SM = Q4 ? 128 : 200, EXP = 80;
+  static_assert(LOW + 2 * SM + (Q4 ? 2 * EXP : 0) <= (WARPS / 4) * (65536 / THREADS / 8 * 8), "registers of the launch");
 };
 
 // Boundary between two runs: tile t of unit (b, kvh, r).
@@ -267,11 +269,11 @@ struct Ctl {
   uint32_t tmem_base;
   int abort_flag;
   Pos end;
-  WalkState walk[Q4 ? 16 : 12];
+  WalkState walk[Q4 ? 20 : 12];
   union {
     struct {
       Pos begin;
-      int64_t wsum[16];
+      int64_t wsum[20];
     };
     float2 joint[128];                   // slot 1's (max, sum)
   };
@@ -373,8 +375,8 @@ __device__ __forceinline__ void produce(const PagedAttendParams& p, uint8_t* sme
 }
 
 // ---------------------------------------------------------------------------------------------
-// 4-bit tiles: a producer (one warp) copies codes and steps to shared memory, expanders (four warps,
-// a thread takes a key) write them to the ring as 16-bit values
+// 4-bit tiles: a producer (one warp) copies codes and steps to shared memory, expanders (four warps
+// for K, four for V, a thread takes a key) write them to the ring as 16-bit values
 // ---------------------------------------------------------------------------------------------
 __device__ __forceinline__ void bulk_load(uint8_t* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
@@ -495,70 +497,64 @@ __device__ __forceinline__ void expand_row(const uint8_t* raw, const uint32_t (&
   }
 }
 
-template <int D, class C, class T>
+template <int D, bool VALUES, class C, class T>
 __device__ __forceinline__ void expand(const PagedAttendParams& p, uint8_t* smem, T* ctl, Walk w) {
   const int row = threadIdx.x % 128, lane = threadIdx.x % 32;
   volatile int* abort_flag = &ctl->abort_flag;
-  int it = 0, tiles = 0;
+  int tiles = 0;
   bool ok = true;
   const Seg* seg;
   while (ok && (seg = w.next())) {
     const Seg& s = *seg;
-    for (int i = 0; ok && i < s.n; ++i, ++tiles) {
-      const int key = (s.t + i) * kTile + row;
+    for (int i = 0; i < s.n; ++i, ++tiles) {
+      const int key = (s.t + i) * kTile + row, it = 2 * tiles + VALUES;
+      const int rs = it % C::RAWS, st = it % C::STAGES;
+      ok = __all_sync(0xffffffffu, mbar_wait(&ctl->raw_full[rs], (it / C::RAWS) & 1, p.status, abort_flag) &&
+                                       mbar_wait(&ctl->kv_empty[st], ((it / C::STAGES) & 1) ^ 1, p.status, abort_flag));
+      if (!ok) break;
+      const uint8_t* raw = smem + C::OFF_RAW + rs * C::RAW;
+      const uint64_t bad = *reinterpret_cast<volatile uint64_t*>(&ctl->raw_bad[rs]);
+      // keys that no row sees, or without a page, are zeros (steps of 0, whatever lies there)
+      const bool seen = key >= s.lo && key < s.hi && !((bad >> (8 * (row / 16))) & 1);
+      uint32_t step2[D / 64];
 #pragma unroll
-      for (int v = 0; v < 2; ++v, ++it) {
-        const int rs = it % C::RAWS, st = it % C::STAGES;
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&ctl->raw_full[rs], (it / C::RAWS) & 1, p.status, abort_flag) &&
-                                               mbar_wait(&ctl->kv_empty[st], ((it / C::STAGES) & 1) ^ 1, p.status, abort_flag));
-        if (!ok) break;
-        const uint8_t* raw = smem + C::OFF_RAW + rs * C::RAW;
-        uint8_t* tile = smem + C::OFF_KV + st * C::TILE;
-        const uint64_t bad = *reinterpret_cast<volatile uint64_t*>(&ctl->raw_bad[rs]);
-        // keys that no row sees, or without a page, are zeros (steps of 0, whatever lies there)
-        const bool seen = key >= s.lo && key < s.hi && !((bad >> (8 * (row / 16))) & 1);
-        uint32_t step2[D / 64];
+      for (int g = 0; g < D / 64; ++g)
+        step2[g] = seen ? *reinterpret_cast<const uint32_t*>(raw + C::CODES + row * (D / 16) + g * 4) : 0u;
+      if constexpr (!VALUES) {
+        // steps under a power of two that takes the tile's largest (finite) one to [2^11, 2^12):
+        // products of 11 bits at most, exact in fp16's normal range
+        uint32_t most = 0;
 #pragma unroll
-        for (int g = 0; g < D / 64; ++g)
-          step2[g] = seen ? *reinterpret_cast<const uint32_t*>(raw + C::CODES + row * (D / 16) + g * 4) : 0u;
-        if (v == 0) {
-          // steps under a power of two that takes the tile's largest (finite) one to [2^11, 2^12):
-          // products of 11 bits at most, exact in fp16's normal range
-          uint32_t most = 0;
-#pragma unroll
-          for (int g = 0; g < D / 64; ++g) {
-            const uint32_t a = step2[g] & 0x7FFFu, b = (step2[g] >> 16) & 0x7FFFu;
-            most = max(most, max(a < 0x7F80u ? a : 0u, b < 0x7F80u ? b : 0u));
-          }
-          most = __reduce_max_sync(0xffffffffu, most);
-          uint32_t(&all)[4] = ctl->most[tiles & 1];
-          if (lane == 0) {
-            all[row / 32] = most;
-            mbar_arrive(&ctl->most_full[tiles & 1]);
-          }
-          ok = __all_sync(0xffffffffu, mbar_wait(&ctl->most_full[tiles & 1], (tiles >> 1) & 1, p.status, abort_flag));
-          if (!ok) break;
-          const uint32_t e = max(max(max(all[0], all[1]), max(all[2], all[3])) >> 7, 12u);
-          const float up = __uint_as_float((254u + 11u - e) << 23);
-          if (row == 0) {
-            ctl->factor[tiles % C::NOTES] = __uint_as_float((e - 11u) << 23);
-            ctl->bad[tiles % C::NOTES] = bad;
-          }
-#pragma unroll
-          for (int g = 0; g < D / 64; ++g) {
-            const __half2 h = __floats2half2_rn(bf16lo_to_f32(step2[g]) * up, bf16hi_to_f32(step2[g]) * up);
-            step2[g] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          expand_row<D, true>(raw, step2, tile, row);
-        } else {
-          expand_row<D, false>(raw, step2, tile, row);
+        for (int g = 0; g < D / 64; ++g) {
+          const uint32_t a = step2[g] & 0x7FFFu, b = (step2[g] >> 16) & 0x7FFFu;
+          most = max(most, max(a < 0x7F80u ? a : 0u, b < 0x7F80u ? b : 0u));
         }
-        fence_proxy_async_smem();
-        __syncwarp();
+        most = __reduce_max_sync(0xffffffffu, most);
+        uint32_t(&all)[4] = ctl->most[tiles & 1];
         if (lane == 0) {
-          mbar_arrive(&ctl->kv_full[st]);
-          mbar_arrive(&ctl->raw_empty[rs]);
+          all[row / 32] = most;
+          mbar_arrive(&ctl->most_full[tiles & 1]);
         }
+        ok = __all_sync(0xffffffffu, mbar_wait(&ctl->most_full[tiles & 1], (tiles >> 1) & 1, p.status, abort_flag));
+        if (!ok) break;
+        const uint32_t e = max(max(max(all[0], all[1]), max(all[2], all[3])) >> 7, 12u);
+        const float up = __uint_as_float((254u + 11u - e) << 23);
+        if (row == 0) {
+          ctl->factor[tiles % C::NOTES] = __uint_as_float((e - 11u) << 23);
+          ctl->bad[tiles % C::NOTES] = bad;
+        }
+#pragma unroll
+        for (int g = 0; g < D / 64; ++g) {
+          const __half2 h = __floats2half2_rn(bf16lo_to_f32(step2[g]) * up, bf16hi_to_f32(step2[g]) * up);
+          step2[g] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+      expand_row<D, !VALUES>(raw, step2, smem + C::OFF_KV + st * C::TILE, row);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&ctl->kv_full[st]);
+        mbar_arrive(&ctl->raw_empty[rs]);
       }
     }
   }
@@ -1051,7 +1047,8 @@ __global__ void __launch_bounds__(Cfg<D, Q4, TWO>::THREADS, 1) attend_kernel(con
     softmax<D, Q4, C>(p, ctl, w, tmem, (warp - 4) / 4);
   } else if constexpr (Q4) {
     setmaxnreg_dec<C::EXP>();
-    expand<D, C>(p, smem, ctl, w);
+    if (warp < 16) expand<D, false, C>(p, smem, ctl, w);
+    else expand<D, true, C>(p, smem, ctl, w);
   }
   __syncwarp();
   tc_fence_before();
