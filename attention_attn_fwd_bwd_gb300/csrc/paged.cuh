@@ -103,6 +103,9 @@ struct PagedDecodeParams : PagedCombineParams {
 };
 // Attention of a chunk (paged_attend.cu): what the kernel that joins cut work needs, what the one
 // that makes its query operands does, and the main kernel's own.
+struct PagedAttendPos {  // where a run begins: tile t of unit (b, kvh, r)
+  int b, kvh, r, t;
+};
 struct PagedAttendWork {
   PagedDev cache;
   const int32_t *first, *count;     // [B]; count may be null: every sequence has N rows
@@ -111,8 +114,9 @@ struct PagedAttendWork {
   __nv_bfloat16* out;               // [B, Hq, N, d], element strides
   int64_t o_sb, o_sh, o_sn;
   float* lse;                       // [B, Hq, N] or null
-  int ctas;
-  float* part_acc;                  // [ctas][2][256][d]: partial rows of a run's ends
+  int ctas, unit;                   // CTAs, and rows of a unit (128 or 256)
+  PagedAttendPos* bounds;           // [ctas], written by the main kernel
+  float* part_acc;                  // [ctas][2][unit][d]: partial rows of a run's ends
   float2* part_ml;                  // (max in log2 units, sum)
 };
 struct PagedQueryParams {

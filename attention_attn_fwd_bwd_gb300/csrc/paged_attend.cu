@@ -38,18 +38,20 @@ namespace afx {
 namespace {
 
 constexpr int kTile = kAttendTile;       // keys of a tile
-constexpr int kRows = 256;               // rows of a unit
 constexpr int kEnds = 256;               // keys that a unit's two ends cost: Q's load, O's way out
 constexpr float kLazy = 8.0f;            // the running maximum may lag by 2^8
 
-template <int D, bool Q4, bool TWO>
+template <int D, bool Q4, bool TWO, int ROWS_>
 struct Cfg {
   static constexpr int WARPS = Q4 ? 20 : 12;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int PANELS = D / 64;
+  static constexpr int ROWS = ROWS_;                               // of a unit: one row tile or two
   static constexpr uint32_t TILE = kTile * D * 2;                  // bytes of a K, V or Q tile
   static constexpr uint32_t QSLOT = TILE * (TWO ? 2 : 1);
-  static constexpr int STAGES = D == 64 ? 6 : TWO ? (Q4 ? 2 : 3) : Q4 ? 4 : 5;
+  static constexpr int STAGES = D == 64 ? 6 : Q4 ? (ROWS == 256 && TWO ? 2 : 4) : TWO ? 3 : 5;
+  // (K and V are expanded independently: each has stages of its own)
+  static_assert(!Q4 || STAGES % 2 == 0, "stages of K and of V");
   // Key tiles whose notes (factors, bad pages) may be in use at once, with tile t the first that a
   // softmax still reads. bf16: the ring's producer is at most STAGES ahead of V(t), which is held until
   // then. 4 bits: K(u) is written once the scores of tile u - STAGES / 2 are complete, and those of
@@ -57,8 +59,8 @@ struct Cfg {
   static constexpr int NOTES = Q4 ? STAGES / 2 + 2 : STAGES <= 3 ? 2 : STAGES <= 5 ? 3 : 4;
   // 4 bits: K or V of a tile as the cache has it, codes and then steps
   static constexpr uint32_t CODES = kTile * (D / 2), RAW = CODES + kTile * (D / 16);
-  static constexpr int RAWS = !Q4 ? 0 : D == 64 ? 6 : 3;
-  static constexpr uint32_t OFF_KV = 2 * QSLOT;
+  static constexpr int RAWS = !Q4 ? 0 : D == 128 && (TWO || ROWS == 256) ? 3 : 6;
+  static constexpr uint32_t OFF_KV = (ROWS / 128) * QSLOT;
   static constexpr uint32_t OFF_RAW = OFF_KV + STAGES * TILE;
   static constexpr uint32_t OFF_CTL = OFF_RAW + RAWS * RAW;
   // registers of the warpgroups: producer, issuer and query loaders; softmax; expanders
@@ -66,10 +68,7 @@ struct Cfg {
   static_assert(LOW + 2 * SM + (Q4 ? 2 * EXP : 0) <= (WARPS / 4) * (65536 / THREADS / 8 * 8), "registers of the launch");
 };
 
-// Boundary between two runs: tile t of unit (b, kvh, r).
-struct Pos {
-  int b, kvh, r, t;
-};
+using Pos = PagedAttendPos;
 
 // ---------------------------------------------------------------------------------------------
 // Work: starts and counts -> units -> this CTA's run
@@ -96,19 +95,19 @@ __device__ __forceinline__ Chunk chunk_of(const PagedAttendWork& p, int b) {
 }
 
 __device__ __forceinline__ int units_of(const PagedAttendWork& p, const Chunk& c) {
-  return static_cast<int>((static_cast<int64_t>(c.count) * p.g + kRows - 1) / kRows);
+  return static_cast<int>((static_cast<int64_t>(c.count) * p.g + p.unit - 1) / p.unit);
 }
 
 // What units before unit r of a (sequence, KV head) cost, in 1/g of a key: unit i reads the keys up
-// to the position of row 256 (i + 1), of which a window leaves W and what its rows spread over.
+// to the position of row (i + 1) unit, of which a window leaves W and what its rows spread over.
 __device__ __forceinline__ int64_t cost_before(const PagedAttendWork& p, const Chunk& c, int64_t r) {
-  const int64_t base = static_cast<int64_t>(c.first) * p.g + kRows;
+  const int64_t base = static_cast<int64_t>(c.first) * p.g + p.unit;
   int64_t k = r, cap = 0;
   if (p.window > 0) {
-    cap = (static_cast<int64_t>(p.window) + 1) * p.g + kRows;
-    k = cap > base ? min(r, (cap - base + kRows - 1) / kRows) : 0;
+    cap = (static_cast<int64_t>(p.window) + 1) * p.g + p.unit;
+    k = cap > base ? min(r, (cap - base + p.unit - 1) / p.unit) : 0;
   }
-  return base * k + kRows / 2 * k * (k - 1) + (r - k) * cap + r * kEnds * p.g;
+  return base * k + p.unit / 2 * k * (k - 1) + (r - k) * cap + r * kEnds * p.g;
 }
 
 // Keys [lo, hi) that a unit's rows see, their first tile and number of tiles.
@@ -116,11 +115,11 @@ struct Span {
   int lo, hi, t0, nt;
 };
 __device__ __forceinline__ Span span_of(const PagedAttendWork& p, const Chunk& c, int r) {
-  const uint32_t g = p.g, row0 = static_cast<uint32_t>(r) * kRows;
+  const uint32_t g = p.g, row0 = static_cast<uint32_t>(r) * p.unit;
   const uint32_t rows = static_cast<uint32_t>(c.count) * g;
   Span s;
   const int p0 = c.first + static_cast<int>(row0 / g);
-  s.hi = c.first + static_cast<int>((min(row0 + kRows, rows) - 1) / g) + 1;
+  s.hi = c.first + static_cast<int>((min(row0 + p.unit, rows) - 1) / g) + 1;
   s.lo = p.window > 0 ? max(0, p0 - p.window + 1) : 0;
   s.t0 = s.lo / kTile;
   s.nt = (s.hi - 1) / kTile - s.t0 + 1;
@@ -162,31 +161,23 @@ __device__ __forceinline__ int tile_at(const PagedAttendWork& p, int64_t x, int6
   return static_cast<int>((x - ends) * nt / (cost - ends));
 }
 
-// Offset x of the work that (sequence b, all KV heads) has -> the unit there, and where it begins.
-struct Found {
-  Pos pos;
-  int64_t unit, cost;  // the unit's first offset and its cost
-  int nt;
-};
-__device__ __forceinline__ Found find_in(const PagedAttendWork& p, int b, const Chunk& c, int64_t x) {
+// Offset x of the work that (sequence b, all KV heads) has -> the unit and tile there.
+__device__ __forceinline__ Pos find_in(const PagedAttendWork& p, int b, const Chunk& c, int64_t x) {
   const int n = units_of(p, c);
   const int64_t head = cost_before(p, c, n);
-  Found f;
-  f.pos.b = b;
-  f.pos.kvh = static_cast<int>(x / head);
-  const int64_t y = x - f.pos.kvh * head;
+  Pos f;
+  f.b = b;
+  f.kvh = static_cast<int>(x / head);
+  x -= f.kvh * head;
   int a = 0, z = n - 1;
-  while (a < z) {  // the last unit that begins at y or before
+  while (a < z) {  // the last unit that begins at x or before
     const int m = (a + z + 1) / 2;
-    if (cost_before(p, c, m) <= y) a = m;
+    if (cost_before(p, c, m) <= x) a = m;
     else z = m - 1;
   }
-  f.pos.r = a;
+  f.r = a;
   const int64_t u = cost_before(p, c, a);
-  f.unit = f.pos.kvh * head + u;
-  f.cost = cost_before(p, c, a + 1) - u;
-  f.nt = span_of(p, c, a).nt;
-  f.pos.t = tile_at(p, y - u, f.cost, f.nt);
+  f.t = tile_at(p, x - u, cost_before(p, c, a + 1) - u, span_of(p, c, a).nt);
   return f;
 }
 
@@ -236,11 +227,11 @@ struct Walk {
       const Span w = span_of(p, c, at.r);
       const bool stop = at.b == end.b && at.kvh == end.kvh && at.r == end.r;
       const int t1 = stop ? end.t : w.nt;
-      s.b = at.b, s.kvh = at.kvh, s.row0 = at.r * kRows, s.rows = c.count * p.g;
+      s.b = at.b, s.kvh = at.kvh, s.row0 = at.r * p.unit, s.rows = c.count * p.g;
       s.first = c.first, s.lo = w.lo, s.hi = w.hi;
       s.t = w.t0 + at.t, s.n = max(0, t1 - at.t);
       s.part = at.t > 0 ? 0 : t1 < w.nt ? 1 : -1;
-      s.kind = s.rows - s.row0 > 128 ? kTwo : s.n > 1 ? kSplit : kOne;
+      s.kind = min(s.rows - s.row0, p.unit) > 128 ? kTwo : s.n > 1 ? kSplit : kOne;
       at.t = 0;
       if (stop) {
         at.b = p.cache.B;
@@ -279,9 +270,9 @@ struct Ctl {
   };
 };
 
-template <int D, bool Q4, bool TWO>
+template <int D, bool Q4, bool TWO, int ROWS_>
 constexpr size_t smem_bytes() {
-  using C = Cfg<D, Q4, TWO>;
+  using C = Cfg<D, Q4, TWO, ROWS_>;
   return 1024 + C::OFF_CTL + sizeof(Ctl<C::NOTES, Q4>);
 }
 
@@ -605,19 +596,20 @@ __device__ __forceinline__ void load_queries(const PagedAttendParams& p, uint8_t
       if (lane == 0) mbar_arrive(&ctl->q_full[slot]);
     }
   }
-  // then, while the last products run, padding: rows [count, N) of every head. CTAs of one number
-  // modulo `groups` share sequences.
-  const int B = p.cache.B, groups = min(B, p.ctas), cta = blockIdx.x;
-  for (int b = cta % groups; b < B; b += groups) {
-    const int count = chunk_of(p, b).count, rows = p.N - count;
-    const int64_t pieces = static_cast<int64_t>(rows) * p.Hq * CH;
-    const int64_t step = static_cast<int64_t>((p.ctas - cta % groups + groups - 1) / groups) * 64;
-    for (int64_t i = static_cast<int64_t>(cta / groups) * 64 + tid; i < pieces; i += step) {
-      const uint32_t row = static_cast<uint32_t>(i / CH);  // below N Hq
-      const uint32_t h = row / static_cast<uint32_t>(rows), n = count + (row - h * rows);
-      __stcs(reinterpret_cast<uint4*>(p.out + b * p.o_sb + h * p.o_sh + n * p.o_sn + i % CH * 8), make_uint4(0, 0, 0, 0));
-      if (p.lse && i % CH == 0) p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.N + n] = kNegInf;
-    }
+  // then, while the last products run, padding: rows [count, N) of every head, 64 rows of a head at a time
+  constexpr int kPad = 64, LINES = 32 / CH;  // rows that a warp's 16-byte pieces cover
+  const int pads = (p.N + kPad - 1) / kPad;
+  const int64_t all = static_cast<int64_t>(p.cache.B) * p.Hq * pads;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 2 + tid / 32; i < all; i += 2 * p.ctas) {
+    const int64_t bh = i / pads;
+    const int b = static_cast<int>(bh / p.Hq), h = static_cast<int>(bh - static_cast<int64_t>(b) * p.Hq);
+    const int n0 = static_cast<int>(i - bh * pads) * kPad, n1 = min(p.N, n0 + kPad), from = max(n0, chunk_of(p, b).count);
+    if (from >= n1) continue;
+    int n = from + lane / CH;
+    __nv_bfloat16* out = p.out + b * p.o_sb + h * p.o_sh + n * p.o_sn + chunk * 8;
+    for (; n < n1; n += LINES, out += LINES * p.o_sn) __stcs(reinterpret_cast<uint4*>(out), make_uint4(0, 0, 0, 0));
+    if (p.lse)
+      for (n = from + lane; n < n1; n += 32) p.lse[bh * p.N + n] = kNegInf;
   }
 }
 
@@ -631,7 +623,7 @@ __device__ __forceinline__ void issue(const PagedAttendParams& p, uint8_t* smem,
   volatile int* abort_flag = &ctl->abort_flag;
   int* status = p.status;
   // descriptors as a low word, to which a product's place in the tile adds a constant, and one high word
-  static_assert(smem_bytes<D, Q4, TWO>() < (1u << 18), "descriptor address field");
+  static_assert(sizeof(T) + C::OFF_CTL + 1024 < (1u << 18), "descriptor address field");
   constexpr uint32_t dhi = desc_sw128_hi(1024);
   const uint32_t dQ = desc_sw128_lo(smem_u32(smem), 16), dK = desc_sw128_lo(smem_u32(smem + C::OFF_KV), 16);
   const uint32_t dV = desc_sw128_lo(smem_u32(smem + C::OFF_KV), kTile * 128);
@@ -641,6 +633,9 @@ __device__ __forceinline__ void issue(const PagedAttendParams& p, uint8_t* smem,
     ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, status, abort_flag));
   };
   auto wait_tile = [&](int it) { wait(&ctl->kv_full[it % C::STAGES], (it / C::STAGES) & 1); };
+  auto ready = [&](int it) {
+    return __all_sync(0xffffffffu, mbar_test(&ctl->kv_full[it % C::STAGES], (it / C::STAGES) & 1)) != 0;
+  };
   // S of slot s from row tile `qs`
   auto scores = [&](int s, int qs, int it, bool first, bool last) {
     if (first) {
@@ -685,21 +680,29 @@ __device__ __forceinline__ void issue(const PagedAttendParams& p, uint8_t* smem,
   int vt = -1;  // ring index of the V before the next K
   while (ok && have) {
     if (split) {
-      // the next tile's scores, in the other slot, go before a tile's values
+      // the next tile's scores, in the other slot, go before a tile's values, unless its K is late
       int kt = vt + 1;
       wait_tile(kt);
       scores(0, 0, kt, true, false);
       if (ok) mma_commit_warp(&ctl->kv_empty[kt % C::STAGES]);
 #pragma unroll 1
       for (int i = 0; i < nn && ok; ++i, kt += 2) {
-        if (i + 1 < nn) {
-          wait_tile(kt + 2);
-          scores(~i & 1, 0, kt + 2, false, i + 2 == nn);
-          if (ok) mma_commit_warp(&ctl->kv_empty[(kt + 2) % C::STAGES]);
+        const bool more = i + 1 < nn;
+        const bool late = more && !ready(kt + 2) && ready(kt + 1) &&
+                          __all_sync(0xffffffffu, mbar_test(&ctl->p_full[i & 1], (phases >> (2 + (i & 1))) & 1));
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {
+          if ((x == 0) == late || !more) {
+            if (!more && x == 0) continue;
+            wait_tile(kt + 1);
+            values(i & 1, kt + 1, i < 2, i >= nn - 2);
+            if (ok) mma_commit_warp(&ctl->kv_empty[(kt + 1) % C::STAGES]);
+          } else {
+            wait_tile(kt + 2);
+            scores(~i & 1, 0, kt + 2, false, i + 2 == nn);
+            if (ok) mma_commit_warp(&ctl->kv_empty[(kt + 2) % C::STAGES]);
+          }
         }
-        wait_tile(kt + 1);
-        values(i & 1, kt + 1, i < 2, i >= nn - 2);
-        if (ok) mma_commit_warp(&ctl->kv_empty[(kt + 1) % C::STAGES]);
       }
       vt += 2 * nn;
       next();
@@ -781,7 +784,7 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
       if constexpr (Q4) part = *reinterpret_cast<volatile float*>(&ctl->factor[(tiles + i) % C::NOTES]);
       const int k0 = (s.t + i) * kTile;
       const float unit = p.slopes ? 1.f : mul * part;
-      const bool edge = k0 + kTile - 1 > pos || k0 < lo || bad != 0;
+      const bool masked = __any_sync(0xffffffffu, k0 + kTile - 1 > pos || k0 < lo || bad != 0);
       // Both passes over the tile read its scores from tensor memory, CW columns at a time, in loops:
       // all 128 at once, unrolled, take registers and instruction cache that the warps of five
       // roles do not have. For the same reason tiles that need masks or a bias have code of their own.
@@ -796,10 +799,15 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
           for (int c = 0; c < CW; ++c) x[c] = __uint_as_float(xr[c]);
           if constexpr (GENERAL) {
             if (p.slopes) {
-              const float base = slope * static_cast<float>(k0 + CW * ch - pos);
+              const float base = slope * static_cast<float>(k0 + CW * ch - pos), f = mul * part;
 #pragma unroll
-              for (int c = 0; c < CW; ++c) x[c] = __fmaf_rn(slope, static_cast<float>(c), __fmaf_rn(x[c], mul * part, base));
+              for (int c = 0; c < CW; c += 2) {
+                const uint64_t y = fma2(f2_pack(slope, slope), f2_pack(c, c + 1),
+                                        fma2(f2_pack(x[c], x[c + 1]), f2_pack(f, f), f2_pack(base, base)));
+                x[c] = f2_lo(y), x[c + 1] = f2_hi(y);
+              }
             }
+            if (!masked) return;
             // a bit for each column that the row sees
             const uint32_t gone = static_cast<uint32_t>(bad >> (CW / 2 * ch));
             const int at = k0 + CW * ch, c0 = min(max(lo - at, 0), 32), c1 = min(max(pos - at, -1), 31) + 1;
@@ -863,7 +871,7 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
         const uint64_t both = add2(acc[0], acc[1]);
         l_run += f2_lo(both) + f2_hi(both);
       };
-      if (p.slopes || __any_sync(0xffffffffu, edge)) tile(std::true_type());
+      if (p.slopes || masked) tile(std::true_type());
       else tile(std::false_type());
       tmem_wait_st();
       tc_fence_before();
@@ -936,7 +944,7 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
       if (p.lse && live)
         p.lse[(static_cast<int64_t>(s.b) * p.Hq + h) * p.N + n] = any ? (m_run + log2f(l_run)) * kLn2 : kNegInf;
     } else {
-      const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + s.part) * kRows + 128 * slot + r;
+      const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + s.part) * p.unit + 128 * slot + r;
 #pragma unroll 1
       for (int ch = 0; ch < D / 32; ++ch) {
         uint32_t o[32];
@@ -957,9 +965,9 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
   }
 }
 
-template <int D, bool Q4, bool TWO>
-__global__ void __launch_bounds__(Cfg<D, Q4, TWO>::THREADS, 1) attend_kernel(const __grid_constant__ PagedAttendParams p) {
-  using C = Cfg<D, Q4, TWO>;
+template <int D, bool Q4, bool TWO, int ROWS_>
+__global__ void __launch_bounds__(Cfg<D, Q4, TWO, ROWS_>::THREADS, 1) attend_kernel(const __grid_constant__ PagedAttendParams p) {
+  using C = Cfg<D, Q4, TWO, ROWS_>;
   using T = Ctl<C::NOTES, Q4>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -1009,7 +1017,7 @@ __global__ void __launch_bounds__(Cfg<D, Q4, TWO>::THREADS, 1) attend_kernel(con
   int64_t total;
   const int64_t before = block_prefix<C::THREADS>(mine, ctl->wsum, &total);
   const Deal deal(total, p.ctas);
-#pragma unroll
+#pragma unroll 1
   for (int e = 0; e < 2; ++e) {
     const int64_t x = deal.start(blockIdx.x + e);
     if (mine > 0 && x >= before && x < before + mine) {
@@ -1018,7 +1026,7 @@ __global__ void __launch_bounds__(Cfg<D, Q4, TWO>::THREADS, 1) attend_kernel(con
         const Chunk c = chunk_of(p, b);
         const int64_t all = cost_before(p, c, units_of(p, c)) * p.cache.Hkv;
         if (y < all) {
-          (e ? ctl->end : ctl->begin) = find_in(p, b, c, y).pos;
+          (e ? ctl->end : ctl->begin) = find_in(p, b, c, y);
           break;
         }
         y -= all;
@@ -1030,6 +1038,7 @@ __global__ void __launch_bounds__(Cfg<D, Q4, TWO>::THREADS, 1) attend_kernel(con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
+  if (tid == 0) p.bounds[blockIdx.x] = ctl->begin;
   Walk w(p, ctl->begin, ctl->end, &ctl->walk[warp]);
   __syncthreads();  // (the begin's place is used for other things from here on)
   if (warp < 4) {
@@ -1065,78 +1074,41 @@ constexpr int kJoinRows = 32;
 
 template <int D>
 __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ PagedAttendWork p) {
-  __shared__ int64_t wsum[8];
-  __shared__ Found found;
-  __shared__ int64_t found_before;
   __shared__ int16_t order[kPagedMaxCtas];
   __shared__ int order_n;
+  const int tid = threadIdx.x, run = blockIdx.x + 1;
   // the stream's next kernel may come in and wait
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int tid = threadIdx.x;
-  const int B = p.cache.B, share = (B + 255) / 256;
-  if (tid == 0) found.pos.t = 0;
-  int64_t mine = 0;
-  for (int b = tid * share; b < min(B, (tid + 1) * share); ++b) {
-    const Chunk c = chunk_of(p, b);
-    mine += cost_before(p, c, units_of(p, c)) * p.cache.Hkv;
-  }
-  int64_t total;
-  const int64_t before = block_prefix<256>(mine, wsum, &total);
-  const Deal deal(total, p.ctas);
-  const int run = blockIdx.x + 1;
-  const int64_t x = run < p.ctas ? deal.start(run) : total;
-  if (mine > 0 && x >= before && x < before + mine) {
-    int64_t y = x - before;
-    for (int b = tid * share;; ++b) {
-      const Chunk c = chunk_of(p, b);
-      const int64_t all = cost_before(p, c, units_of(p, c)) * p.cache.Hkv;
-      if (y < all) {
-        found = find_in(p, b, c, y);
-        found_before = x - y;
-        break;
-      }
-      y -= all;
-    }
+  // partial rows, the runs' bounds, and the order of writes to out and lse against earlier kernels
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Pos f = run < p.ctas ? p.bounds[run] : Pos{p.cache.B, 0, 0, 0};
+  auto within = [&](const Pos& q) { return q.b == f.b && q.kvh == f.kvh && q.r == f.r && q.t > 0; };
+  if (f.b >= p.cache.B || f.t == 0 || within(p.bounds[run - 1])) return;
+  // Partial results of the unit, in the order of its tiles: run - 1's last segment, then the first ones
+  // of the runs that begin within it. (A run of less than a tile has none.)
+  for (int k = run + tid; k < p.ctas; k += 256) {
+    const Pos q = p.bounds[k];
+    const Pos z = k + 1 < p.ctas ? p.bounds[k + 1] : Pos{p.cache.B, 0, 0, 0};
+    order[k - run] = !within(q) ? -1 : !within(z) || z.t > q.t ? 1 : 0;
   }
   __syncthreads();
-  const Found f = found;
-  // Partial results of the unit, in the order of its tiles: run - 1's last segment, then the first ones
-  // of the runs that begin within it. (A run of less than a tile may have none.)
-  int parts = 0;
-  if (f.pos.t > 0) {
-    const int64_t unit = found_before + f.unit;
-    auto tile_of = [&](int k) {  // where boundary k cuts the unit
-      const int64_t z = k < p.ctas ? deal.start(k) : total;
-      return z <= unit ? 0 : z >= unit + f.cost ? f.nt : tile_at(p, z - unit, f.cost, f.nt);
-    };
-    if (tile_of(run - 1) == 0) {
-      for (int k = run - 1 + tid; k < p.ctas; k += 256) {
-        const int t0 = tile_of(k), t1 = tile_of(k + 1);
-        order[k - run + 1] = t0 == f.nt ? -1 : t0 < t1 ? 1 : 0;
-      }
-      __syncthreads();
-      if (tid == 0) {
-        int n = 0;
-        for (int k = 0; k < p.ctas - run + 1 && order[k] >= 0; ++k)
-          if (order[k]) order[n++] = static_cast<int16_t>(k);
-        order_n = n;
-      }
-      __syncthreads();
-      parts = order_n;
-    }
+  if (tid == 0) {
+    int n = 0;
+    for (int k = 0; k < p.ctas - run && order[k] >= 0; ++k)
+      if (order[k]) order[n++] = static_cast<int16_t>(k + 1);
+    order_n = n;
   }
-  // partial rows, and the order of writes to out and lse against earlier kernels, from here on
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (parts == 0) return;
-  const Chunk c = chunk_of(p, f.pos.b);
+  __syncthreads();
+  const int parts = order_n + 1;
+  const Chunk c = chunk_of(p, f.b);
   constexpr int L = D / 4;  // threads of a row
   const int col = tid % L * 4;
   for (int i = tid / L; i < kJoinRows; i += 256 / L) {
-    const int r = blockIdx.y * kJoinRows + i, row = f.pos.r * kRows + r;
-    if (row >= c.count * p.g) break;
+    const int r = blockIdx.y * kJoinRows + i, row = f.r * p.unit + r;
+    if (r >= p.unit || row >= c.count * p.g) break;
     auto at = [&](int i) {
-      const int k = order[i];
-      return (static_cast<int64_t>(run - 1 + k) * 2 + (k == 0 ? 1 : 0)) * kRows + r;
+      const int k = i == 0 ? 0 : order[i - 1];
+      return (static_cast<int64_t>(run - 1 + k) * 2 + (k == 0 ? 1 : 0)) * p.unit + r;
     };
     float mx = kNegInf;
     for (int k = 0; k < parts; ++k) mx = fmaxf(mx, p.part_ml[at(k)].x);
@@ -1152,10 +1124,10 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     }
     const bool any = !(sum == 0.f);
     const float inv = any ? 1.f / sum : 0.f;
-    const int n = row / p.g, h = f.pos.kvh * p.g + row % p.g;
-    *reinterpret_cast<uint2*>(p.out + f.pos.b * p.o_sb + h * p.o_sh + n * p.o_sn + col) =
+    const int n = row / p.g, h = f.kvh * p.g + row % p.g;
+    *reinterpret_cast<uint2*>(p.out + f.b * p.o_sb + h * p.o_sh + n * p.o_sn + col) =
         any ? make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv)) : make_uint2(0, 0);
-    if (p.lse && col == 0) p.lse[(static_cast<int64_t>(f.pos.b) * p.Hq + h) * p.N + n] = any ? (mx + log2f(sum)) * kLn2 : kNegInf;
+    if (p.lse && col == 0) p.lse[(static_cast<int64_t>(f.b) * p.Hq + h) * p.N + n] = any ? (mx + log2f(sum)) * kLn2 : kNegInf;
   }
 }
 
@@ -1281,12 +1253,12 @@ cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, int threads, size_t smem, 
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int D, bool Q4, bool TWO>
+template <int D, bool Q4, bool TWO, int ROWS_>
 cudaError_t launch(const PagedAttendParams& p, cudaStream_t stream) {
-  using C = Cfg<D, Q4, TWO>;
-  constexpr size_t bytes = smem_bytes<D, Q4, TWO>();
+  using C = Cfg<D, Q4, TWO, ROWS_>;
+  constexpr size_t bytes = smem_bytes<D, Q4, TWO, ROWS_>();
   static_assert(bytes <= 232448, "shared memory");
-  auto kern = attend_kernel<D, Q4, TWO>;
+  auto kern = attend_kernel<D, Q4, TWO, ROWS_>;
   static std::atomic<uint64_t> ready;  // devices that the kernel's shared memory was allowed on
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1299,20 +1271,24 @@ cudaError_t launch(const PagedAttendParams& p, cudaStream_t stream) {
   }
   e = launch_pdl<PagedAttendParams>(kern, dim3(p.ctas), C::THREADS, bytes, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl<PagedAttendWork>(attend_join_kernel<D>, dim3(p.ctas, kRows / kJoinRows), 256, 0, stream, p);
+  return launch_pdl<PagedAttendWork>(attend_join_kernel<D>, dim3(p.ctas, C::ROWS / kJoinRows), 256, 0, stream, p);
 }
 
-size_t part_bytes(int d) {
-  return (size_t)std::min(paged_sm_count(), kPagedMaxCtas) * 2 * kRows * (d * sizeof(float) + sizeof(float2));
+// Rows of a unit. Two row tiles share the keys that are read (and, 4 bits, expanded); where a 4-bit
+// cache's calls have one row tile anyway, shared memory has more of the keys instead.
+int unit_rows(int format, int N, int g) { return format == kPagedQ4 && static_cast<int64_t>(N) * g <= 128 ? 128 : 256; }
+
+size_t part_bytes(int d, int unit) {
+  return (size_t)std::min(paged_sm_count(), kPagedMaxCtas) * 2 * unit * (d * sizeof(float) + sizeof(float2)) +
+         kPagedMaxCtas * sizeof(Pos);
 }
 
 }  // namespace
 
 // Partial rows of each CTA; where q is rotated or the cache has 4 bits, its parts and their factors.
 size_t paged_attend_workspace(int B, int Hq, int Hkv, int N, int d, int format, bool rope) {
-  (void)Hkv;
   const size_t rows = (size_t)B * Hq * N;
-  size_t n = part_bytes(d);
+  size_t n = part_bytes(d, unit_rows(format, N, Hq / Hkv));
   if (rope || format == kPagedQ4) n += rows * d * 2 * (rope ? 2 : 1);
   if (format == kPagedQ4) n += rows * sizeof(float);
   return n;
@@ -1322,8 +1298,10 @@ cudaError_t launch_paged_attend(const PagedAttendCall& c, int d, int format, cud
   PagedAttendParams p = c.p;
   const bool q4 = format == kPagedQ4, two = c.rope;
   p.ctas = std::min(paged_sm_count(), kPagedMaxCtas);
-  p.part_acc = static_cast<float*>(c.workspace);
-  p.part_ml = reinterpret_cast<float2*>(p.part_acc + (int64_t)p.ctas * 2 * kRows * d);
+  p.unit = unit_rows(format, p.N, p.g);
+  p.bounds = static_cast<Pos*>(c.workspace);
+  p.part_acc = reinterpret_cast<float*>(p.bounds + kPagedMaxCtas);
+  p.part_ml = reinterpret_cast<float2*>(p.part_acc + (int64_t)p.ctas * 2 * p.unit * d);
   if (two || q4) {
     PagedQueryParams q;
     q.q = reinterpret_cast<const uint8_t*>(p.q);
@@ -1336,7 +1314,7 @@ cudaError_t launch_paged_attend(const PagedAttendCall& c, int d, int format, cud
     q.rows = (int64_t)p.cache.B * p.N;
     q.div_n = p.N > 1 ? ~0ull / p.N + 1 : 0;
     const int64_t plane = q.rows * p.Hq * d;
-    q.hi = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(c.workspace) + part_bytes(d));
+    q.hi = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(c.workspace) + part_bytes(d, p.unit));
     q.lo = two ? q.hi + plane : nullptr;
     q.factor = reinterpret_cast<float*>(q.hi + plane * (two ? 2 : 1));
     q.freqs = c.freqs;
@@ -1358,12 +1336,16 @@ cudaError_t launch_paged_attend(const PagedAttendCall& c, int d, int format, cud
     p.q_lo = plane;
     p.factor = q.factor;
   }
-  if (q4) {
-    if (d == 128) return two ? launch<128, true, true>(p, stream) : launch<128, true, false>(p, stream);
-    return two ? launch<64, true, true>(p, stream) : launch<64, true, false>(p, stream);
+  if (q4 && p.unit == 128) {
+    if (d == 128) return two ? launch<128, true, true, 128>(p, stream) : launch<128, true, false, 128>(p, stream);
+    return two ? launch<64, true, true, 128>(p, stream) : launch<64, true, false, 128>(p, stream);
   }
-  if (d == 128) return two ? launch<128, false, true>(p, stream) : launch<128, false, false>(p, stream);
-  return two ? launch<64, false, true>(p, stream) : launch<64, false, false>(p, stream);
+  if (q4) {
+    if (d == 128) return two ? launch<128, true, true, 256>(p, stream) : launch<128, true, false, 256>(p, stream);
+    return two ? launch<64, true, true, 256>(p, stream) : launch<64, true, false, 256>(p, stream);
+  }
+  if (d == 128) return two ? launch<128, false, true, 256>(p, stream) : launch<128, false, false, 256>(p, stream);
+  return two ? launch<64, false, true, 256>(p, stream) : launch<64, false, false, 256>(p, stream);
 }
 
 }  // namespace afx
