@@ -114,7 +114,8 @@ struct PagedAttendWork {
   __nv_bfloat16* out;               // [B, Hq, N, d], element strides
   int64_t o_sb, o_sh, o_sn;
   float* lse;                       // [B, Hq, N] or null
-  int ctas, unit;                   // CTAs, and rows of a unit (128 or 256)
+  int ctas, unit, unit_log2;        // CTAs, and rows of a unit (128 or 256)
+  uint64_t div_g;                   // ceil(2^63 / g)
   PagedAttendPos* bounds;           // [ctas], written by the main kernel
   float* part_acc;                  // [ctas][2][unit][d]: partial rows of a run's ends
   float2* part_ml;                  // (max in log2 units, sum)

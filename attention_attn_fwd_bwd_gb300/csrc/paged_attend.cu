@@ -95,7 +95,7 @@ __device__ __forceinline__ Chunk chunk_of(const PagedAttendWork& p, int b) {
 }
 
 __device__ __forceinline__ int units_of(const PagedAttendWork& p, const Chunk& c) {
-  return static_cast<int>((static_cast<int64_t>(c.count) * p.g + p.unit - 1) / p.unit);
+  return static_cast<int>((static_cast<int64_t>(c.count) * p.g + p.unit - 1) >> p.unit_log2);
 }
 
 // What units before unit r of a (sequence, KV head) cost, in 1/g of a key: unit i reads the keys up
@@ -105,9 +105,15 @@ __device__ __forceinline__ int64_t cost_before(const PagedAttendWork& p, const C
   int64_t k = r, cap = 0;
   if (p.window > 0) {
     cap = (static_cast<int64_t>(p.window) + 1) * p.g + p.unit;
-    k = cap > base ? min(r, (cap - base + p.unit - 1) / p.unit) : 0;
+    k = cap > base ? min(r, (cap - base + p.unit - 1) >> p.unit_log2) : 0;
   }
   return base * k + p.unit / 2 * k * (k - 1) + (r - k) * cap + r * kEnds * p.g;
+}
+
+// row / g for row < 2^30: row (M g - 2^63) < 2^30 g keeps the error of the rounded-up reciprocal M
+// below 1 / g.
+__device__ __forceinline__ int row_div(const PagedAttendWork& p, int row) {
+  return static_cast<int>(__umul64hi(2ull * static_cast<uint32_t>(row), p.div_g));
 }
 
 // Keys [lo, hi) that a unit's rows see, their first tile and number of tiles.
@@ -115,11 +121,10 @@ struct Span {
   int lo, hi, t0, nt;
 };
 __device__ __forceinline__ Span span_of(const PagedAttendWork& p, const Chunk& c, int r) {
-  const uint32_t g = p.g, row0 = static_cast<uint32_t>(r) * p.unit;
-  const uint32_t rows = static_cast<uint32_t>(c.count) * g;
+  const int row0 = r << p.unit_log2, rows = c.count * p.g;
   Span s;
-  const int p0 = c.first + static_cast<int>(row0 / g);
-  s.hi = c.first + static_cast<int>((min(row0 + p.unit, rows) - 1) / g) + 1;
+  const int p0 = c.first + row_div(p, row0);
+  s.hi = c.first + row_div(p, min(row0 + p.unit, rows) - 1) + 1;
   s.lo = p.window > 0 ? max(0, p0 - p.window + 1) : 0;
   s.t0 = s.lo / kTile;
   s.nt = (s.hi - 1) / kTile - s.t0 + 1;
@@ -222,12 +227,17 @@ struct Walk {
     Seg& s = st->seg;
     Pos at = st->at;
     s.n = 0;
+#pragma unroll 1
     while (at.b < p.cache.B) {
       const Chunk c = chunk_of(p, at.b);
+      if (c.count == 0) {
+        ++at.b;
+        continue;
+      }
       const Span w = span_of(p, c, at.r);
       const bool stop = at.b == end.b && at.kvh == end.kvh && at.r == end.r;
       const int t1 = stop ? end.t : w.nt;
-      s.b = at.b, s.kvh = at.kvh, s.row0 = at.r * p.unit, s.rows = c.count * p.g;
+      s.b = at.b, s.kvh = at.kvh, s.row0 = at.r << p.unit_log2, s.rows = c.count * p.g;
       s.first = c.first, s.lo = w.lo, s.hi = w.hi;
       s.t = w.t0 + at.t, s.n = max(0, t1 - at.t);
       s.part = at.t > 0 ? 0 : t1 < w.nt ? 1 : -1;
@@ -239,8 +249,7 @@ struct Walk {
         at.r = 0;
         if (++at.kvh == p.cache.Hkv) {
           at.kvh = 0;
-          do ++at.b;
-          while (at.b < p.cache.B && chunk_of(p, at.b).count == 0);
+          ++at.b;
         }
       }
       if (s.n > 0) break;
@@ -311,8 +320,10 @@ __device__ __forceinline__ void produce(const PagedAttendParams& p, uint8_t* sme
       const uint32_t loads = __ballot_sync(0xffffffffu, page >= 0);
       if (lane == 0) {
         uint64_t bad = 0;
+#pragma unroll 1
         for (uint32_t m = none; m; m &= m - 1) {
           const int f = (__ffs(m) - 1) / C::PANELS;
+#pragma unroll 1
           for (int x = 0; x < frag / 16; ++x) bad |= 0xFFull << (8 * (f * (frag / 16) + x));
         }
         ctl->bad[tiles % C::NOTES] = bad;
@@ -346,6 +357,7 @@ __device__ __forceinline__ void produce(const PagedAttendParams& p, uint8_t* sme
         if (mine && !some)
           tma_load_4d(dst + panel * (kTile * 128) + grp * 2048, &p.tmV16, &ctl->kv_full[st], panel * 64, slot, s.kvh,
                       page >= 0 ? page : cache.num_pages);
+#pragma unroll 1
         for (uint32_t m = __ballot_sync(0xffffffffu, some); m; m &= m - 1) {
           const int src = __ffs(m) - 1;
           const int a2 = __shfl_sync(0xffffffffu, a, src), pg = __shfl_sync(0xffffffffu, page, src);
@@ -361,6 +373,7 @@ __device__ __forceinline__ void produce(const PagedAttendParams& p, uint8_t* sme
     }
   }
   // no copy may be in flight when the CTA ends
+#pragma unroll 1
   for (int i = max(0, it - C::STAGES); i < it; ++i)
     mbar_wait(&ctl->kv_full[i % C::STAGES], (i / C::STAGES) & 1, p.status, nullptr);
 }
@@ -393,14 +406,16 @@ __device__ __forceinline__ void produce4(const PagedAttendParams& p, uint8_t* sm
       if (seen) page = page_at(cache, s.b, key, &slot);
       const uint32_t none = __ballot_sync(0xffffffffu, seen && page < 0), loads = __ballot_sync(0xffffffffu, page >= 0);
       if (none && lane == 0) atomicOr(p.status, kDevPageRange);
-#pragma unroll
+#pragma unroll 1
       for (int v = 0; v < 2; ++v, ++it) {
         const int st = it % C::RAWS;
         ok = ok && __all_sync(0xffffffffu, mbar_wait(&ctl->raw_empty[st], ((it / C::RAWS) & 1) ^ 1, p.status, abort_flag));
         if (!ok) break;
         if (lane == 0) {
           uint64_t bad = 0;
+#pragma unroll 1
           for (uint32_t m = none; m; m &= m - 1)
+#pragma unroll 1
             for (int x = 0; x < frag / 16; ++x) bad |= 0xFFull << (8 * ((__ffs(m) - 1) * (frag / 16) + x));
           ctl->raw_bad[st] = bad;
           mbar_arrive_expect_tx(&ctl->raw_full[st], __popc(loads) * frag * (D / 2 + D / 16));
@@ -418,6 +433,7 @@ __device__ __forceinline__ void produce4(const PagedAttendParams& p, uint8_t* sm
     }
   }
   // no copy may be in flight when the CTA ends
+#pragma unroll 1
   for (int i = max(0, it - C::RAWS); i < it; ++i) mbar_wait(&ctl->raw_full[i % C::RAWS], (i / C::RAWS) & 1, p.status, nullptr);
 }
 
@@ -564,24 +580,24 @@ __device__ __forceinline__ void load_queries(const PagedAttendParams& p, uint8_t
   const int tid = threadIdx.x - 64, lane = threadIdx.x % 32;
   const int chunk = tid % CH;
   volatile int* abort_flag = &ctl->abort_flag;
-  int used[2] = {0, 0};
+  uint32_t used = 0;  // bit s: phase of q_empty[s]
   bool ok = true;
   const Seg* seg;
   while (ok && (seg = w.next())) {
     const Seg& s = *seg;
-#pragma unroll
+#pragma unroll 1
     for (int slot = 0; slot < 2; ++slot) {
       const int r0 = s.row0 + 128 * slot;
       if (slot > 0 && s.kind != kTwo) continue;
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(&ctl->q_empty[slot], (used[slot] & 1) ^ 1, p.status, abort_flag));
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(&ctl->q_empty[slot], ((used >> slot) & 1) ^ 1, p.status, abort_flag));
       if (!ok) break;
-      ++used[slot];
+      used ^= 1u << slot;
       const uint32_t to = smem_u32(smem + slot * C::QSLOT) + (chunk >> 3) * (kTile * 128);
       const __nv_bfloat16* from = p.q + s.b * p.q_sb + static_cast<int64_t>(s.kvh) * p.g * p.q_sh + chunk * 8;
       constexpr int STEP = 64 / CH;
-      const int g = p.g, dn = STEP / g, dj = STEP - dn * g, last = s.rows - r0;  // rows behind the last are not used
-      int n = (r0 + tid / CH) / g, j = r0 + tid / CH - n * g;
-#pragma unroll 4
+      const int g = p.g, dn = row_div(p, STEP), dj = STEP - dn * g, last = s.rows - r0;  // rows behind the last are not used
+      int n = row_div(p, r0 + tid / CH), j = r0 + tid / CH - n * g;
+#pragma unroll 2
       for (int r = tid / CH; r < min(128, last); r += STEP) {
         const uint32_t dst = to + sw128_offset(r, chunk & 7);
         const __nv_bfloat16* x = from + n * p.q_sn + j * p.q_sh;
@@ -607,8 +623,10 @@ __device__ __forceinline__ void load_queries(const PagedAttendParams& p, uint8_t
     if (from >= n1) continue;
     int n = from + lane / CH;
     __nv_bfloat16* out = p.out + b * p.o_sb + h * p.o_sh + n * p.o_sn + chunk * 8;
+#pragma unroll 1
     for (; n < n1; n += LINES, out += LINES * p.o_sn) __stcs(reinterpret_cast<uint4*>(out), make_uint4(0, 0, 0, 0));
     if (p.lse)
+#pragma unroll 1
       for (n = from + lane; n < n1; n += 32) p.lse[bh * p.N + n] = kNegInf;
   }
 }
@@ -761,9 +779,9 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
     }
     const int row = s.row0 + (split ? 0 : 128 * slot) + r;
     const bool live = row < s.rows;
-    const uint32_t n = static_cast<uint32_t>(min(row, s.rows - 1)) / static_cast<uint32_t>(p.g);
-    const int h = s.kvh * p.g + (min(row, s.rows - 1) - static_cast<int>(n) * p.g);
-    const int pos = live ? s.first + static_cast<int>(n) : INT_MAX;  // a row behind the last needs no mask
+    const int n = row_div(p, min(row, s.rows - 1));
+    const int h = s.kvh * p.g + (min(row, s.rows - 1) - n * p.g);
+    const int pos = live ? s.first + n : INT_MAX;  // a row behind the last needs no mask
     const bool some = __any_sync(0xffffffffu, live);
     const int lo = p.window > 0 && live ? max(0, pos - p.window + 1) : 0;
     float mul = p.scale_log2;
@@ -1009,6 +1027,7 @@ __global__ void __launch_bounds__(Cfg<D, Q4, TWO, ROWS_>::THREADS, 1) attend_ker
   // thread j sums the work of its share of the sequences
   const int B = p.cache.B, share = (B + C::THREADS - 1) / C::THREADS;
   int64_t mine = 0;
+#pragma unroll 1
   for (int b = tid * share; b < min(B, (tid + 1) * share); ++b) {
     const Chunk c = chunk_of(p, b);
     if (blockIdx.x == 0 && c.bad) atomicOr(p.status, kDevPageRange);
@@ -1022,6 +1041,7 @@ __global__ void __launch_bounds__(Cfg<D, Q4, TWO, ROWS_>::THREADS, 1) attend_ker
     const int64_t x = deal.start(blockIdx.x + e);
     if (mine > 0 && x >= before && x < before + mine) {
       int64_t y = x - before;
+#pragma unroll 1
       for (int b = tid * share;; ++b) {
         const Chunk c = chunk_of(p, b);
         const int64_t all = cost_before(p, c, units_of(p, c)) * p.cache.Hkv;
@@ -1104,7 +1124,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   constexpr int L = D / 4;  // threads of a row
   const int col = tid % L * 4;
   for (int i = tid / L; i < kJoinRows; i += 256 / L) {
-    const int r = blockIdx.y * kJoinRows + i, row = f.r * p.unit + r;
+    const int r = blockIdx.y * kJoinRows + i, row = (f.r << p.unit_log2) + r;
     if (r >= p.unit || row >= c.count * p.g) break;
     auto at = [&](int i) {
       const int k = i == 0 ? 0 : order[i - 1];
@@ -1124,7 +1144,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     }
     const bool any = !(sum == 0.f);
     const float inv = any ? 1.f / sum : 0.f;
-    const int n = row / p.g, h = f.kvh * p.g + row % p.g;
+    const int n = row_div(p, row), h = f.kvh * p.g + (row - n * p.g);
     *reinterpret_cast<uint2*>(p.out + f.b * p.o_sb + h * p.o_sh + n * p.o_sn + col) =
         any ? make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv)) : make_uint2(0, 0);
     if (p.lse && col == 0) p.lse[(static_cast<int64_t>(f.b) * p.Hq + h) * p.N + n] = any ? (mx + log2f(sum)) * kLn2 : kNegInf;
@@ -1299,6 +1319,8 @@ cudaError_t launch_paged_attend(const PagedAttendCall& c, int d, int format, cud
   const bool q4 = format == kPagedQ4, two = c.rope;
   p.ctas = std::min(paged_sm_count(), kPagedMaxCtas);
   p.unit = unit_rows(format, p.N, p.g);
+  p.unit_log2 = p.unit == 128 ? 7 : 8;
+  p.div_g = ((1ull << 63) + p.g - 1) / p.g;
   p.bounds = static_cast<Pos*>(c.workspace);
   p.part_acc = reinterpret_cast<float*>(p.bounds + kPagedMaxCtas);
   p.part_ml = reinterpret_cast<float2*>(p.part_acc + (int64_t)p.ctas * 2 * p.unit * d);
