@@ -64,7 +64,7 @@ struct Cfg {
   static constexpr uint32_t OFF_RAW = OFF_KV + STAGES * TILE;
   static constexpr uint32_t OFF_CTL = OFF_RAW + RAWS * RAW;
   // registers of the warpgroups: producer, issuer and query loaders; softmax; expanders
-  static constexpr uint32_t LOW = Q4 ? 64 : 104, SM = Q4 ? 128 : 200, EXP = 80;
+  static constexpr uint32_t LOW = Q4 ? 80 : 104, SM = Q4 ? 120 : 200, EXP = 80;
   static_assert(LOW + 2 * SM + (Q4 ? 2 * EXP : 0) <= (WARPS / 4) * (65536 / THREADS / 8 * 8), "registers of the launch");
 };
 
@@ -654,6 +654,20 @@ __device__ __forceinline__ void issue(const PagedAttendParams& p, uint8_t* smem,
   auto ready = [&](int it) {
     return __all_sync(0xffffffffu, mbar_test(&ctl->kv_full[it % C::STAGES], (it / C::STAGES) & 1)) != 0;
   };
+  // A product, issued by one thread. 4 bits: the thread is elected once for all products of a tile,
+  // and their bases are made the warp's, which takes a tenth of the instructions (instruction fetches
+  // bound that kernel: the calls of 8 tokens over 16 contexts 0.176 and 0.15 ms). bf16: elected for each;
+  // products that come faster hold up the softmax's reads of tensor memory (1024 tokens over 16k keys
+  // 0.238 and 0.245 ms).
+  auto ss = [&](auto acc, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+    if constexpr (Q4) mma_ss_w<decltype(acc)::value>(d, a, b, dhi, idesc);
+    else mma_ss_warp<decltype(acc)::value>(d, a, b, dhi, idesc);
+  };
+  auto ts = [&](auto acc, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+    if constexpr (Q4) mma_ts_w<decltype(acc)::value>(d, a, b, dhi, idesc);
+    else mma_ts_warp<decltype(acc)::value>(d, a, b, dhi, idesc);
+  };
+  auto base = [&](uint32_t x) { return Q4 ? __shfl_sync(0xffffffffu, x, 0) : x; };
   // S of slot s from row tile `qs`
   auto scores = [&](int s, int qs, int it, bool first, bool last) {
     if (first) {
@@ -662,26 +676,38 @@ __device__ __forceinline__ void issue(const PagedAttendParams& p, uint8_t* smem,
     }
     if (!ok) return;
     tc_fence_after();
-    const uint32_t q = dQ + qs * (C::QSLOT >> 4), k = dK + (it % C::STAGES) * (C::TILE >> 4);
-    mma_ss_warp<0>(tmem + 128 * s, q, k, dhi, idesc_s);
+    const uint32_t q = base(dQ + qs * (C::QSLOT >> 4)), k = base(dK + (it % C::STAGES) * (C::TILE >> 4)), d = base(tmem + 128 * s);
+    if (!Q4 || elect_one()) {
+      ss(std::integral_constant<int, 0>(), d, q, k, idesc_s);
 #pragma unroll
-    for (int kk = 1; kk < (TWO ? 2 : 1) * (D / 16); ++kk) {
-      const uint32_t off = ((kk % (D / 16)) >> 2) * (kTile * 128) + (kk & 3) * 32;
-      mma_ss_warp<1>(tmem + 128 * s, q + (((kk / (D / 16)) * C::TILE + off) >> 4), k + (off >> 4), dhi, idesc_s);
+      for (int kk = 1; kk < (TWO ? 2 : 1) * (D / 16); ++kk) {
+        const uint32_t off = ((kk % (D / 16)) >> 2) * (kTile * 128) + (kk & 3) * 32;
+        ss(std::integral_constant<int, 1>(), d, q + (((kk / (D / 16)) * C::TILE + off) >> 4), k + (off >> 4), idesc_s);
+      }
     }
+    if (Q4) __syncwarp();
     mma_commit_warp(&ctl->s_full[s]);
     if (last) mma_commit_warp(&ctl->q_empty[qs]);
   };
   auto values = [&](int s, int it, bool first, bool last) {
-    const uint32_t v = dV + (it % C::STAGES) * (C::TILE >> 4), o = tmem + 256 + 128 * s, w = tmem + 128 * s;
     wait(&ctl->p_full[s], (phases >> (2 + s)) & 1);
     phases ^= 4u << s;
     if (!ok) return;
     tc_fence_after();
-    if (first) mma_ts_warp<0>(o, w, v, dhi, idesc_o);
-    else mma_ts_warp<1>(o, w, v, dhi, idesc_o);
+    const uint32_t v = base(dV + (it % C::STAGES) * (C::TILE >> 4)), w = base(tmem + 128 * s), o = w + 256;
+    if (!Q4 || elect_one()) {
+      if (first) ts(std::integral_constant<int, 0>(), o, w, v, idesc_o);
+      else ts(std::integral_constant<int, 1>(), o, w, v, idesc_o);
+      // 4 bits: of every 32 columns, 16 of weights and 16 of what their rounding left
+      if constexpr (Q4) ts(std::integral_constant<int, 1>(), o, w + 16, v, idesc_o);
 #pragma unroll
-    for (int kk = 1; kk < 8; ++kk) mma_ts_warp<1>(o, w + kk * 8, v + kk * (2048 >> 4), dhi, idesc_o);
+      for (int kk = 1; kk < 8; ++kk) {
+        const uint32_t at = w + (Q4 ? kk / 2 * 32 + kk % 2 * 8 : kk * 8);
+        ts(std::integral_constant<int, 1>(), o, at, v + kk * (2048 >> 4), idesc_o);
+        if constexpr (Q4) ts(std::integral_constant<int, 1>(), o, at + 16, v + kk * (2048 >> 4), idesc_o);
+      }
+    }
+    if (Q4) __syncwarp();
     if (last) mma_commit_warp(&ctl->o_full[s]);
   };
   // the next segment's tiles and kind (as votes, so that branches on them are known to be the warp's)
@@ -876,15 +902,25 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
         for (int ch = 0; ch < kTile / CW; ++ch) {
           float x[CW];
           load(ch, x);
-          uint32_t pk[CW / 2];
+          uint32_t pk[CW / 2], rest[Q4 ? CW / 2 : 1] = {};
 #pragma unroll
           for (int c = 0; c < CW / 2; ++c) {
             const uint64_t a = fma2(f2_pack(x[2 * c], x[2 * c + 1]), u2, nb2);
-            const float p0 = ex2_approx(f2_lo(a)), p1 = ex2_approx(f2_hi(a));
-            acc[c & 1] = add2(acc[c & 1], f2_pack(p0, p1));
-            pk[c] = pack_bf16x2(p0, p1);
+            const uint64_t w = f2_pack(ex2_approx(f2_lo(a)), ex2_approx(f2_hi(a)));
+            acc[c & 1] = add2(acc[c & 1], w);
+            pk[c] = pack_bf16x2(f2_lo(w), f2_hi(w));
+            if constexpr (Q4) {
+              const uint64_t r = add2(w, bf16x2_to_f2(pk[c] ^ 0x80008000u));
+              rest[c] = pack_bf16x2(f2_lo(r), f2_hi(r));
+            }
           }
-          tmem_st16(tS + CW / 2 * ch, pk);  // over scores that are weighed already
+          // over scores that are weighed already
+          if constexpr (Q4) {
+            tmem_st16(tS + CW * ch, pk);
+            tmem_st16(tS + CW * ch + CW / 2, rest);
+          } else {
+            tmem_st16(tS + CW / 2 * ch, pk);
+          }
         }
         const uint64_t both = add2(acc[0], acc[1]);
         l_run += f2_lo(both) + f2_hi(both);
