@@ -115,6 +115,7 @@ struct PagedAttendWork {
   int64_t o_sb, o_sh, o_sn;
   float* lse;                       // [B, Hq, N] or null
   int ctas, unit, unit_log2;        // CTAs, and rows of a unit (128 or 256)
+  int half_cost;                    // of a unit of one row tile among those of two, in quarters
   uint64_t div_g;                   // ceil(2^63 / g)
   PagedAttendPos* bounds;           // [ctas], written by the main kernel
   float* part_acc;                  // [ctas][2][unit][d]: partial rows of a run's ends

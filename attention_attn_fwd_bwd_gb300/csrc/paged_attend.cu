@@ -109,6 +109,16 @@ __device__ __forceinline__ int64_t cost_before(const PagedAttendWork& p, const C
   }
   return base * k + p.unit / 2 * k * (k - 1) + (r - k) * cap + r * kEnds * p.g;
 }
+// What unit r of n costs: a last one of half the rows less for each key (p.half_cost quarters).
+__device__ __forceinline__ int64_t cost_of(const PagedAttendWork& p, const Chunk& c, int r, int n) {
+  const int64_t all = cost_before(p, c, r + 1) - cost_before(p, c, r), ends = static_cast<int64_t>(kEnds) * p.g;
+  return r == n - 1 && p.unit > 128 && c.count * p.g - (r << p.unit_log2) <= 128 ? ends + (all - ends) / 4 * p.half_cost : all;
+}
+// All units of a (sequence, KV head).
+__device__ __forceinline__ int64_t cost_all(const PagedAttendWork& p, const Chunk& c) {
+  const int n = units_of(p, c);
+  return n ? cost_before(p, c, n - 1) + cost_of(p, c, n - 1, n) : 0;
+}
 
 // row / g for row < 2^30: row (M g - 2^63) < 2^30 g keeps the error of the rounded-up reciprocal M
 // below 1 / g.
@@ -169,7 +179,7 @@ __device__ __forceinline__ int tile_at(const PagedAttendWork& p, int64_t x, int6
 // Offset x of the work that (sequence b, all KV heads) has -> the unit and tile there.
 __device__ __forceinline__ Pos find_in(const PagedAttendWork& p, int b, const Chunk& c, int64_t x) {
   const int n = units_of(p, c);
-  const int64_t head = cost_before(p, c, n);
+  const int64_t head = cost_all(p, c);
   Pos f;
   f.b = b;
   f.kvh = static_cast<int>(x / head);
@@ -182,7 +192,7 @@ __device__ __forceinline__ Pos find_in(const PagedAttendWork& p, int b, const Ch
   }
   f.r = a;
   const int64_t u = cost_before(p, c, a);
-  f.t = tile_at(p, x - u, cost_before(p, c, a + 1) - u, span_of(p, c, a).nt);
+  f.t = tile_at(p, x - u, cost_of(p, c, a, n), span_of(p, c, a).nt);
   return f;
 }
 
@@ -829,29 +839,31 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
       const int k0 = (s.t + i) * kTile;
       const float unit = p.slopes ? 1.f : mul * part;
       const bool masked = __any_sync(0xffffffffu, k0 + kTile - 1 > pos || k0 < lo || bad != 0);
-      // Both passes over the tile read its scores from tensor memory, CW columns at a time, in loops:
-      // all 128 at once, unrolled, take registers and instruction cache that the warps of five
-      // roles do not have. For the same reason tiles that need masks or a bias have code of their own.
-      auto tile = [&](auto general) {
-        constexpr bool GENERAL = decltype(general)::value;
-        // scores of columns CW ch .. of the row, in units of 1 / unit
-        auto load = [&](int ch, float (&x)[CW]) {
-          uint32_t xr[CW];
-          tmem_ld32(tS + CW * ch, xr);
-          tmem_wait_ld_dep(xr);
+      // Passes over the tile read its scores from tensor memory, CW columns at a time, in loops: all 128
+      // at once, unrolled, take registers and instruction cache that the warps of five roles do not have.
+      auto scores = [&](int ch, float (&x)[CW]) {
+        uint32_t xr[CW];
+        tmem_ld32(tS + CW * ch, xr);
+        tmem_wait_ld_dep(xr);
 #pragma unroll
-          for (int c = 0; c < CW; ++c) x[c] = __uint_as_float(xr[c]);
-          if constexpr (GENERAL) {
-            if (p.slopes) {
-              const float base = slope * static_cast<float>(k0 + CW * ch - pos), f = mul * part;
+        for (int c = 0; c < CW; ++c) x[c] = __uint_as_float(xr[c]);
+      };
+      if (p.slopes || masked) {
+        // a pass of its own writes them back with the bias and the mask
+#pragma unroll 1
+        for (int ch = 0; ch < kTile / CW; ++ch) {
+          float x[CW];
+          scores(ch, x);
+          if (p.slopes) {
+            const float from = slope * static_cast<float>(k0 + CW * ch - pos), f = mul * part;
 #pragma unroll
-              for (int c = 0; c < CW; c += 2) {
-                const uint64_t y = fma2(f2_pack(slope, slope), f2_pack(c, c + 1),
-                                        fma2(f2_pack(x[c], x[c + 1]), f2_pack(f, f), f2_pack(base, base)));
-                x[c] = f2_lo(y), x[c + 1] = f2_hi(y);
-              }
+            for (int c = 0; c < CW; c += 2) {
+              const uint64_t y = fma2(f2_pack(slope, slope), f2_pack(c, c + 1),
+                                      fma2(f2_pack(x[c], x[c + 1]), f2_pack(f, f), f2_pack(from, from)));
+              x[c] = f2_lo(y), x[c + 1] = f2_hi(y);
             }
-            if (!masked) return;
+          }
+          if (masked) {
             // a bit for each column that the row sees
             const uint32_t gone = static_cast<uint32_t>(bad >> (CW / 2 * ch));
             const int at = k0 + CW * ch, c0 = min(max(lo - at, 0), 32), c1 = min(max(pos - at, -1), 31) + 1;
@@ -861,72 +873,75 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
 #pragma unroll
             for (int c = 0; c < CW; ++c) x[c] = (see >> c) & 1 ? x[c] : kNegInf;
           }
-        };
-        float mx = kNegInf;
-#pragma unroll 1
-        for (int ch = 0; ch < kTile / CW; ++ch) {
-          float x[CW], m[CW / 8];
-          load(ch, x);
+          uint32_t y[CW];
 #pragma unroll
-          for (int k = 0; k < CW / 8; ++k) m[k] = fmaxf(x[2 * k], x[2 * k + 1]);
-#pragma unroll
-          for (int j = 1; j < 4; ++j)
-#pragma unroll
-            for (int k = 0; k < CW / 8; ++k) m[k] = max3f(m[k], x[CW / 4 * j + 2 * k], x[CW / 4 * j + 2 * k + 1]);
-#pragma unroll
-          for (int k = 0; k < CW / 8; k += 2) mx = max3f(mx, m[k], m[k + 1]);
+          for (int c = 0; c < CW; ++c) y[c] = __float_as_uint(x[c]);
+          tmem_st32(tS + CW * ch, y);
         }
-        mx *= unit;
-        // O keeps its scale unless this tile exceeds it by more than 2^kLazy
-        const float m_new = mx > m_run + kLazy ? mx : m_run;
-        const bool grow = m_new > m_run && m_run != kNegInf && live;
-        if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
-          // (the products of the tile before are complete: S of this one was issued behind them)
-          const float alpha = grow ? ex2_approx(m_run - m_new) : 1.f;
-          l_run *= alpha;
+        tmem_wait_st();
+      }
+      float mx = kNegInf;
 #pragma unroll 1
-          for (int ch = 0; ch < D / 32; ++ch) {
-            uint32_t o[32];
-            tmem_ld32(tO + ch * 32, o);
-            tmem_wait_ld_dep(o);
+      for (int ch = 0; ch < kTile / CW; ++ch) {
+        float x[CW], m[CW / 8];
+        scores(ch, x);
 #pragma unroll
-            for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
-            tmem_st32(tO + ch * 32, o);
-          }
+        for (int k = 0; k < CW / 8; ++k) m[k] = fmaxf(x[2 * k], x[2 * k + 1]);
+#pragma unroll
+        for (int j = 1; j < 4; ++j)
+#pragma unroll
+          for (int k = 0; k < CW / 8; ++k) m[k] = max3f(m[k], x[CW / 4 * j + 2 * k], x[CW / 4 * j + 2 * k + 1]);
+#pragma unroll
+        for (int k = 0; k < CW / 8; k += 2) mx = max3f(mx, m[k], m[k + 1]);
+      }
+      mx *= unit;
+      // O keeps its scale unless this tile exceeds it by more than 2^kLazy
+      const float m_new = mx > m_run + kLazy ? mx : m_run;
+      const bool grow = m_new > m_run && m_run != kNegInf && live;
+      if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
+        // (the products of the tile before are complete: S of this one was issued behind them)
+        const float alpha = grow ? ex2_approx(m_run - m_new) : 1.f;
+        l_run *= alpha;
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t o[32];
+          tmem_ld32(tO + ch * 32, o);
+          tmem_wait_ld_dep(o);
+#pragma unroll
+          for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
+          tmem_st32(tO + ch * 32, o);
         }
-        m_run = m_new;
-        const float nb = m_new == kNegInf ? 0.f : -m_new;
-        const uint64_t u2 = f2_pack(unit, unit), nb2 = f2_pack(nb, nb);
-        uint64_t acc[2] = {0, 0};
+      }
+      m_run = m_new;
+      const float nb = m_new == kNegInf ? 0.f : -m_new;
+      const uint64_t u2 = f2_pack(unit, unit), nb2 = f2_pack(nb, nb);
+      uint64_t acc[2] = {0, 0};
 #pragma unroll 1
-        for (int ch = 0; ch < kTile / CW; ++ch) {
-          float x[CW];
-          load(ch, x);
-          uint32_t pk[CW / 2], rest[Q4 ? CW / 2 : 1] = {};
+      for (int ch = 0; ch < kTile / CW; ++ch) {
+        float x[CW];
+        scores(ch, x);
+        uint32_t pk[CW / 2], rest[Q4 ? CW / 2 : 1] = {};
 #pragma unroll
-          for (int c = 0; c < CW / 2; ++c) {
-            const uint64_t a = fma2(f2_pack(x[2 * c], x[2 * c + 1]), u2, nb2);
-            const uint64_t w = f2_pack(ex2_approx(f2_lo(a)), ex2_approx(f2_hi(a)));
-            acc[c & 1] = add2(acc[c & 1], w);
-            pk[c] = pack_bf16x2(f2_lo(w), f2_hi(w));
-            if constexpr (Q4) {
-              const uint64_t r = add2(w, bf16x2_to_f2(pk[c] ^ 0x80008000u));
-              rest[c] = pack_bf16x2(f2_lo(r), f2_hi(r));
-            }
-          }
-          // over scores that are weighed already
+        for (int c = 0; c < CW / 2; ++c) {
+          const uint64_t a = fma2(f2_pack(x[2 * c], x[2 * c + 1]), u2, nb2);
+          const uint64_t w = f2_pack(ex2_approx(f2_lo(a)), ex2_approx(f2_hi(a)));
+          acc[c & 1] = add2(acc[c & 1], w);
+          pk[c] = pack_bf16x2(f2_lo(w), f2_hi(w));
           if constexpr (Q4) {
-            tmem_st16(tS + CW * ch, pk);
-            tmem_st16(tS + CW * ch + CW / 2, rest);
-          } else {
-            tmem_st16(tS + CW / 2 * ch, pk);
+            const uint64_t r = add2(w, bf16x2_to_f2(pk[c] ^ 0x80008000u));
+            rest[c] = pack_bf16x2(f2_lo(r), f2_hi(r));
           }
         }
-        const uint64_t both = add2(acc[0], acc[1]);
-        l_run += f2_lo(both) + f2_hi(both);
-      };
-      if (p.slopes || masked) tile(std::true_type());
-      else tile(std::false_type());
+        // over scores that are weighed already
+        if constexpr (Q4) {
+          tmem_st16(tS + CW * ch, pk);
+          tmem_st16(tS + CW * ch + CW / 2, rest);
+        } else {
+          tmem_st16(tS + CW / 2 * ch, pk);
+        }
+      }
+      const uint64_t both = add2(acc[0], acc[1]);
+      l_run += f2_lo(both) + f2_hi(both);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -1067,7 +1082,7 @@ __global__ void __launch_bounds__(Cfg<D, Q4, TWO, ROWS_>::THREADS, 1) attend_ker
   for (int b = tid * share; b < min(B, (tid + 1) * share); ++b) {
     const Chunk c = chunk_of(p, b);
     if (blockIdx.x == 0 && c.bad) atomicOr(p.status, kDevPageRange);
-    mine += cost_before(p, c, units_of(p, c)) * p.cache.Hkv;
+    mine += cost_all(p, c) * p.cache.Hkv;
   }
   int64_t total;
   const int64_t before = block_prefix<C::THREADS>(mine, ctl->wsum, &total);
@@ -1080,7 +1095,7 @@ __global__ void __launch_bounds__(Cfg<D, Q4, TWO, ROWS_>::THREADS, 1) attend_ker
 #pragma unroll 1
       for (int b = tid * share;; ++b) {
         const Chunk c = chunk_of(p, b);
-        const int64_t all = cost_before(p, c, units_of(p, c)) * p.cache.Hkv;
+        const int64_t all = cost_all(p, c) * p.cache.Hkv;
         if (y < all) {
           (e ? ctl->end : ctl->begin) = find_in(p, b, c, y);
           break;
@@ -1356,6 +1371,9 @@ cudaError_t launch_paged_attend(const PagedAttendCall& c, int d, int format, cud
   p.ctas = std::min(paged_sm_count(), kPagedMaxCtas);
   p.unit = unit_rows(format, p.N, p.g);
   p.unit_log2 = p.unit == 128 ? 7 : 8;
+  // Measured with 2, 3 and 4 quarters: a batch of chunks and single tokens, d = 128, 0.419, 0.335 and
+  // 0.350 ms; windows of 1024 keys for 24 chunks of up to 300 rows, d = 64, 0.090, 0.099 and 0.109 ms.
+  p.half_cost = d == 64 ? 2 : 3;
   p.div_g = ((1ull << 63) + p.g - 1) / p.g;
   p.bounds = static_cast<Pos*>(c.workspace);
   p.part_acc = reinterpret_cast<float*>(p.bounds + kPagedMaxCtas);
