@@ -460,7 +460,8 @@ attnfuse_status attnfuse_paged_attend(const attnfuse_paged_cache* cache, const v
   if ((rc = check_rope(&mode, rope_theta))) return rc;
   if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
     return fail(ATTNFUSE_ERR_WORKSPACE_TOO_SMALL, "workspace needs %zu bytes (got %zu)", need, workspace_bytes);
-  if ((double)cache->B * Hq * (N + 256.0) * (p.cache.cap + 1024.0) > 0x1p60)
+  // the work of the batch, in 1/g of a key for every 128 rows and more, is counted in 63 bits
+  if ((double)cache->B * Hq * ((double)N * (Hq / cache->Hkv) / 128 + 1.0) * (p.cache.cap + 1024.0) > 0x1p60)
     return fail(ATTNFUSE_ERR_UNSUPPORTED, "B * Hq * N * max_pages * page_size too large");
   if ((rc = current_status_word(&p.status))) return rc;
   p.q = static_cast<const __nv_bfloat16*>(q);

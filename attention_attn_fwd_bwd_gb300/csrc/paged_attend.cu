@@ -28,7 +28,6 @@
 #include <algorithm>
 #include <atomic>
 #include <climits>
-#include <type_traits>
 
 #include "launch.h"
 #include "paged.cuh"
@@ -642,8 +641,11 @@ __device__ __forceinline__ void load_queries(const PagedAttendParams& p, uint8_t
 }
 
 // ---------------------------------------------------------------------------------------------
-// Issuer of the products (one warp, converged, so that descriptors stay in uniform registers: one
-// thread alone took 100 cycles to issue a product of 64)
+// Issuer of the products: a converged warp, of which one thread is elected for a tile's products.
+// Their bases are made the warp's own by a shuffle: values of one thread alone, or an election for
+// each product, take the compiler ten times the instructions to bring to the uniform registers that
+// the products want (one thread took 100 cycles for a product of 64; and instruction fetches bound
+// the 4-bit kernel: 8 tokens over each of 16 contexts 0.176 ms with elections for each, 0.147 so).
 // ---------------------------------------------------------------------------------------------
 template <int D, bool Q4, bool TWO, class C, class T>
 __device__ __forceinline__ void issue(const PagedAttendParams& p, uint8_t* smem, T* ctl, Walk w, uint32_t tmem) {
@@ -664,20 +666,7 @@ __device__ __forceinline__ void issue(const PagedAttendParams& p, uint8_t* smem,
   auto ready = [&](int it) {
     return __all_sync(0xffffffffu, mbar_test(&ctl->kv_full[it % C::STAGES], (it / C::STAGES) & 1)) != 0;
   };
-  // A product, issued by one thread. 4 bits: the thread is elected once for all products of a tile,
-  // and their bases are made the warp's, which takes a tenth of the instructions (instruction fetches
-  // bound that kernel: the calls of 8 tokens over 16 contexts 0.176 and 0.15 ms). bf16: elected for each;
-  // products that come faster hold up the softmax's reads of tensor memory (1024 tokens over 16k keys
-  // 0.238 and 0.245 ms).
-  auto ss = [&](auto acc, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
-    if constexpr (Q4) mma_ss_w<decltype(acc)::value>(d, a, b, dhi, idesc);
-    else mma_ss_warp<decltype(acc)::value>(d, a, b, dhi, idesc);
-  };
-  auto ts = [&](auto acc, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
-    if constexpr (Q4) mma_ts_w<decltype(acc)::value>(d, a, b, dhi, idesc);
-    else mma_ts_warp<decltype(acc)::value>(d, a, b, dhi, idesc);
-  };
-  auto base = [&](uint32_t x) { return Q4 ? __shfl_sync(0xffffffffu, x, 0) : x; };
+  auto base = [&](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
   // S of slot s from row tile `qs`
   auto scores = [&](int s, int qs, int it, bool first, bool last) {
     if (first) {
@@ -687,15 +676,15 @@ __device__ __forceinline__ void issue(const PagedAttendParams& p, uint8_t* smem,
     if (!ok) return;
     tc_fence_after();
     const uint32_t q = base(dQ + qs * (C::QSLOT >> 4)), k = base(dK + (it % C::STAGES) * (C::TILE >> 4)), d = base(tmem + 128 * s);
-    if (!Q4 || elect_one()) {
-      ss(std::integral_constant<int, 0>(), d, q, k, idesc_s);
+    if (elect_one()) {
+      mma_ss_w<0>(d, q, k, dhi, idesc_s);
 #pragma unroll
       for (int kk = 1; kk < (TWO ? 2 : 1) * (D / 16); ++kk) {
         const uint32_t off = ((kk % (D / 16)) >> 2) * (kTile * 128) + (kk & 3) * 32;
-        ss(std::integral_constant<int, 1>(), d, q + (((kk / (D / 16)) * C::TILE + off) >> 4), k + (off >> 4), idesc_s);
+        mma_ss_w<1>(d, q + (((kk / (D / 16)) * C::TILE + off) >> 4), k + (off >> 4), dhi, idesc_s);
       }
     }
-    if (Q4) __syncwarp();
+    __syncwarp();
     mma_commit_warp(&ctl->s_full[s]);
     if (last) mma_commit_warp(&ctl->q_empty[qs]);
   };
@@ -705,19 +694,19 @@ __device__ __forceinline__ void issue(const PagedAttendParams& p, uint8_t* smem,
     if (!ok) return;
     tc_fence_after();
     const uint32_t v = base(dV + (it % C::STAGES) * (C::TILE >> 4)), w = base(tmem + 128 * s), o = w + 256;
-    if (!Q4 || elect_one()) {
-      if (first) ts(std::integral_constant<int, 0>(), o, w, v, idesc_o);
-      else ts(std::integral_constant<int, 1>(), o, w, v, idesc_o);
+    if (elect_one()) {
+      if (first) mma_ts_w<0>(o, w, v, dhi, idesc_o);
+      else mma_ts_w<1>(o, w, v, dhi, idesc_o);
       // 4 bits: of every 32 columns, 16 of weights and 16 of what their rounding left
-      if constexpr (Q4) ts(std::integral_constant<int, 1>(), o, w + 16, v, idesc_o);
+      if constexpr (Q4) mma_ts_w<1>(o, w + 16, v, dhi, idesc_o);
 #pragma unroll
       for (int kk = 1; kk < 8; ++kk) {
         const uint32_t at = w + (Q4 ? kk / 2 * 32 + kk % 2 * 8 : kk * 8);
-        ts(std::integral_constant<int, 1>(), o, at, v + kk * (2048 >> 4), idesc_o);
-        if constexpr (Q4) ts(std::integral_constant<int, 1>(), o, at + 16, v + kk * (2048 >> 4), idesc_o);
+        mma_ts_w<1>(o, at, v + kk * (2048 >> 4), dhi, idesc_o);
+        if constexpr (Q4) mma_ts_w<1>(o, at + 16, v + kk * (2048 >> 4), dhi, idesc_o);
       }
     }
-    if (Q4) __syncwarp();
+    __syncwarp();
     if (last) mma_commit_warp(&ctl->o_full[s]);
   };
   // the next segment's tiles and kind (as votes, so that branches on them are known to be the warp's)

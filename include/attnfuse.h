@@ -409,17 +409,21 @@ attnfuse_status attnfuse_paged_decode(const attnfuse_paged_cache* cache, const v
  * at position p = start[b] + n (append the chunk's K and V first), against positions m <= p, with
  * window > 0 only m > p - window:
  *   s_m = scale <R_p q, k_m> [+ alibi_slopes[h] (m - p)],  lse = ln sum exp s_m,  out = sum exp(s_m - lse) v_m
- * out [B, Hq, N, d] bf16, lse [B, Hq, N] fp32 contiguous or NULL. Rows at and behind count[b] (padding) are not
- * read; their out is 0 and their lse -inf. count NULL: all N. It continues prompts, verifies drafted
- * tokens and serves batches that mix prompts with single tokens; one token (N = 1) gives what
- * attnfuse_paged_decode with lens = start + 1 does, at coarser weights. rope_mode NONE or FUSED (AUTO means
- * FUSED): q is rotated at its position and keeps 16 significant bits against a BF16 cache, 22 against a Q4 one.
- * Weights are rounded to bf16, and so are the values of a Q4 cache (its keys are not). A value that
- * is not finite at a visible position may give NaN in all rows of its sequence and KV head, also in those that do
- * not see it; positions behind start[b] + count[b] - 1, and before the first that some row sees, are not read.
- * A bad page in a visible place is skipped (status word, above). Hq: a multiple of Hkv up to 4096.
- * Results do not vary from run to run. workspace: attnfuse_paged_attend_workspace_size bytes on the current device,
- * 16-byte aligned. Calls that may overlap need workspaces of their own. */
+ * out [B, Hq, N, d] bf16 (strides as q), lse [B, Hq, N] fp32 contiguous or NULL; alibi_slopes [Hq] fp32 or
+ * NULL. Rows at and behind count[b] (padding) are not read; their out is 0 and their lse -inf. count
+ * NULL: all N. A row whose position lies outside the table counts as padding (status word, above), all rows do where
+ * start[b] < 0. It continues prompts, verifies drafted tokens and serves batches that mix prompts
+ * with single tokens; N = 1 is attnfuse_paged_decode with lens = start + 1, at coarser weights.
+ * rope_mode NONE or FUSED (AUTO means FUSED): q is rotated at its position and keeps 16 significant bits
+ * against a BF16 cache, 22 against a Q4 one (as does a q that is not rotated, of its 8). Weights are rounded
+ * to bf16 against a BF16 cache; against a Q4 one they keep 16 bits, and its values are rounded to bf16. Q4
+ * keys are exact down to steps of 2^-28 of the largest among 128 keys (from a multiple of 128 on) and off by up to 2^-36
+ * of it below. Infinities and NaN: a row that sees one may give NaN, and so may the chunk's earlier rows of the same KV head,
+ * since 128 or 256 rows share the keys that any of them sees; positions behind start[b] + count[b] - 1 and before
+ * the first that some row sees have no effect, whatever they hold. With a Q4 cache |q| >= 2^100 or keys of 2^90 may give NaN.
+ * Hq: a multiple of Hkv up to 4096, N * Hq / Hkv up to 2^30. Results do not vary from run to run. workspace:
+ * attnfuse_paged_attend_workspace_size bytes on the current device, 16-byte aligned (partial rows for each SM, and where q is rotated or
+ * the cache is Q4 one or two 16-bit copies of q). Calls that may overlap need workspaces of their own. */
 attnfuse_status attnfuse_paged_attend_workspace_size(int B, int Hq, int Hkv, int N, int d, int format,
                                                      attnfuse_rope_mode rope_mode, size_t* bytes);
 

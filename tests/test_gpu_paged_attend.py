@@ -358,6 +358,51 @@ def test_rotation_append_attention_and_decode_together(q4):
     K.check(got, K.attend(rq, cache, [0] * B, [total] * B, d ** -0.5))
 
 
+@pytest.mark.parametrize("seed", range(40))
+def test_random_calls(seed):
+    """Sizes, groups, pages, windows, bias and rotation of any mix."""
+    r = random.Random(1000 + seed)
+    d, q4 = r.choice([64, 128]), r.random() < 0.5
+    Hkv, g = r.choice([1, 2, 3, 5]), r.choice([1, 2, 3, 4, 5, 8, 11, 16, 33])
+    B, N, page = r.randint(1, 9), r.choice([1, 2, 7, 40, 129, 260, 400]), r.choice([16, 32, 48, 64, 112, 128, 256, 400])
+    start = [r.choice([0, r.randint(0, 200), r.randint(0, 1500)]) for _ in range(B)]
+    count = [r.choice([0, 1, N, r.randint(0, N)]) for _ in range(B)]
+    cache = make_cache([max(1, s + n) for s, n in zip(start, count)], Hkv, page, d, q4, seed=seed)
+    check(randn(B, Hkv * g, N, d, seed=seed), cache, start, count, r.choice([None, 1e4]),
+          window=r.choice([0, 0, 1, r.randint(2, 400)]), slopes=slopes_of(Hkv * g) if r.random() < 0.3 else None)
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_the_largest_group(q4):
+    cache = make_cache([40, 200], 1, 16, 64, q4, seed=60)
+    check(randn(2, 4096, 2, 64, seed=61), cache, [38, 198], [2, 1], 1e4)
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_many_short_sequences(q4):
+    """More of them than threads and CTAs, most without new tokens."""
+    r = random.Random(62)
+    B = 1500
+    start = [r.randint(0, 60) for _ in range(B)]
+    count = [r.choice([0, 0, 0, 1, 2, 3]) for _ in range(B)]
+    cache = make_cache([max(1, s + n) for s, n in zip(start, count)], 1, 16, 64, q4, seed=63)
+    check(randn(B, 2, 3, 64, seed=64), cache, start, count, 1e4)
+    check(randn(B, 2, 3, 64, seed=65), cache, start, [0] * B, 1e4)
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_a_key_of_large_values_that_others_see_last(q4):
+    """A chunk's last key and value are 2^20 times the others: rows before it keep their bits."""
+    N = 50
+    cache = make_cache([300 + N], 2, 16, 128, q4, seed=66, garbage=False)
+    q = randn(1, 8, N, 128, seed=67)
+    k, v = randn(1, 2, 1, 128, seed=68) * 2.0 ** 20, randn(1, 2, 1, 128, seed=69) * 2.0 ** 20
+    af.paged_append(cache, k, v, i32([300 + N - 1]), rope_mode=af.ROPE_NONE)
+    out, lse = run(q, cache, [300], None)
+    ref = K.attend(q, cache, [300], [N], 128 ** -0.5)
+    K.check((out[:, :, :-1].contiguous(), lse[:, :, :-1].contiguous()), [x[:, :, :-1] for x in ref])
+
+
 @pytest.mark.parametrize("q4", [False, True])
 def test_shared_pages(q4):
     """Sequences that share a prompt's pages."""
