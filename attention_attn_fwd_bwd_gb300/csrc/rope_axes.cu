@@ -4,7 +4,9 @@
 //   y_i = x_i cos a - x_{i + d/2} sin a,  y_{i + d/2} = x_{i + d/2} cos a + x_i sin a,
 //   a = pos[axis(i)][b][n] f_i  (negative for the inverse)
 //
-// Each element is read once and written once, and HBM bounds it. A block takes a few rows (tokens)
+// Each element is read once and written once, and HBM bounds it (2 x 8000 tokens of 40 heads, d = 128:
+// 61 us, 79% of a copy's rate; 24 x 1025 of 32 heads, d = 64: 39 us, 76%; blocks of 64 or 256 threads, 8 rows,
+// or two heads in flight: within 5%). A block takes a few rows (tokens)
 // and a run of their heads, of q and k alike: the angles of its rows are computed once, finer than
 // fp32 as in the paged append (some 60 instructions each), into shared memory, and serve all of
 // the block's heads.
