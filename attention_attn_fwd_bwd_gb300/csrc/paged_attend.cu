@@ -454,69 +454,59 @@ __device__ __forceinline__ void produce4(const PagedAttendParams& p, uint8_t* sm
   for (int i = max(0, it - C::RAWS); i < it; ++i) mbar_wait(&ctl->raw_full[i % C::RAWS], (i / C::RAWS) & 1, p.status, nullptr);
 }
 
-// Eight elements of each of two groups, from a word of four codes of both for the first four and one
-// for the last: fp16 (F16) or bf16 pairs, times the groups' steps (a pair). Codes of the two groups are
-// handled in pairs, as they lie, and sorted at the end.
+// Order of a head's elements in these tiles: of every 64, elements e and 32 + e (e < 32), of two groups,
+// lie side by side, as a register of codes has them; sorting them took a fifth of the instructions. The
+// query pass writes the same order, and the way out undoes it for the values.
+
+// Four elements of each of two groups, from a word of their codes (the first group's in the low half):
+// fp16 (F16) or bf16 pairs, times the groups' steps (a pair).
 template <bool F16>
-__device__ __forceinline__ void expand8(uint32_t first, uint32_t last, uint32_t step2, uint4& g0, uint4& g1) {
-  uint32_t y[2][4];
+__device__ __forceinline__ uint4 expand8(uint32_t w, uint32_t step2) {
+  uint32_t y[4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t w = i ? last : first;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      uint32_t c;
-      if constexpr (F16) {
-        // 1024 + n, or 1024 + 16 n times 1/16, less what makes it n - 8: all exact
-        const uint32_t u = e < 2 ? w : w >> 8;
-        if (e & 1) {
-          const uint32_t x = (u & 0x00F000F0u) | 0x64006400u;
-          asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(c) : "r"(x), "r"(0x2C002C00u), "r"(0xD480D480u));
-        } else {
-          const uint32_t x = (u & 0x000F000Fu) | 0x64006400u;
-          asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(c) : "r"(x), "r"(0x64086408u));
-        }
-        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[i][e]) : "r"(c), "r"(step2));
+  for (int e = 0; e < 4; ++e) {
+    uint32_t c;
+    if constexpr (F16) {
+      // 1024 + n, or 1024 + 16 n times 1/16, less what makes it n - 8: all exact
+      const uint32_t u = e < 2 ? w : w >> 8;
+      if (e & 1) {
+        const uint32_t x = (u & 0x00F000F0u) | 0x64006400u;
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(c) : "r"(x), "r"(0x2C002C00u), "r"(0xD480D480u));
       } else {
-        const uint32_t x = ((w >> (4 * e)) & 0x000F000Fu) | 0x43004300u;  // 128 + n
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(x), "r"(0x43084308u));
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y[i][e]) : "r"(c), "r"(step2));
+        const uint32_t x = (u & 0x000F000Fu) | 0x64006400u;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(c) : "r"(x), "r"(0x64086408u));
       }
+      asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[e]) : "r"(c), "r"(step2));
+    } else {
+      const uint32_t x = ((w >> (4 * e)) & 0x000F000Fu) | 0x43004300u;  // 128 + n
+      asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(x), "r"(0x43084308u));
+      asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y[e]) : "r"(c), "r"(step2));
     }
   }
-  g0 = make_uint4(__byte_perm(y[0][0], y[0][1], 0x5410), __byte_perm(y[0][2], y[0][3], 0x5410),
-                  __byte_perm(y[1][0], y[1][1], 0x5410), __byte_perm(y[1][2], y[1][3], 0x5410));
-  g1 = make_uint4(__byte_perm(y[0][0], y[0][1], 0x7632), __byte_perm(y[0][2], y[0][3], 0x7632),
-                  __byte_perm(y[1][0], y[1][1], 0x7632), __byte_perm(y[1][2], y[1][3], 0x7632));
+  return make_uint4(y[0], y[1], y[2], y[3]);
 }
 
 // Expands row `row` of a copied tile into a tile of the ring (128-byte swizzle, panels of 64
-// elements). Rows take their 16-byte pieces in different orders, so that neither the loads nor
-// the stores of eight rows meet in a bank.
+// elements). With d = 128 rows take their 16-byte pieces in different orders, so that neither the
+// loads nor the stores of eight rows meet in a bank (d = 64: the two loads do, in pairs).
 template <int D, bool F16>
 __device__ __forceinline__ void expand_row(const uint8_t* raw, const uint32_t (&step2)[D / 64], uint8_t* tile, int row) {
-  const int turn = D == 128 ? (row & 2) | ((row >> 2) & 1) : (row >> 2) & 1;
+  const int turn = D == 128 ? (row & 2) | ((row >> 2) & 1) : 0;
 #pragma unroll 1
   for (int j = 0; j < D / 32; ++j) {
     const int at = j ^ turn;
     const uint4 c = *reinterpret_cast<const uint4*>(raw + row * (D / 2) + at * 16);
-    uint4 g0, g1;
-    auto put = [&](int chunk, const uint4& x) {
-      *reinterpret_cast<uint4*>(tile + (chunk >> 3) * (kTile * 128) + sw128_offset(row, chunk & 7)) = x;
+    auto put = [&](int panel, int chunk, uint32_t w) {
+      *reinterpret_cast<uint4*>(tile + panel * (kTile * 128) + sw128_offset(row, chunk)) = expand8<F16>(w, step2[panel]);
     };
     if constexpr (D == 128) {
       // two chunks of four groups; slots (as rows: pages are multiples of 16) with bit 1 have their halves swapped
       const int m = at ^ (row & 2);
-      expand8<F16>(c.x, c.z, step2[0], g0, g1);
-      put(m, g0), put(4 + m, g1);
-      expand8<F16>(c.y, c.w, step2[1], g0, g1);
-      put(8 + m, g0), put(12 + m, g1);
+      put(0, 2 * m, c.x), put(0, 2 * m + 1, c.z);
+      put(1, 2 * m, c.y), put(1, 2 * m + 1, c.w);
     } else {
       // four chunks of two groups
-      expand8<F16>(c.x, c.y, step2[0], g0, g1);
-      put(2 * at, g0), put(4 + 2 * at, g1);
-      expand8<F16>(c.z, c.w, step2[0], g0, g1);
-      put(2 * at + 1, g0), put(5 + 2 * at, g1);
+      put(0, 4 * at, c.x), put(0, 4 * at + 1, c.y), put(0, 4 * at + 2, c.z), put(0, 4 * at + 3, c.w);
     }
   }
 }
@@ -972,8 +962,9 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
       l_run = w0 * l_run + w1 * ml.y;
       m_run = m;
     }
-    // columns 32 ch .. of the row's accumulator
-    auto result = [&](int ch, uint32_t (&o)[32]) {
+    // Columns 32 ch .. of the row's accumulator: two runs of 16 elements, the k-th from place_of(ch, k) on.
+    auto result = [&](int ch, uint32_t (&y)[32]) {
+      uint32_t o[32];
       tmem_ld32(tO + ch * 32, o);
       tmem_wait_ld_dep(o);
       if (split) {
@@ -984,7 +975,10 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
         for (int q = 0; q < 32; ++q)
           o[q] = __float_as_uint(__fmaf_rn(__uint_as_float(o1[q]), w1, __uint_as_float(o[q]) * w0));
       }
+#pragma unroll
+      for (int q = 0; q < 32; ++q) y[q] = o[Q4 ? 2 * (q % 16) + q / 16 : q];
     };
+    auto place_of = [](int ch, int k) { return Q4 ? 64 * (ch >> 1) + 32 * k + 16 * (ch & 1) : 32 * ch + 16 * k; };
     const bool any = !(l_run == 0.f);  // a NaN goes to the output
     if (s.part < 0) {
       const float inv = any ? 1.f / l_run : 0.f;
@@ -994,16 +988,16 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
         uint32_t o[32];
         result(ch, o);
         if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(out + ch * 32);
 #pragma unroll
           for (int v4 = 0; v4 < 4; ++v4) {
+            uint4* dst = reinterpret_cast<uint4*>(out + place_of(ch, v4 / 2) + v4 % 2 * 8);
             uint32_t y[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int q = v4 * 8 + 2 * e;
               y[e] = any ? pack_bf16x2(__uint_as_float(o[q]) * inv, __uint_as_float(o[q + 1]) * inv) : 0u;
             }
-            __stcs(dst + v4, make_uint4(y[0], y[1], y[2], y[3]));
+            __stcs(dst, make_uint4(y[0], y[1], y[2], y[3]));
           }
         }
       }
@@ -1016,9 +1010,10 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
         uint32_t o[32];
         result(ch, o);
         if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(p.part_acc + at * D + ch * 32);
 #pragma unroll
-          for (int v4 = 0; v4 < 8; ++v4) dst[v4] = make_uint4(o[4 * v4], o[4 * v4 + 1], o[4 * v4 + 2], o[4 * v4 + 3]);
+          for (int v4 = 0; v4 < 8; ++v4)
+            *reinterpret_cast<uint4*>(p.part_acc + at * D + place_of(ch, v4 / 4) + v4 % 4 * 4) =
+                make_uint4(o[4 * v4], o[4 * v4 + 1], o[4 * v4 + 2], o[4 * v4 + 3]);
         }
       }
       if (live) p.part_ml[at] = make_float2(m_run, l_run);
@@ -1276,6 +1271,30 @@ __global__ void __launch_bounds__(kQueryThreads) attend_query_kernel(const __gri
 #pragma unroll
       for (int q = 0; q < 16; ++q) x[q] *= up;
     }
+    // 4 bits: of every 64 elements, e and 32 + e side by side. With d = 128 the thread four further on
+    // has the partners: the first keeps the first four of each eight.
+    int at = t * 8, next = D / 2;  // where the first eight values go, and how far on the others
+    if constexpr (Q4) {
+      float y[16];
+      if constexpr (D == 128) {
+        const bool up = t & 4;
+#pragma unroll
+        for (int q = 0; q < 16; q += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float other = __shfl_xor_sync(0xffffffffu, up ? x[q + e] : x[q + 4 + e], 4);
+            y[q + 2 * e] = up ? other : x[q + e];
+            y[q + 2 * e + 1] = up ? x[q + 4 + e] : other;
+          }
+        at = 16 * (t & 3) + (up ? 8 : 0);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[2 * e] = x[e], y[2 * e + 1] = x[8 + e];
+        at = 16 * t, next = 8;
+      }
+#pragma unroll
+      for (int q = 0; q < 16; ++q) x[q] = y[q];
+    }
     if (!on) continue;
     const int64_t to = (static_cast<int64_t>(b) * p.Hq + h) * p.N + n;
     if (Q4 && t == 0) p.factor[to] = f;
@@ -1294,13 +1313,13 @@ __global__ void __launch_bounds__(kQueryThreads) attend_query_kernel(const __gri
         lo[w] = pack_bf16x2(a - bf16lo_to_f32(hi[w]), c - bf16hi_to_f32(hi[w]));
       }
     }
-    uint4* dst = reinterpret_cast<uint4*>(p.hi + to * D + t * 8);
-    dst[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    dst[D / 16] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+    uint16_t* dst = p.hi + to * D + at;
+    *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(dst + next) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
     if (ROPE) {
-      dst = reinterpret_cast<uint4*>(p.lo + to * D + t * 8);
-      dst[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      dst[D / 16] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+      dst = p.lo + to * D + at;
+      *reinterpret_cast<uint4*>(dst) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      *reinterpret_cast<uint4*>(dst + next) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
     }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
