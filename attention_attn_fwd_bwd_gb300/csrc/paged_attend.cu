@@ -20,10 +20,10 @@
 // TMEM (512 columns): S_0 [0, 128), S_1 [128, 256), O_0 [256, 384), O_1 [384, 512); P_s over S_s.
 //
 // What bounds it. bf16: the chain of scores, softmax and values of a row tile beside the other's
-// (4096 tokens over 28672 keys, Hq 32 / Hkv 8, d 128: 1.51 ms, 1369 TFLOP/s, 71% of a library product's rate; with a
-// rotated q, whose scores take twice the products, 1024 tokens over 15360 keys take 0.286 instead of
-// 0.233 ms). 4 bits: the expansion and, with queries and weights in two parts, twice the products (the
-// same tokens: 0.41 ms, tensor pipe 58%, integer pipe 45%).
+// (4096 tokens over 28672 keys, Hq 32 / Hkv 8, d 128: 1.53 ms, 1349 TFLOP/s, 70% of a library product's rate; with a
+// rotated q, whose scores take twice the products, 1024 tokens over 15360 keys take 0.285 instead of
+// 0.228 ms). 4 bits: the expansion and, with queries and weights in two parts, twice the products (the
+// same tokens: 0.396 ms; before the elements' order changed, 0.414 ms, tensor pipe 58%, integer pipe 45%).
 //
 // Keys of a 4-bit cache are s_g c (8 and 3 bits): exact in fp16 under a power of two of the tile's
 // largest step, for steps down to 2^-28 of it (and off by at most 2^-36 of it below); q enters as fp16
@@ -45,7 +45,10 @@ namespace afx {
 namespace {
 
 constexpr int kTile = kAttendTile;       // keys of a tile
-constexpr int kEnds = 256;               // keys that a unit's two ends cost: Q's load, O's way out
+// Keys that a unit's two ends cost: Q's load, O's way out. With 128, 256 and 384: 4 x 2048 tokens over up to
+// 6144 keys 0.579, 0.555, 0.551 ms; windows of 1024 keys, d = 64, 0.088, 0.090, 0.094; 1024 tokens of 4
+// sequences over a 4-bit cache 0.413, 0.396, 0.400.
+constexpr int kEnds = 256;
 constexpr float kLazy = 8.0f;            // the running maximum may lag by 2^8
 
 template <int D, bool Q4, bool TWO, int ROWS_>

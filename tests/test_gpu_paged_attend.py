@@ -373,6 +373,17 @@ def test_random_calls(seed):
 
 
 @pytest.mark.parametrize("q4", [False, True])
+@pytest.mark.parametrize("window", [1, 100, 1000])
+def test_positions_up_to_the_last(q4, window):
+    """A table of 2^24 positions over a few pages that it names again and again."""
+    N, page, end = 40, 256, 1 << 24
+    small = make_cache([4 * page], 2, page, 64, q4, seed=70, garbage=False)
+    table = (torch.arange(end // page, device=DEV, dtype=torch.int32) % 4)[None].contiguous()
+    cache = af.PagedCache(small.k, small.v, table, small.k_scales, small.v_scales)
+    check(randn(1, 4, N, 64, seed=71), cache, [end - N], None, 5e5, window=window)
+
+
+@pytest.mark.parametrize("q4", [False, True])
 def test_the_largest_group(q4):
     cache = make_cache([40, 200], 1, 16, 64, q4, seed=60)
     check(randn(2, 4096, 2, 64, seed=61), cache, [38, 198], [2, 1], 1e4)
