@@ -827,7 +827,10 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
       float part = 1.f;  // of the scores: a power of two
       if constexpr (Q4) part = *reinterpret_cast<volatile float*>(&ctl->factor[(tiles + i) % C::NOTES]);
       const int k0 = (s.t + i) * kTile;
-      const float unit = p.slopes ? 1.f : mul * part;
+      // 4 bits: not 0, which times a masked column's -inf would be NaN (a row of zeros has a factor of
+      // 2^-100, a tile of zeros one of 2^-126). Scores as they come are below 2^15 * 2^15 * 128 = 2^37, so
+      // that at 2^-126 they move no weight. (bf16: the scale alone, which may be below 2^-126 in earnest.)
+      const float unit = p.slopes ? 1.f : Q4 ? fmaxf(mul * part, 0x1p-126f) : mul;
       const bool masked = __any_sync(0xffffffffu, k0 + kTile - 1 > pos || k0 < lo || bad != 0);
       // Passes over the tile read its scores from tensor memory, CW columns at a time, in loops: all 128
       // at once, unrolled, take registers and instruction cache that the warps of five roles do not have.
