@@ -58,7 +58,10 @@ def rope(theta=10000.0, mode="auto"):
 
 def rope_axes(positions, sections, theta=10000.0, interleaved=False, own_spectrum=False):
     """Rotary position embedding of q and k by given positions on one to four axes (af.rope_axes):
-    positions int32 [axes, B, N] or [axes, N] device tensor, sections: pairs of each axis."""
+    positions int32 [axes, B, N] or [axes, N] device tensor, sections: pairs of each axis. The
+    rotated q and k are bf16 (those of the rope stage fp16 within the forward), and dq and dk are
+    rounded to bf16 twice, by the backward and once turned back (those of the rope stage once):
+    rows in fp32 between the two passes would double what both move."""
     return Combinator("rope_axes", positions=positions, sections=tuple(sections), theta=float(theta),
                       interleaved=bool(interleaved), own_spectrum=bool(own_spectrum))
 

@@ -462,7 +462,8 @@ attnfuse_status attnfuse_rope_prerotate(const void* x, const int64_t x_strides[4
  * is (R x), off by at most 2^-34 (|x_i| + |x_{i + d/2}|) for positions up to 2^24 (2^-30 beyond), rounded
  * to fp32 and then to bf16. With one axis and positions start + n these are the keys that
  * attnfuse_paged_append stores. Rows to attend over with ATTNFUSE_ROPE_NONE: attnfuse_fwd, attnfuse_bwd
- * (then turn dq and dk back), attnfuse_paged_append and what reads the cache.
+ * (then turn dq and dk back: they are rounded to bf16 by the backward and again here, where the
+ * backward's own inverse rotation rounds once), attnfuse_paged_append and what reads the cache.
  * ------------------------------------------------------------------------------------------ */
 typedef struct {
   int32_t axes;                /* 1 to 4 */
