@@ -1393,9 +1393,20 @@ cudaError_t launch_paged_attend(const PagedAttendCall& c, int d, int format, cud
   p.ctas = std::min(paged_sm_count(), kPagedMaxCtas);
   p.unit = unit_rows(format, p.N, p.g);
   p.unit_log2 = p.unit == 128 ? 7 : 8;
-  // Measured with 2, 3 and 4 quarters: a batch of chunks and single tokens, d = 128, 0.419, 0.335 and
-  // 0.350 ms; windows of 1024 keys for 24 chunks of up to 300 rows, d = 64, 0.090, 0.099 and 0.109 ms.
-  p.half_cost = d == 64 ? 2 : 3;
+  // Half of a unit's rows have half of its products and weights, but all of its keys: more than half of the
+  // time where few tiles of them fit into shared memory, q in two parts and d = 128 (bf16: 3; 4 bits: one of K,
+  // one of V). With 4 bits and d = 64 or windows either way is better in some cases. Measured with 2, 3 and 4 quarters, us, Hkv 8, Hq 32; 24 chunks of up to 300 tokens over up to 6001 keys, and 32
+  // of one or up to 512 over up to 4096:
+  //   d 128, two parts: bf16 295, 267, 260 and 413, 328, 333; windows of 1024 keys 136, 131, 128 and 245, 218, 220;
+  //     4 bits 339, 326, 342 and 451, 409, 422; with windows 158, 161, 159 and 275, 277, 279
+  //   d 128, one part: bf16 195, 200, 212 and 256, 263, 275; with windows 101, 103, 101 and 167, 169, 171;
+  //     4 bits 297, 294, 304 and 377, 377, 391; with windows 148, 149, 146 and 256, 256, 255
+  //   d 64, one part: bf16 152, 157, 168 and 193, 198, 209; with windows 75, 77, 78 and 129, 131, 134;
+  //     4 bits 271, 256, 268 and 325, 313, 339; with windows 122, 127, 123 and 219, 214, 220
+  //   d 64, two parts: bf16 171, 175, 186 and 220, 225, 237; with windows 89, 91, 91 and 155, 156, 158;
+  //     4 bits 266, 260, 270 and 328, 323, 336; with windows 124, 127, 125 and 222, 220, 221
+  // (Groups of one, Hkv 16: the same, but that 4 bits with d = 64 take 190, 193, 221.)
+  p.half_cost = two && d == 128 ? 3 : 2;
   p.div_g = ((1ull << 63) + p.g - 1) / p.g;
   p.bounds = static_cast<Pos*>(c.workspace);
   p.part_acc = reinterpret_cast<float*>(p.bounds + kPagedMaxCtas);
