@@ -20,10 +20,10 @@
 // TMEM (512 columns): S_0 [0, 128), S_1 [128, 256), O_0 [256, 384), O_1 [384, 512); P_s over S_s.
 //
 // What bounds it. bf16: the chain of scores, softmax and values of a row tile beside the other's
-// (4096 tokens over 28672 keys, Hq 32 / Hkv 8, d 128: 1.53 ms, 1349 TFLOP/s, 70% of a library product's rate; with a
+// (4096 tokens over 28672 keys, Hq 32 / Hkv 8, d 128: 1.54 ms, 1339 TFLOP/s, 70% of a library product's rate; with a
 // rotated q, whose scores take twice the products, 1024 tokens over 15360 keys take 0.285 instead of
 // 0.228 ms). 4 bits: the expansion and, with queries and weights in two parts, twice the products (the
-// same tokens: 0.396 ms; before the elements' order changed, 0.414 ms, tensor pipe 58%, integer pipe 45%).
+// same tokens: 0.396 ms, tensor pipe 61%, integer pipe 43%).
 //
 // Keys of a 4-bit cache are s_g c (8 and 3 bits): exact in fp16 under a power of two of the tile's
 // largest step, for steps down to 2^-28 of it (and off by at most 2^-36 of it below); q enters as fp16
@@ -45,9 +45,9 @@ namespace afx {
 namespace {
 
 constexpr int kTile = kAttendTile;       // keys of a tile
-// Keys that a unit's two ends cost: Q's load, O's way out. With 128, 256 and 384: 4 x 2048 tokens over up to
-// 6144 keys 0.579, 0.555, 0.551 ms; windows of 1024 keys, d = 64, 0.088, 0.090, 0.094; 1024 tokens of 4
-// sequences over a 4-bit cache 0.413, 0.396, 0.400.
+// Keys that a unit's two ends cost: Q's load, O's way out. A compromise: with 128, 256 and 384, 4 x 2048 tokens
+// over up to 6144 keys take 536, 524, 519 us; windows of 1024 keys with ALiBi, d = 64, 74, 78, 80; a batch of
+// chunks and single tokens 357, 327, 327; over 4-bit caches 4 x 1024 tokens 382, 365, 369, 16 x 8 tokens 155, 136, 136.
 constexpr int kEnds = 256;
 constexpr float kLazy = 8.0f;            // the running maximum may lag by 2^8
 
@@ -55,9 +55,9 @@ template <int D, bool Q4, bool TWO, int ROWS_>
 struct Cfg {
   static constexpr int WARPS = Q4 ? 20 : 12;
   static constexpr int THREADS = 32 * WARPS;
-  static constexpr int PANELS = D / 64;
+  static constexpr int PANELS = D / 64;                            // of 64 elements, 128 bytes a row
   static constexpr int ROWS = ROWS_;                               // of a unit: one row tile or two
-  static constexpr uint32_t TILE = kTile * D * 2;                  // bytes of a K, V or Q tile
+  static constexpr uint32_t TILE = kTile * 128 * PANELS;           // bytes of a K, V or Q tile
   static constexpr uint32_t QSLOT = TILE * (TWO ? 2 : 1);
   static constexpr int STAGES = D == 64 ? 6 : Q4 ? (ROWS == 256 && TWO ? 2 : 4) : TWO ? 3 : 5;
   // (K and V are expanded independently: each has stages of its own)
@@ -646,7 +646,8 @@ __device__ __forceinline__ void load_queries(const PagedAttendParams& p, uint8_t
 // Their bases are made the warp's own by a shuffle: values of one thread alone, or an election for
 // each product, take the compiler ten times the instructions to bring to the uniform registers that
 // the products want (one thread took 100 cycles for a product of 64; and instruction fetches bound
-// the 4-bit kernel: 8 tokens over each of 16 contexts 0.176 ms with elections for each, 0.147 so).
+// the 4-bit kernel: 8 tokens over each of 16 contexts 0.176 ms with elections for each, 0.147 so; later
+// steps brought that to 0.137).
 // ---------------------------------------------------------------------------------------------
 template <int D, bool Q4, bool TWO, class C, class T>
 __device__ __forceinline__ void issue(const PagedAttendParams& p, uint8_t* smem, T* ctl, Walk w, uint32_t tmem) {
@@ -791,8 +792,7 @@ __device__ __forceinline__ void softmax(const PagedAttendParams& p, T* ctl, Walk
   const int lane = threadIdx.x % 32, quarter = (threadIdx.x / 32) % 4, r = quarter * 32 + lane;
   volatile int* abort_flag = &ctl->abort_flag;
   int* status = p.status;
-  const uint32_t tS = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 128 * slot;
-  const uint32_t tO = tS - 128 * slot + 256 + 128 * slot;
+  const uint32_t tS = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 128 * slot, tO = tS + 256;
   int sc = 0, oc = 0, jc = 0, tiles = 0;
   bool ok = true;
   const Seg* seg;
@@ -1395,8 +1395,9 @@ cudaError_t launch_paged_attend(const PagedAttendCall& c, int d, int format, cud
   p.unit_log2 = p.unit == 128 ? 7 : 8;
   // Half of a unit's rows have half of its products and weights, but all of its keys: more than half of the
   // time where few tiles of them fit into shared memory, q in two parts and d = 128 (bf16: 3; 4 bits: one of K,
-  // one of V). With 4 bits and d = 64 or windows either way is better in some cases. Measured with 2, 3 and 4 quarters, us, Hkv 8, Hq 32; 24 chunks of up to 300 tokens over up to 6001 keys, and 32
-  // of one or up to 512 over up to 4096:
+  // one of V). With 4 bits and d = 64 or windows either way is better in some cases. Measured with 2, 3 and 4
+  // quarters, us, Hq 32, Hkv 8: 24 chunks of up to 300 tokens over up to 6001 keys, and 32 of one or up to 512
+  // tokens over up to 4096.
   //   d 128, two parts: bf16 295, 267, 260 and 413, 328, 333; windows of 1024 keys 136, 131, 128 and 245, 218, 220;
   //     4 bits 339, 326, 342 and 451, 409, 422; with windows 158, 161, 159 and 275, 277, 279
   //   d 128, one part: bf16 195, 200, 212 and 256, 263, 275; with windows 101, 103, 101 and 167, 169, 171;
