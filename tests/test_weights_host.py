@@ -1,4 +1,4 @@
-"""The cases that judge the weights' rounding beside a 4-bit cache, without a GPU: they tell weights in two
+"""The cases that show the weights' rounding beside a 4-bit cache, without a GPU: they tell weights in two
 bf16 parts from weights in one."""
 import pytest
 import torch
