@@ -886,7 +886,8 @@ def paged_attend(q, cache, start, count=None, scale=None, rope_theta=10000.0, ro
     None: all N), against positions up to its own (window > 0: the last `window` of them) -> (out
     [B, Hq, N, d], lse [B, Hq, N]). Rows at and behind count[b]: out 0, lse -inf. alibi_slopes: fp32 [Hq], adds
     slope_h (m - p) to the scores. Weights keep 8 bits against a bf16 cache (paged_decode: 16), so that a token's
-    row here and there may differ by up to 2^-8 of sum p|v|, and by both roundings to bf16. With a stream, what the call allocates belongs to that stream."""
+    row here and there may differ by up to 2^-8 of sum p|v|, and by both roundings to bf16. With a
+    stream, what the call allocates belongs to that stream."""
     import torch
 
     if not isinstance(cache, PagedCache):
